@@ -67,8 +67,8 @@ def draw(rng):
         B = _log_int(rng, 1, 16)
         L = _log_int(rng, 1, 16384)
         cost = H * L * D * (1 if packed else B) * (1 if dtype == "bf16" else 2)
-        if cost > 1 << 24:
-            L = max(1, L * (1 << 24) // cost)
+        if cost > 16_000_000:
+            L = max(1, L * 16_000_000 // cost)
         return dict(op=op, B=B, H=H, L=L, D=D, dtype=dtype, gate=rng.choice(["channel", "preact"]),
                     write=rng.choice(["input", "leak"]), packed=packed, z_mean=rng.choice([0.0, 2.0]))
     if op == "step":
