@@ -79,8 +79,10 @@ def draw(rng):
     B = _log_int(rng, 1, 64)
     K = rng.choice([16, 64, 96, 128, 256, rng.randint(8, 256)])
     V = rng.choice([64, 128, 256, 512, 16 * rng.randint(1, 32), rng.randint(8, 512)])
+    H = rng.choice([1, 2, 4, 8])
+    B = max(1, min(B, (1 << 24) // (H * K * V)))
     fmt = rng.choice(["int8", "e4m3"])
-    c = dict(op=op, B=B, H=rng.choice([1, 2, 4, 8]), P=B + rng.randint(0, 16), K=K, V=V,
+    c = dict(op=op, B=B, H=H, P=B + rng.randint(0, 16), K=K, V=V,
              W=rng.choice([4, 8, 16, 16, 32]), fmt=fmt, dtype=dtype)
     if op == "cstep":
         c.update(gate=rng.choice(["channel", "preact"]), fold=fmt == "e4m3")
