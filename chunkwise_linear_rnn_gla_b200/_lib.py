@@ -23,6 +23,9 @@ DTYPE = {"f32": 0, "bf16": 1}
 STATE_MODE = {"auto": 0, "materialized": 1, "nonmaterialized": 2}
 IMPL = {"auto": 0, "simt": 1, "tc": 2}
 GATE = {"channel": 0, "scalar": 1, "head": 2, "preact": 3}
+SCAN_WRITE = {"input": 0, "leak": 1}
+CACHE_FORMAT = {"int8": 0, "e4m3": 1}
+CACHE_GROUP = 128  # state columns that share one scale
 FLAG_WS_FROM_FWD = 0x1
 FLAG_CHECKS = 0x2
 
@@ -35,6 +38,8 @@ EXPORTS = (
     "gla_segment_decay", "gla_state_combine", "gla_fwd_final_state", "gla_bwd_initial_grad",
     "gla_gsa_resolve", "gla_gsa_fwd_workspace_size", "gla_gsa_bwd_workspace_size", "gla_gsa_fwd", "gla_gsa_bwd",
     "gla_gsa_step",
+    "gla_scan_workspace_size", "gla_scan_fwd", "gla_scan_bwd", "gla_scan_step",
+    "gla_cache_store", "gla_cache_load", "gla_cache_step",
 )
 
 
@@ -43,6 +48,12 @@ class GlaDesc(ctypes.Structure):
                 ("Dv", ctypes.c_int64), ("dtype", ctypes.c_int32), ("chunk", ctypes.c_int32),
                 ("subchunk", ctypes.c_int32), ("state_mode", ctypes.c_int32), ("impl", ctypes.c_int32),
                 ("flags", ctypes.c_int32), ("gate", ctypes.c_int32), ("gate_tau", ctypes.c_float)]
+
+
+class GlaCache(ctypes.Structure):
+    _fields_ = [("codes", ctypes.c_void_p), ("scale", ctypes.c_void_p), ("k", ctypes.c_void_p), ("v", ctypes.c_void_p),
+                ("log_a", ctypes.c_void_p), ("slots", ctypes.c_int64), ("window", ctypes.c_int32),
+                ("format", ctypes.c_int32)]
 
 
 _lock = threading.Lock()
@@ -112,9 +123,23 @@ def _declare(lib):
     lib.gla_gsa_bwd.restype = ctypes.c_int
     lib.gla_gsa_step.argtypes = [dp, i32] + [vp] * 7 + [vp]
     lib.gla_gsa_step.restype = ctypes.c_int
+    i64, cp = ctypes.c_int64, ctypes.POINTER(GlaCache)
+    lib.gla_scan_workspace_size.argtypes = [dp, i32]
+    lib.gla_scan_workspace_size.restype = sz
+    lib.gla_scan_fwd.argtypes = [dp, i32] + [vp] * 6 + [vp, sz, vp]
+    lib.gla_scan_fwd.restype = ctypes.c_int
+    lib.gla_scan_bwd.argtypes = [dp, i32] + [vp] * 9 + [vp, sz, vp]
+    lib.gla_scan_bwd.restype = ctypes.c_int
+    lib.gla_scan_step.argtypes = [dp, i32, vp, vp, vp, i64, vp, vp, vp]
+    lib.gla_scan_step.restype = ctypes.c_int
+    lib.gla_cache_store.argtypes = [dp, cp, vp, vp, vp]
+    lib.gla_cache_store.restype = ctypes.c_int
+    lib.gla_cache_load.argtypes = [dp, cp] + [vp] * 4
+    lib.gla_cache_load.restype = ctypes.c_int
+    lib.gla_cache_step.argtypes = [dp, cp] + [vp] * 8
+    lib.gla_cache_step.restype = ctypes.c_int
     lib.gla_segment_decay.argtypes = [dp, vp, vp, vp]
     lib.gla_segment_decay.restype = ctypes.c_int
-    i64 = ctypes.c_int64
     lib.gla_state_combine.argtypes = [i64, i64, i64, i64, vp, vp, vp, i32, i32, vp, vp]
     lib.gla_state_combine.restype = ctypes.c_int
 

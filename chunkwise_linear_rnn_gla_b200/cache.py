@@ -1,0 +1,140 @@
+"""Recurrent-state cache: thin binding over ``gla_cache_store`` / ``gla_cache_load`` / ``gla_cache_step``
+(include/gla.h). The matrix states of many sequences live in a pool of slots, in 8 bits with one scale per
+state row and 128 columns, and the last few tokens of each beside them; a decode step reads both and rounds
+the state back only when its window of tokens is full.
+
+    cache = StateCache.empty(slots, H, Dk, Dv)          # one per layer
+    o, hT = gla_fwd(q, k, v, log_a)                     # prefill
+    cache_store(cache, hT, slots)                       # quantised into its slots; lengths = 0
+    o_t = cache_step(cache, q1, k1, v1, log_a1, slots, lengths); lengths += 1
+    S = cache_load(cache, slots, lengths)               # fp32, e.g. the h0 of the next gla_fwd
+
+`lengths` (int32, device) counts each row's tokens since its state was stored; the caller advances it. A
+negative slot is a padding row (its output row is 0). A slot outside the pool, a negative length, or a slot
+named twice in one store or step is treated as padding and reported by gla_check_device_error.
+"""
+from __future__ import annotations
+
+import ctypes
+
+import torch
+
+from . import _check, _dt, _finish_checks, _lib, _need, _ptr, _stream, gate_shape, make_desc
+from ._lib import load
+
+__all__ = ["StateCache", "cache_store", "cache_load", "cache_step"]
+
+_FORMATS = {torch.int8: "int8", torch.float8_e4m3fn: "e4m3"}
+_CODES = {v: k for k, v in _FORMATS.items()}
+
+
+class StateCache:
+    """The tensors of a pool: codes [slots,H,Dk,Dv] (torch.int8 or torch.float8_e4m3fn), scale
+    [slots,H,Dk,ceil(Dv/128)] fp32, and the windows k [slots,H,W,Dk], v [slots,H,W,Dv] (fp32 or bf16, the
+    type of the layer's q, k, v) and log_a [slots,H,W,Dk] fp32."""
+
+    def __init__(self, codes, scale, k, v, log_a):
+        if not isinstance(codes, torch.Tensor) or codes.dim() != 4:
+            raise ValueError("codes must be a [slots, H, Dk, Dv] tensor")
+        if codes.dtype not in _FORMATS:
+            raise TypeError("codes must be int8 or float8_e4m3fn, got %s" % codes.dtype)
+        self.slots, self.H, self.Dk, self.Dv = codes.shape
+        if not isinstance(k, torch.Tensor) or k.dim() != 4:
+            raise ValueError("k must be a [slots, H, window, Dk] tensor")
+        self.window = k.shape[2]
+        dev = codes.device
+        _dt(k)
+        _need(codes, "codes", codes.shape, codes.dtype, dev)
+        _need(scale, "scale", (self.slots, self.H, self.Dk, -(-self.Dv // _lib.CACHE_GROUP)), torch.float32, dev)
+        _need(k, "k", (self.slots, self.H, self.window, self.Dk), k.dtype, dev)
+        _need(v, "v", (self.slots, self.H, self.window, self.Dv), k.dtype, dev)
+        _need(log_a, "log_a", k.shape, torch.float32, dev)
+        self.codes, self.scale, self.k, self.v, self.log_a = codes, scale, k, v, log_a
+        self.format, self.dtype, self.device = _FORMATS[codes.dtype], k.dtype, dev
+        self._c = _lib.GlaCache(codes.data_ptr(), scale.data_ptr(), k.data_ptr(), v.data_ptr(), log_a.data_ptr(),
+                                self.slots, self.window, _lib.CACHE_FORMAT[self.format])
+
+    @classmethod
+    def empty(cls, slots, H, Dk, Dv, *, window=16, format="int8", dtype=torch.bfloat16, device="cuda"):
+        """A pool of zero states."""
+        if format not in _CODES:
+            raise ValueError("format must be one of %s, got %r" % (sorted(_CODES), format))
+        f32 = dict(dtype=torch.float32, device=device)
+        return cls(torch.zeros(slots, H, Dk, Dv, dtype=torch.uint8, device=device).view(_CODES[format]),
+                   torch.zeros(slots, H, Dk, -(-Dv // _lib.CACHE_GROUP), **f32),
+                   torch.zeros(slots, H, window, Dk, dtype=dtype, device=device),
+                   torch.zeros(slots, H, window, Dv, dtype=dtype, device=device),
+                   torch.zeros(slots, H, window, Dk, **f32))
+
+    def _desc(self, B, gate="channel", tau=0.0, checks=False):
+        return make_desc(B, self.H, 1, self.Dk, self.Dv, "bf16" if self.dtype == torch.bfloat16 else "f32",
+                         flags=_lib.FLAG_CHECKS if checks else 0, gate=gate, tau=tau)
+
+
+def _rows(cache, slots, lengths=None):
+    if not isinstance(cache, StateCache):
+        raise TypeError("cache must be a StateCache")
+    if not isinstance(slots, torch.Tensor) or slots.dim() != 1:
+        raise ValueError("slots must be an int32 [B] tensor")
+    _need(slots, "slots", slots.shape, torch.int32, cache.device)
+    if lengths is not None:
+        _need(lengths, "lengths", slots.shape, torch.int32, cache.device)
+    return slots.shape[0]
+
+
+def cache_store(cache, S, slots, *, checks=False):
+    """Quantise the states S [B,H,Dk,Dv] (fp32) into their slots (int32 [B], device). Their lengths are 0 then."""
+    lib = load()
+    B = _rows(cache, slots)
+    dev = cache.device
+    _need(S, "S", (B, cache.H, cache.Dk, cache.Dv), torch.float32, dev)
+    desc = cache._desc(B, checks=checks)
+    with torch.cuda.device(dev):
+        st = lib.gla_cache_store(ctypes.byref(desc), ctypes.byref(cache._c), _ptr(S), _ptr(slots), _stream(dev))
+        _check(st, "gla_cache_store")
+        if checks:
+            _finish_checks([], "gla_cache_store")
+
+
+def cache_load(cache, slots, lengths=None, S=None, *, checks=False):
+    """The states of the slots, S [B,H,Dk,Dv] fp32, with the tokens in their windows applied (lengths None: as
+    stored)."""
+    lib = load()
+    B = _rows(cache, slots, lengths)
+    dev = cache.device
+    if S is None:
+        S = torch.empty(B, cache.H, cache.Dk, cache.Dv, dtype=torch.float32, device=dev)
+    _need(S, "S", (B, cache.H, cache.Dk, cache.Dv), torch.float32, dev)
+    desc = cache._desc(B, checks=checks)
+    with torch.cuda.device(dev):
+        st = lib.gla_cache_load(ctypes.byref(desc), ctypes.byref(cache._c), _ptr(slots), _ptr(lengths), _ptr(S),
+                                _stream(dev))
+        _check(st, "gla_cache_load")
+        if checks:
+            _finish_checks([], "gla_cache_load")
+    return S
+
+
+def cache_step(cache, q, k, v, log_a, slots, lengths, o=None, *, gate="channel", tau=0.0, checks=False):
+    """One decode step through the cache: q, k [B,H,Dk], v [B,H,Dv] (the cache's dtype), log_a as for gla_step
+    (fp32; every gate kind). Returns o [B,H,Dv]. The caller adds 1 to `lengths` afterwards."""
+    lib = load()
+    B = _rows(cache, slots, lengths)
+    if lengths is None:
+        raise TypeError("cache_step needs lengths")
+    dev, dt, H, Dk, Dv = cache.device, cache.dtype, cache.H, cache.Dk, cache.Dv
+    _need(q, "q", (B, H, Dk), dt, dev)
+    _need(k, "k", (B, H, Dk), dt, dev)
+    _need(v, "v", (B, H, Dv), dt, dev)
+    desc = cache._desc(B, gate, tau, checks)
+    _need(log_a, "log_a", gate_shape(gate, B, H, None, Dk), torch.float32, dev)
+    if o is None:
+        o = torch.empty(B, H, Dv, dtype=dt, device=dev)
+    _need(o, "o", (B, H, Dv), dt, dev)
+    with torch.cuda.device(dev):
+        st = lib.gla_cache_step(ctypes.byref(desc), ctypes.byref(cache._c), _ptr(q), _ptr(k), _ptr(v), _ptr(log_a),
+                                _ptr(slots), _ptr(lengths), _ptr(o), _stream(dev))
+        _check(st, "gla_cache_step")
+        if checks:
+            _finish_checks([], "gla_cache_step")
+    return o

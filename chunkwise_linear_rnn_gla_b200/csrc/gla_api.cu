@@ -271,6 +271,82 @@ gla_status resolve_gsa(const gla_desc* d, int32_t slots, gla::GsaProblem& g) {
     return st;
 }
 
+// Fields that the scan and the cache share with the chunkwise passes but have no use for.
+bool chunk_fields_unset(const gla_desc* d) {
+    return d->chunk == 0 && d->subchunk == 0 && d->state_mode == GLA_STATE_AUTO &&
+           (d->impl == GLA_IMPL_AUTO || d->impl == GLA_IMPL_SIMT);
+}
+
+gla_status resolve_scan(const gla_desc* d, int32_t write, bool packed, bool one_step, gla::ScanProblem& p) {
+    if (!d) return GLA_ERR_INVALID_ARG;
+    if (d->B < 1 || d->H < 1 || d->Dk < 1 || (!one_step && d->L < 1)) return GLA_ERR_INVALID_ARG;
+    if (d->dtype != GLA_DTYPE_F32 && d->dtype != GLA_DTYPE_BF16) return GLA_ERR_INVALID_ARG;
+    if (d->flags & ~int32_t(GLA_FLAG_WS_FROM_FWD | GLA_FLAG_CHECKS)) return GLA_ERR_INVALID_ARG;
+    if (write != GLA_SCAN_INPUT && write != GLA_SCAN_LEAK) return GLA_ERR_INVALID_ARG;
+    Problem gp{};
+    if (!gate_ok(d, gp)) return GLA_ERR_INVALID_ARG;
+    if (d->gate != GLA_GATE_CHANNEL && d->gate != GLA_GATE_PREACT) return GLA_ERR_UNSUPPORTED;
+    if (!chunk_fields_unset(d)) return GLA_ERR_UNSUPPORTED;
+    p.B = d->B;
+    p.H = d->H;
+    p.L = one_step ? 1 : d->L;
+    p.D = d->Dk;
+    p.bf16 = d->dtype == GLA_DTYPE_BF16;
+    p.packed = packed;
+    p.leak = write == GLA_SCAN_LEAK;
+    p.preact = d->gate == GLA_GATE_PREACT;
+    p.inv_tau = gp.inv_tau;
+    p.flags = d->flags;
+    // the grid's first axis counts (sequence or head, channel tile, segment); its second a step's rows
+    const int64_t lead = packed ? p.H : p.B * p.H;
+    if (lead > (int64_t(1) << 22) || p.B > (int64_t(1) << 22) || p.H > 65535 || p.L > (int64_t(1) << 30) ||
+        p.D > (int64_t(1) << 20) || lead * p.D > (int64_t(1) << 30))
+        return GLA_ERR_UNSUPPORTED;
+    if (one_step && (p.B > 65535 || p.H * p.D > (int64_t(1) << 30))) return GLA_ERR_UNSUPPORTED;
+    return GLA_OK;
+}
+
+gla::Arena scan_arena(const gla::ScanProblem& p, void* base, size_t cap) {
+    Problem f{};
+    f.flags = p.flags;
+    return gla::make_arena(f, base, cap);
+}
+
+bool scan_checks(const gla::ScanProblem& p) {
+    Problem f{};
+    f.flags = p.flags;
+    return gla::checks_on(f);
+}
+
+bool aligned4(const void* p) { return aligned(p, 4); }
+
+gla_status resolve_cache(const gla_desc* d, const gla_cache* c, gla::CacheProblem& p) {
+    if (!d || !c) return GLA_ERR_INVALID_ARG;
+    if (d->B < 1 || d->H < 1 || d->Dk < 1 || d->Dv < 1) return GLA_ERR_INVALID_ARG;
+    if (d->dtype != GLA_DTYPE_F32 && d->dtype != GLA_DTYPE_BF16) return GLA_ERR_INVALID_ARG;
+    if (d->flags & ~int32_t(GLA_FLAG_CHECKS)) return GLA_ERR_INVALID_ARG;
+    if (c->format != GLA_CACHE_INT8 && c->format != GLA_CACHE_E4M3) return GLA_ERR_INVALID_ARG;
+    if (c->slots < 1 || c->slots > INT32_MAX || c->window < 1 || c->window > 64) return GLA_ERR_INVALID_ARG;
+    Problem gp{};
+    if (!gate_ok(d, gp)) return GLA_ERR_INVALID_ARG;
+    if (!chunk_fields_unset(d)) return GLA_ERR_UNSUPPORTED;
+    p.B = d->B;
+    p.H = d->H;
+    p.K = d->Dk;
+    p.V = d->Dv;
+    p.bf16 = d->dtype == GLA_DTYPE_BF16;
+    p.gate = d->gate;
+    p.inv_tau = gp.inv_tau;
+    p.c = *c;
+    return gla::cache_supported(p) ? GLA_OK : GLA_ERR_UNSUPPORTED;
+}
+
+bool cache_checks(const gla_desc* d) {
+    Problem f{};
+    f.flags = d->flags;
+    return gla::checks_on(f);
+}
+
 #define GLA_REQUIRE_PTR(ptr) \
     do {                     \
         if (!(ptr) || !aligned((ptr), 16)) return GLA_ERR_INVALID_ARG; \
@@ -673,6 +749,169 @@ gla_status gla_gsa_bwd(const gla_desc* d, int32_t slots, const void* q, const vo
     return st;
 }
 
+// ---- elementwise gated recurrence ---------------------------------------------------
+size_t gla_scan_workspace_size(const gla_desc* d, int32_t packed) {
+    gla::ScanProblem p{};
+    if (resolve_scan(d, GLA_SCAN_INPUT, packed != 0, false, p) != GLA_OK) return 0;
+    gla::Arena a = scan_arena(p, nullptr, 0);
+    return gla::scan_workspace(p, a);
+}
+
+gla_status gla_scan_fwd(const gla_desc* d, int32_t write, const void* x, const float* log_a,
+                        const int32_t* cu_seqlens, const float* h0, void* h, float* hT, void* workspace,
+                        size_t workspace_bytes, void* stream) {
+    gla::ScanProblem p{};
+    gla_status st = resolve_scan(d, write, cu_seqlens != nullptr, false, p);
+    if (st != GLA_OK) return st;
+    if (p.flags & GLA_FLAG_WS_FROM_FWD) return GLA_ERR_INVALID_ARG;
+    GLA_REQUIRE_PTR(x);
+    GLA_REQUIRE_PTR(log_a);
+    GLA_REQUIRE_PTR(h);
+    GLA_OPTIONAL_PTR(h0);
+    GLA_OPTIONAL_PTR(hT);
+    if (!aligned4(cu_seqlens)) return GLA_ERR_INVALID_ARG;
+    gla::Arena a = scan_arena(p, workspace, workspace_bytes);
+    const size_t need = gla::scan_workspace(p, a);
+    float* seg = nullptr;
+    if (workspace) {
+        if ((st = check_ws(workspace, workspace_bytes, need)) != GLA_OK) return st;
+        seg = static_cast<float*>(workspace);
+    }
+    cudaStream_t s = static_cast<cudaStream_t>(stream);
+    const bool chk = scan_checks(p);
+    const int64_t rows = (p.packed ? p.H : p.B * p.H) * p.L;
+    if (chk) {
+        if (!p.preact && (st = gla::check_gates(log_a, rows * p.D, s)) != GLA_OK) return st;
+        if (workspace && (st = gla::guards_fill(a, s)) != GLA_OK) return st;
+    }
+    st = gla::scan_fwd(p, x, log_a, cu_seqlens, h0, h, hT, seg, s);
+    if (st != GLA_OK || !chk) return st;
+    // a packed h has rows that belong to no sequence and hold whatever the caller left there
+    if (!p.packed) st = gla::check_finite(h, rows * p.D, p.bf16, s);
+    if (st == GLA_OK) st = gla::check_finite(hT, p.B * p.H * p.D, false, s);
+    if (st == GLA_OK && workspace) st = gla::guards_check(a, s);
+    return st;
+}
+
+gla_status gla_scan_bwd(const gla_desc* d, int32_t write, const void* x, const float* log_a,
+                        const int32_t* cu_seqlens, const float* h0, const void* dh, const float* dhT, void* dx,
+                        float* dlog_a, float* dh0, void* workspace, size_t workspace_bytes, void* stream) {
+    gla::ScanProblem p{};
+    gla_status st = resolve_scan(d, write, cu_seqlens != nullptr, false, p);
+    if (st != GLA_OK) return st;
+    GLA_REQUIRE_PTR(x);
+    GLA_REQUIRE_PTR(log_a);
+    GLA_REQUIRE_PTR(dh);
+    GLA_REQUIRE_PTR(dx);
+    GLA_REQUIRE_PTR(dlog_a);
+    GLA_OPTIONAL_PTR(h0);
+    GLA_OPTIONAL_PTR(dhT);
+    GLA_OPTIONAL_PTR(dh0);
+    if (!aligned4(cu_seqlens)) return GLA_ERR_INVALID_ARG;
+    gla::Arena a = scan_arena(p, workspace, workspace_bytes);
+    if ((st = check_ws(workspace, workspace_bytes, gla::scan_workspace(p, a))) != GLA_OK) return st;
+    cudaStream_t s = static_cast<cudaStream_t>(stream);
+    const bool chk = scan_checks(p);
+    const int64_t rows = (p.packed ? p.H : p.B * p.H) * p.L;
+    if (chk) {
+        if (!p.preact && (st = gla::check_gates(log_a, rows * p.D, s)) != GLA_OK) return st;
+        if ((st = gla::guards_fill(a, s)) != GLA_OK) return st;
+    }
+    st = gla::scan_bwd(p, x, log_a, cu_seqlens, h0, dh, dhT, dx, dlog_a, dh0, static_cast<float*>(workspace),
+                       (p.flags & GLA_FLAG_WS_FROM_FWD) != 0, s);
+    if (st != GLA_OK || !chk) return st;
+    if (!p.packed) {
+        st = gla::check_finite(dx, rows * p.D, p.bf16, s);
+        if (st == GLA_OK) st = gla::check_finite(dlog_a, rows * p.D, false, s);
+    }
+    if (st == GLA_OK) st = gla::check_finite(dh0, p.B * p.H * p.D, false, s);
+    if (st == GLA_OK) st = gla::guards_check(a, s);
+    return st;
+}
+
+gla_status gla_scan_step(const gla_desc* d, int32_t write, const void* x, const float* log_a, const int32_t* slots,
+                         int64_t pool, float* state, void* h, void* stream) {
+    gla::ScanProblem p{};
+    gla_status st = resolve_scan(d, write, false, true, p);
+    if (st != GLA_OK) return st;
+    if (p.flags & GLA_FLAG_WS_FROM_FWD) return GLA_ERR_INVALID_ARG;
+    if (pool < 1 || pool > INT32_MAX || (!slots && pool < p.B)) return GLA_ERR_INVALID_ARG;
+    GLA_REQUIRE_PTR(x);
+    GLA_REQUIRE_PTR(log_a);
+    GLA_REQUIRE_PTR(state);
+    GLA_REQUIRE_PTR(h);
+    if (!aligned4(slots)) return GLA_ERR_INVALID_ARG;
+    cudaStream_t s = static_cast<cudaStream_t>(stream);
+    const bool chk = scan_checks(p);
+    const int64_t n = p.B * p.H * p.D;
+    if (chk && !p.preact && (st = gla::check_gates(log_a, n, s)) != GLA_OK) return st;
+    st = gla::scan_step(p, x, log_a, slots, pool, state, h, s);
+    if (st != GLA_OK || !chk) return st;
+    return gla::check_finite(h, n, p.bf16, s);
+}
+
+// ---- recurrent-state cache ------------------------------------------------------------
+gla_status gla_cache_store(const gla_desc* d, const gla_cache* c, const float* S, const int32_t* slots,
+                           void* stream) {
+    gla::CacheProblem p{};
+    gla_status st = resolve_cache(d, c, p);
+    if (st != GLA_OK) return st;
+    GLA_REQUIRE_PTR(c->codes);
+    GLA_REQUIRE_PTR(c->scale);
+    GLA_REQUIRE_PTR(S);
+    if (!slots || !aligned4(slots)) return GLA_ERR_INVALID_ARG;
+    cudaStream_t s = static_cast<cudaStream_t>(stream);
+    if (cache_checks(d) && (st = gla::check_finite(S, p.B * p.H * p.K * p.V, false, s)) != GLA_OK) return st;
+    return gla::cache_store(p, S, slots, s);
+}
+
+gla_status gla_cache_load(const gla_desc* d, const gla_cache* c, const int32_t* slots, const int32_t* lengths,
+                          float* S, void* stream) {
+    gla::CacheProblem p{};
+    gla_status st = resolve_cache(d, c, p);
+    if (st != GLA_OK) return st;
+    GLA_REQUIRE_PTR(c->codes);
+    GLA_REQUIRE_PTR(c->scale);
+    if (lengths) {
+        GLA_REQUIRE_PTR(c->k);
+        GLA_REQUIRE_PTR(c->v);
+        GLA_REQUIRE_PTR(c->log_a);
+    }
+    GLA_REQUIRE_PTR(S);
+    if (!slots || !aligned4(slots) || !aligned4(lengths)) return GLA_ERR_INVALID_ARG;
+    cudaStream_t s = static_cast<cudaStream_t>(stream);
+    st = gla::cache_load(p, slots, lengths, S, s);
+    if (st != GLA_OK || !cache_checks(d)) return st;
+    return gla::check_finite(S, p.B * p.H * p.K * p.V, false, s);
+}
+
+gla_status gla_cache_step(const gla_desc* d, const gla_cache* c, const void* q, const void* k, const void* v,
+                          const float* log_a, const int32_t* slots, const int32_t* lengths, void* o, void* stream) {
+    gla::CacheProblem p{};
+    gla_status st = resolve_cache(d, c, p);
+    if (st != GLA_OK) return st;
+    GLA_REQUIRE_PTR(c->codes);
+    GLA_REQUIRE_PTR(c->scale);
+    GLA_REQUIRE_PTR(c->k);
+    GLA_REQUIRE_PTR(c->v);
+    GLA_REQUIRE_PTR(c->log_a);
+    GLA_REQUIRE_PTR(q);
+    GLA_REQUIRE_PTR(k);
+    GLA_REQUIRE_PTR(v);
+    GLA_REQUIRE_PTR(log_a);
+    GLA_REQUIRE_PTR(o);
+    if (!slots || !lengths || !aligned4(slots) || !aligned4(lengths)) return GLA_ERR_INVALID_ARG;
+    cudaStream_t s = static_cast<cudaStream_t>(stream);
+    const bool chk = cache_checks(d);
+    if (chk && d->gate != GLA_GATE_PREACT) {
+        const int64_t n = d->gate == GLA_GATE_HEAD ? p.H : p.B * p.H * (d->gate == GLA_GATE_SCALAR ? 1 : p.K);
+        if ((st = gla::check_gates(log_a, n, s)) != GLA_OK) return st;
+    }
+    st = gla::cache_step(p, q, k, v, log_a, slots, lengths, o, s);
+    if (st != GLA_OK || !chk) return st;
+    return gla::check_finite(o, p.B * p.H * p.V, p.bf16, s);
+}
+
 namespace {
 // One thread waits on an mbarrier nothing arrives on: the bounded wait must give up, record the
 // timeout and let the kernel finish.
@@ -706,7 +945,7 @@ gla_status gla_check_device_error(void* stream) {
         const int zero = 0;
         if (cudaMemcpy(w, &zero, sizeof(int), cudaMemcpyHostToDevice) != cudaSuccess) return GLA_ERR_CUDA;
         if (h & gla::tc::kErrWaitTimeout) return GLA_ERR_TIMEOUT;
-        if (h & (gla::kErrBadGate | gla::kErrNonFinite)) return GLA_ERR_INVALID_ARG;
+        if (h & (gla::kErrBadGate | gla::kErrNonFinite | gla::kErrBadRow)) return GLA_ERR_INVALID_ARG;
         if (h & gla::kErrGuard) return GLA_ERR_WORKSPACE;
         return GLA_ERR_CUDA;
     }

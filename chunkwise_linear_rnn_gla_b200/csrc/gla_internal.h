@@ -65,9 +65,9 @@ gla_status launch_end(const char* name, cudaStream_t s);
 
 // Device-side error word (set by kernels whose bounded waits run out, and by
 // the checking build's checks). Bits: tc::kErrWaitTimeout, kErrBadGate,
-// kErrNonFinite, kErrGuard.
+// kErrNonFinite, kErrGuard, and kErrBadRow (a row that a pooled call refused for its slot or length).
 int* device_error_word();
-enum : int { kErrBadGate = 2, kErrNonFinite = 4, kErrGuard = 8 };
+enum : int { kErrBadGate = 2, kErrNonFinite = 4, kErrGuard = 8, kErrBadRow = 16 };
 
 // ---- checking build (gla_checks.cu) ------------------------------------------
 // Before a pass: every gate must be finite and <= 0 (kErrBadGate); the workspace
@@ -153,6 +153,41 @@ gla_status gsa_bwd(const GsaProblem& g, const void* q, const void* k, const void
                    const float* hk0, const float* hv0, const void* dO, const float* dhkT, const float* dhvT, void* dq,
                    void* dk, void* dv, float* dla, float* dhk0, float* dhv0, bool reuse, void* ws, size_t cap,
                    cudaStream_t s);
+
+// ---- elementwise gated recurrence (gla_scan.cu) -------------------------------------
+struct ScanProblem {
+    int64_t B, H, L, D;  // dense: B sequences of L steps; packed: B sequences in L rows
+    bool bf16;
+    bool packed;
+    bool leak;      // w_t = 1 - a_t
+    bool preact;    // log_a holds z
+    float inv_tau;
+    int flags;
+};
+// Workspace: the fp32 state entering every segment of rows, [B*H or H][segments][D].
+size_t scan_workspace(const ScanProblem& p, Arena& a);
+gla_status scan_fwd(const ScanProblem& p, const void* x, const float* la, const int32_t* cu, const float* h0, void* h,
+                    float* hT, float* seg, cudaStream_t s);
+gla_status scan_bwd(const ScanProblem& p, const void* x, const float* la, const int32_t* cu, const float* h0,
+                    const void* dh, const float* dhT, void* dx, float* dla, float* dh0, float* seg, bool reuse,
+                    cudaStream_t s);
+gla_status scan_step(const ScanProblem& p, const void* x, const float* la, const int32_t* slots, int64_t pool,
+                     float* state, void* h, cudaStream_t s);
+
+// ---- recurrent-state cache (gla_cache.cu) -------------------------------------------
+struct CacheProblem {
+    int64_t B, H, K, V;
+    bool bf16;
+    int gate;
+    float inv_tau;
+    gla_cache c;
+};
+constexpr int kCacheGroup = 128;  // state columns that share one scale
+bool cache_supported(const CacheProblem& p);
+gla_status cache_store(const CacheProblem& p, const float* S, const int32_t* slots, cudaStream_t s);
+gla_status cache_load(const CacheProblem& p, const int32_t* slots, const int32_t* lengths, float* S, cudaStream_t s);
+gla_status cache_step(const CacheProblem& p, const void* q, const void* k, const void* v, const float* la,
+                      const int32_t* slots, const int32_t* lengths, void* o, cudaStream_t s);
 
 }  // namespace gla
 

@@ -1,0 +1,175 @@
+"""Elementwise gated recurrence (vector state): thin binding over ``gla_scan_fwd`` / ``gla_scan_bwd`` /
+``gla_scan_step`` (include/gla.h). Argument checks, output allocation and the current stream only; every
+step runs in libgla's kernels.
+
+Per sequence, head and channel, with a_t = exp(log_a_t):
+    h_t = a_t h_{t-1} + w_t x_t,    w_t = 1 (write="input") or 1 - a_t (write="leak"),
+with h_{-1} = h0 and hT the last state. It is the layer's gated memory without a key dimension, for
+recurrent layers that stand beside GLA layers in a stack.
+
+Shapes: x, h [B,H,L,D] (a [B,L,D] tensor is the H=1 case: x.unsqueeze(1)); log_a [B,H,L,D] fp32;
+states h0, hT [B,H,D] fp32. Packed sequences: x, log_a [1,H,T,D] and cu_seqlens (int32 [N+1], device);
+sequence n holds the rows cu_seqlens[n] .. cu_seqlens[n+1]-1, may be empty, and has row n of the states
+[N,H,D]. Rows outside every sequence are left as they were in a buffer that the caller passes, and are 0 in
+one that is allocated here.
+gate="preact": log_a holds the gate's argument z, log a = logsigmoid(z) / tau.
+"""
+from __future__ import annotations
+
+import ctypes
+from typing import Optional
+
+import torch
+
+from . import _check, _dt, _finish_checks, _lib, _need, _ptr, _stream, _workspace, make_desc
+from ._lib import load
+
+__all__ = ["scan_fwd", "scan_bwd", "scan_step", "scan_workspace_size", "scan_workspace"]
+
+
+def _write(write: str) -> int:
+    if write not in _lib.SCAN_WRITE:
+        raise ValueError("write must be one of %s, got %r" % (sorted(_lib.SCAN_WRITE), write))
+    return _lib.SCAN_WRITE[write]
+
+
+def _index(t, name, n, dev):
+    _need(t, name, (n,), torch.int32, dev)
+
+
+def _sizes(x, cu_seqlens):
+    """(sequences, H, rows, D) of x, which is [B,H,L,D], or [1,H,T,D] with cu_seqlens."""
+    if not isinstance(x, torch.Tensor) or x.dim() != 4:
+        raise ValueError("x must be a [B, H, L, D] tensor")
+    if not x.is_contiguous():
+        raise ValueError("x must be contiguous")
+    B, H, L, D = x.shape
+    if cu_seqlens is None:
+        return B, H, L, D
+    if B != 1:
+        raise ValueError("packed sequences need x of shape [1, H, T, D], got %s" % (tuple(x.shape),))
+    if not isinstance(cu_seqlens, torch.Tensor) or cu_seqlens.dim() != 1 or cu_seqlens.numel() < 2:
+        raise ValueError("cu_seqlens must be an int32 [N + 1] tensor, N >= 1")
+    _index(cu_seqlens, "cu_seqlens", cu_seqlens.numel(), x.device)
+    return cu_seqlens.numel() - 1, H, L, D
+
+
+def _desc(x, B, H, L, D, gate, tau, flags):
+    return make_desc(B, H, L, D, 1, _dt(x), flags=flags, gate=gate, tau=tau)
+
+
+def scan_workspace_size(desc, packed: bool = False) -> int:
+    """Workspace bytes of scan_fwd / scan_bwd for a descriptor (Dk = channels, Dv ignored)."""
+    return int(load().gla_scan_workspace_size(ctypes.byref(desc), 1 if packed else 0))
+
+
+def scan_workspace(x, cu_seqlens=None, checks=False) -> torch.Tensor:
+    """A workspace for scan_fwd and the scan_bwd that follows it."""
+    B, H, L, D = _sizes(x, cu_seqlens)
+    d = _desc(x, B, H, L, D, "channel", 0.0, _lib.FLAG_CHECKS if checks else 0)
+    return torch.empty(scan_workspace_size(d, cu_seqlens is not None), dtype=torch.uint8, device=x.device)
+
+
+def _buffer(t, like, name, packed):
+    if t is None:
+        return torch.zeros_like(like) if packed else torch.empty_like(like)
+    _need(t, name, like.shape, like.dtype, like.device)
+    return t
+
+
+def scan_fwd(x, log_a, h0=None, *, cu_seqlens=None, write="input", gate="channel", tau=0.0, h=None, hT=None,
+             want_hT=True, workspace: Optional[torch.Tensor] = None, checks=False):
+    """Forward. Returns (h, hT); hT is None when want_hT is False and no hT buffer is given. A `workspace`
+    (scan_workspace) keeps what scan_bwd(ws_from_fwd=True) reuses. checks=True: the library's checking mode
+    (gate domain, finite outputs), synchronous, raises GlaError on a failure."""
+    lib = load()
+    B, H, L, D = _sizes(x, cu_seqlens)
+    dev = x.device
+    _need(log_a, "log_a", x.shape, torch.float32, dev)
+    if h0 is not None:
+        _need(h0, "h0", (B, H, D), torch.float32, dev)
+    desc = _desc(x, B, H, L, D, gate, tau, _lib.FLAG_CHECKS if checks else 0)
+    h = _buffer(h, x, "h", cu_seqlens is not None)
+    if hT is None and want_hT:
+        hT = torch.empty(B, H, D, dtype=torch.float32, device=dev)
+    if hT is not None:
+        _need(hT, "hT", (B, H, D), torch.float32, dev)
+    ws, nbytes = None, 0
+    if workspace is not None:
+        ws, nbytes = _workspace(scan_workspace_size(desc, cu_seqlens is not None), dev, workspace)
+    with torch.cuda.device(dev):
+        st = lib.gla_scan_fwd(ctypes.byref(desc), _write(write), _ptr(x), _ptr(log_a), _ptr(cu_seqlens), _ptr(h0),
+                              _ptr(h), _ptr(hT), _ptr(ws), nbytes, _stream(dev))
+        _check(st, "gla_scan_fwd")
+        if checks:
+            _finish_checks([], "gla_scan_fwd")
+    return h, hT
+
+
+def scan_bwd(x, log_a, dh, h0=None, dhT=None, *, cu_seqlens=None, write="input", gate="channel", tau=0.0,
+             want_dh0=True, workspace: Optional[torch.Tensor] = None, ws_from_fwd=False, out=None, checks=False):
+    """Backward of <dh, h> + <dhT, hT>. Returns a dict with dx, dlog_a (dL/dz for gate="preact") and dh0
+    (None when want_dh0 is False and `out` has no buffer for it). `out` may hold buffers under these names.
+    With ws_from_fwd=True the workspace must be the one the matching scan_fwd was given (same inputs, same
+    options)."""
+    lib = load()
+    B, H, L, D = _sizes(x, cu_seqlens)
+    dev = x.device
+    packed = cu_seqlens is not None
+    _need(log_a, "log_a", x.shape, torch.float32, dev)
+    _need(dh, "dh", x.shape, x.dtype, dev)
+    for t, n in ((h0, "h0"), (dhT, "dhT")):
+        if t is not None:
+            _need(t, n, (B, H, D), torch.float32, dev)
+    if ws_from_fwd and workspace is None:
+        raise ValueError("ws_from_fwd needs the forward's workspace")
+    flags = (_lib.FLAG_WS_FROM_FWD if ws_from_fwd else 0) | (_lib.FLAG_CHECKS if checks else 0)
+    desc = _desc(x, B, H, L, D, gate, tau, flags)
+    out = dict(out or {})
+    dx = _buffer(out.get("dx"), x, "dx", packed)
+    dla = _buffer(out.get("dlog_a"), log_a, "dlog_a", packed)
+    dh0 = out.get("dh0")
+    if dh0 is None and want_dh0:
+        dh0 = torch.empty(B, H, D, dtype=torch.float32, device=dev)
+    if dh0 is not None:
+        _need(dh0, "dh0", (B, H, D), torch.float32, dev)
+    ws, nbytes = _workspace(scan_workspace_size(desc, packed), dev, workspace)
+    with torch.cuda.device(dev):
+        st = lib.gla_scan_bwd(ctypes.byref(desc), _write(write), _ptr(x), _ptr(log_a), _ptr(cu_seqlens), _ptr(h0),
+                              _ptr(dh), _ptr(dhT), _ptr(dx), _ptr(dla), _ptr(dh0), _ptr(ws), nbytes, _stream(dev))
+        _check(st, "gla_scan_bwd")
+        if checks:
+            _finish_checks([], "gla_scan_bwd")
+    return {"dx": dx, "dlog_a": dla, "dh0": dh0}
+
+
+def scan_step(x, log_a, state, slots=None, *, write="input", gate="channel", tau=0.0, h=None, checks=False):
+    """One token per row: x, log_a [B,H,D]; state [pool,H,D] fp32, updated in place. slots (int32 [B], device)
+    names each row's entry of the pool (None: row b has entry b); a negative slot is a padding row, whose h is
+    0. Returns h [B,H,D]. A slot outside the pool, or named twice in one call, is treated as padding and
+    reported by gla_check_device_error."""
+    lib = load()
+    if not isinstance(x, torch.Tensor) or x.dim() != 3:
+        raise ValueError("x must be a [B, H, D] tensor")
+    dev = x.device
+    B, H, D = x.shape
+    _need(x, "x", x.shape, x.dtype, dev)
+    _need(log_a, "log_a", x.shape, torch.float32, dev)
+    if not isinstance(state, torch.Tensor) or state.dim() != 3:
+        raise ValueError("state must be a [pool, H, D] tensor")
+    _need(state, "state", (state.shape[0], H, D), torch.float32, dev)
+    if slots is not None:
+        _index(slots, "slots", B, dev)
+    elif state.shape[0] < B:
+        raise ValueError("state has %d entries for %d rows" % (state.shape[0], B))
+    if h is None:
+        h = torch.empty_like(x)
+    _need(h, "h", x.shape, x.dtype, dev)
+    desc = _desc(x, B, H, 1, D, gate, tau, _lib.FLAG_CHECKS if checks else 0)
+    with torch.cuda.device(dev):
+        st = lib.gla_scan_step(ctypes.byref(desc), _write(write), _ptr(x), _ptr(log_a), _ptr(slots), state.shape[0],
+                               _ptr(state), _ptr(h), _stream(dev))
+        _check(st, "gla_scan_step")
+        if checks:
+            _finish_checks([], "gla_scan_step")
+    return h

@@ -291,6 +291,139 @@ gla_status gla_gsa_bwd(const gla_desc* d, int32_t slots, const void* q, const vo
                        const float* dhkT, const float* dhvT, void* dq, void* dk, void* dv, float* dlog_a,
                        float* dhk0, float* dhv0, void* workspace, size_t workspace_bytes, void* stream);
 
+/* ---- elementwise gated recurrence (scan) -----------------------------------
+ * The vector-state member of the family: the same decay, with one state value
+ * per channel instead of a Dk x Dv matrix (a gated linear recurrent layer that
+ * stands beside GLA layers in a stack). Per sequence, head and channel, with
+ * a_t = exp(log_a_t):
+ *
+ *     h_t = a_t h_{t-1} + w_t x_t,      w_t = 1       (GLA_SCAN_INPUT)
+ *                                       w_t = 1 - a_t (GLA_SCAN_LEAK: the input
+ *                                             enters as far as the state decays)
+ * with h_{-1} = h0 (NULL: zero) and hT the state after the last step.
+ *
+ * Descriptor: Dk is the number of channels D (Dv is ignored), dtype the type of
+ * x, h, dh and dx; gate is GLA_GATE_CHANNEL or GLA_GATE_PREACT (as for gla_fwd;
+ * other kinds GLA_ERR_UNSUPPORTED); chunk, subchunk and state_mode must be 0
+ * and impl AUTO or SIMT (GLA_ERR_UNSUPPORTED otherwise); flags as for gla_fwd /
+ * gla_bwd. log_a may be any value <= 0, a zero gate included.
+ * Layouts (row-major, contiguous, device):
+ *   cu_seqlens == NULL (B sequences of L steps):
+ *     x, h, dh, dx            [B, H, L, D]  (dtype);  log_a, dlog_a [B, H, L, D] fp32
+ *   cu_seqlens != NULL (B sequences packed into L rows in all; int32 [B+1] on
+ *   the device, non-decreasing, 0 <= cu[0], cu[B] <= L; sequence n holds the
+ *   rows cu[n] .. cu[n+1]-1 and may be empty):
+ *     x, h, dh, dx            [H, L, D]     (dtype);  log_a, dlog_a [H, L, D] fp32
+ *     Rows outside every sequence are left as they were. An empty sequence has
+ *     hT = h0 and dh0 = dhT. The values are not checked on the host; whatever
+ *     they hold, no access leaves the tensors.
+ *   h0, hT, dhT, dh0          [B, H, D] fp32 (nullable)
+ * Sums and states are fp32; only h and dx are rounded to dtype. The result does
+ * not depend on how the sequences are packed beyond the rounding of the joins.
+ *
+ * The backward returns the gradients of <dh, h> + <dhT, hT>:
+ *     g_t = dh_t + a_{t+1} g_{t+1}  (+ dhT at the last step),   dx_t = w_t g_t,
+ *     dlog_a_t = a_t (h_{t-1} [- x_t with GLA_SCAN_LEAK]) g_t,  dh0 = a_0 g_0,
+ * times sigmoid(-z) / gate_tau for GLA_GATE_PREACT. It recomputes h_{t-1} in
+ * fp32 from the states entering each segment of rows, which the forward leaves
+ * in the workspace when it is given one (GLA_FLAG_WS_FROM_FWD: the backward
+ * takes them from there; otherwise it computes them first).
+ * Workspace: gla_scan_workspace_size bytes, the same for both passes; the
+ * forward's may be NULL (nothing is kept for a backward). */
+typedef enum gla_scan_write {
+    GLA_SCAN_INPUT = 0,
+    GLA_SCAN_LEAK = 1
+} gla_scan_write;
+
+/* packed: whether the call gets cu_seqlens. 0 for an invalid descriptor. */
+size_t gla_scan_workspace_size(const gla_desc* d, int32_t packed);
+gla_status gla_scan_fwd(const gla_desc* d, int32_t write, const void* x, const float* log_a,
+                        const int32_t* cu_seqlens, const float* h0, void* h, float* hT, void* workspace,
+                        size_t workspace_bytes, void* stream);
+gla_status gla_scan_bwd(const gla_desc* d, int32_t write, const void* x, const float* log_a,
+                        const int32_t* cu_seqlens, const float* h0, const void* dh, const float* dhT, void* dx,
+                        float* dlog_a, float* dh0, void* workspace, size_t workspace_bytes, void* stream);
+
+/* One token for B sequences: x, h [B, H, D] (dtype), log_a [B, H, D] (fp32, or z
+ * with GLA_GATE_PREACT); state [pool, H, D] fp32, updated in place. slots (int32
+ * [B], device) names each row's entry of the pool; NULL: row b has entry b
+ * (pool >= B). A negative slot marks a padding row: its h is 0 and no state is
+ * touched. A slot >= pool, or one that an earlier row of the call names too, is
+ * refused: that row is treated as padding and gla_check_device_error reports
+ * GLA_ERR_INVALID_ARG. d->L is ignored. */
+gla_status gla_scan_step(const gla_desc* d, int32_t write, const void* x, const float* log_a, const int32_t* slots,
+                         int64_t pool, float* state, void* h, void* stream);
+
+/* ---- recurrent-state cache ---------------------------------------------------
+ * The serving form of the layer's state: a pool of slots, each holding the
+ * matrix state S of one sequence (H heads) in 8 bits, and the last few tokens
+ * that are not yet part of it.
+ *
+ *   codes [slots, H, Dk, Dv]                 int8 or e4m3
+ *   scale [slots, H, Dk, ceil(Dv / 128)]     fp32: one per state row and 128 columns
+ *   k     [slots, H, window, Dk]  (dtype)    keys,
+ *   v     [slots, H, window, Dv]  (dtype)    values and
+ *   log_a [slots, H, window, Dk]  fp32       log decays of up to `window` tokens
+ *
+ * A group of 128 columns of one row with largest magnitude m is held as
+ *   scale = m / 127 (int8) or m / 448 (e4m3),   code = round(S / scale),
+ * rounded to nearest, ties to even (scale = m * fl(1/127), and S times the
+ * rounded reciprocal of scale). A group with m < 1e-30 is held as zero; one with
+ * an infinite or NaN entry reads back as NaN throughout.
+ *
+ * A single-token step (gla_cache_step) of a sequence that has seen `length`
+ * tokens since its state was stored, n = length mod window, puts the token into
+ * place n of the window and returns o = q S_t, where
+ *   S_t = diag(e^G) (scale code) + sum_{j<=n} (k_j e^{D_j})^T v_j,
+ *   D_j = sum of log a over the window tokens behind j,  G = the sum over all of
+ * them: exactly the recurrence, in fp32, from the cached state. Only the step
+ * that fills the window (n = window - 1) rounds S_t back into the slot. So a
+ * step reads 1 byte per state entry where gla_step reads 4 and writes 4, and a
+ * state is rounded once per `window` tokens and not at every one, which would
+ * lose every update below half a code step.
+ *
+ * The caller keeps `length` per sequence (0 after gla_cache_store) and passes it
+ * with the slot; a step does not change it. slots and lengths are int32 [B] on
+ * the device. A negative slot marks a padding row: it touches no slot, and its
+ * row of o (or of S in gla_cache_load) is 0. A slot >= `slots` or a negative length
+ * is refused, and so is a slot that an earlier row of the same gla_cache_step or
+ * gla_cache_store names too: the row is treated as padding and
+ * gla_check_device_error reports GLA_ERR_INVALID_ARG.
+ *
+ * Descriptor: B rows, H, Dk, Dv, dtype (q, k, v, o and the window), gate and
+ * gate_tau (gla_cache_step; all kinds, stored as per-channel log a) and flags
+ * (GLA_FLAG_CHECKS); L is ignored, the other fields as for the scan. window is
+ * 1 .. 64; GLA_ERR_UNSUPPORTED when a head's window does not fit on chip
+ * (4 * window * (Dk + 128) + 16 Dk + 8192 bytes above 200 KB). */
+typedef enum gla_cache_format {
+    GLA_CACHE_INT8 = 0,
+    GLA_CACHE_E4M3 = 1
+} gla_cache_format;
+
+typedef struct gla_cache {
+    void* codes;
+    float* scale;
+    void* k;
+    void* v;
+    float* log_a;
+    int64_t slots;
+    int32_t window;
+    int32_t format; /* gla_cache_format */
+} gla_cache;
+
+/* Quantise S [B,H,Dk,Dv] (fp32) into the slots (their windows then count as
+ * empty: length 0). Only codes and scale are used. */
+gla_status gla_cache_store(const gla_desc* d, const gla_cache* c, const float* S, const int32_t* slots, void* stream);
+/* Read the states back: S [B,H,Dk,Dv] fp32, with the first (lengths mod window)
+ * tokens of each window applied. lengths NULL: the states as stored (the window
+ * is not read). A padding row gives a zero state. The same slot may be named by
+ * several rows. */
+gla_status gla_cache_load(const gla_desc* d, const gla_cache* c, const int32_t* slots, const int32_t* lengths,
+                          float* S, void* stream);
+/* One token per row: q, k [B,H,Dk], v, o [B,H,Dv] (dtype), log_a as for gla_step. */
+gla_status gla_cache_step(const gla_desc* d, const gla_cache* c, const void* q, const void* k, const void* v,
+                          const float* log_a, const int32_t* slots, const int32_t* lengths, void* o, void* stream);
+
 /* ---- forward without any allocation ---------------------------------------
  * The paper has no counterpart to this entry point; it exists for callers
  * that cannot allocate device memory or provide a workspace: a plugin under
@@ -322,9 +455,10 @@ gla_status gla_fwd_noalloc(const gla_desc* d, const void* q, const void* k, cons
 
 /* Blocks until `stream` is idle, then reports (and clears) the device-side
  * error flag: GLA_ERR_TIMEOUT if a bounded wait ran out in any kernel since
- * the last check; else, for calls made in checking mode (GLA_FLAG_CHECKS),
- * GLA_ERR_INVALID_ARG if a gate was outside its domain or an output was not
- * finite, GLA_ERR_WORKSPACE if a workspace guard block was overwritten;
+ * the last check; else GLA_ERR_INVALID_ARG if a row of a gla_scan_step or
+ * gla_cache_* call was refused (a bad slot or length), or if, in a call made in
+ * checking mode (GLA_FLAG_CHECKS), a gate was outside its domain or an output
+ * was not finite; GLA_ERR_WORKSPACE if a workspace guard block was overwritten;
  * GLA_ERR_CUDA on a sticky CUDA error; else GLA_OK. */
 gla_status gla_check_device_error(void* stream);
 
