@@ -197,6 +197,26 @@ def test_scan_packed_leaves_other_rows(lib):
 
 
 @pytest.mark.gpu
+@pytest.mark.parametrize("bad", [float("nan"), float("inf")])
+def test_scan_packed_sequences_do_not_reach_each_other(lib, bad):
+    """One sequence full of NaN or infinities: its neighbours' results are those without it, bit for bit."""
+    cu, T, D = [0, 37, 300, 1500, 1507], 1507, 64
+    t = make(1, 1, T, D, torch.float32, "channel", cu=cu, seed=12)
+    want = run(t, cu, "leak", "channel")
+    for n in ("x", "z", "dh"):
+        p = dict(t, **{n: t[n].clone()})
+        p[n][:, :, 37:300] = bad if n != "z" else -bad
+        p["h0"], p["dhT"] = t["h0"].clone(), t["dhT"].clone()
+        p["h0"][1], p["dhT"][1] = bad, bad
+        got = run(p, cu, "leak", "channel")
+        for m in ("h", "dx", "dlog_a"):
+            assert torch.equal(got[m][:, :, :37], want[m][:, :, :37]) and torch.equal(got[m][:, :, 300:], want[m][:, :, 300:])
+        for m in ("hT", "dh0"):
+            assert torch.equal(got[m][[0, 2, 3]], want[m][[0, 2, 3]])
+        assert not bool(torch.isfinite(got["dx"][:, :, 37:300]).all())
+
+
+@pytest.mark.gpu
 @pytest.mark.parametrize("cu", [None, [0, 100, 700]])
 def test_scan_without_states_and_without_reuse(lib, cu):
     t = make(2, 1, 700, 40, torch.float32, "channel", cu=cu, seed=3, h0=False)
