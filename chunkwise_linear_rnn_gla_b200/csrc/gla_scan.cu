@@ -20,18 +20,19 @@
 #include <cuda_runtime.h>
 
 #include <cstdint>
+#include <type_traits>
 
 #include "gla_common.cuh"
 #include "gla_gate.cuh"
 #include "gla_internal.h"
+#include "tc_prims.cuh"
 
 namespace gla {
 namespace {
 
 constexpr int kWarps = 8;
 constexpr int kThreads = kWarps * 32;
-constexpr int kRows = 8;                 // rows of a warp
-constexpr int kTile = kWarps * kRows;    // rows of a block in a round; one state per tile is kept for the backward
+constexpr int kSeg = 64;  // rows between the states kept for the backward, which takes a block's rows from one of them
 constexpr int kMaxCluster = 16;
 
 struct GateForm {
@@ -86,11 +87,58 @@ __device__ __forceinline__ void stv(__nv_bfloat16* p, const float* y) {
     else *p = __float2bfloat16_rn(y[0]);
 }
 
-// a_t and w_t from the gate argument
-__device__ __forceinline__ void gate_of(const GateForm& f, float g, float& a, float& w) {
-    const float la = f.preact ? logsigmoid_f(g) * f.inv_tau : g;
-    a = expf(la);
-    w = f.leak ? -expm1f(la) : 1.f;
+// ---- gates --------------------------------------------------------------------------------
+// The library's expf / expm1f / log1pf come to about 60 instructions an element, four times what the memory
+// bandwidth leaves room for; these take 13 (a and w) and 12 (log alpha from z). Accuracies in units of u = 2^-24.
+
+// a = e^la and 1 - a for la <= 0. Near 0, where a multiplies up over many steps and 1 - a must keep its relative
+// precision: 1 - a = -la q(la) with q = (e^x - 1) / x as a polynomial fitted at the Chebyshev nodes of [-1/2, 0]
+// (relative error 3e-9), so 1 - a is within 3 u and a = 1 - (1 - a) correctly rounded from it. Below -1/2 (a < 0.61,
+// no long products): the ex2 instruction, within (4 + |la|) u.
+__device__ __forceinline__ void decay_of(float la, float& a, float& one_minus_a) {
+    float q = fmaf(0.00112340425f, la, 0.00818961393f);
+    q = fmaf(q, la, 0.0416300744f);
+    q = fmaf(q, la, 0.166662425f);
+    q = fmaf(q, la, 0.499999821f);
+    q = fmaf(q, la, 1.f);
+    const float m = -la * q;
+    const float e = tc::exp2_ftz(la * tc::kLog2e);
+    const bool near = fabsf(la) < 0.5f;
+    a = near ? 1.f - m : e;
+    one_minus_a = near ? m : 1.f - e;
+}
+
+__device__ __forceinline__ float rcp(float x) {
+    float y;
+    asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+    return y;
+}
+
+// logsigmoid(z) = min(z, 0) - log(1 + t), t = e^-|z| in [0, 1], with log(1 + t) = 2 atanh(s), s = t / (2 + t) <= 1/3:
+// atanh(s) / s as a polynomial in s^2 fitted at the Chebyshev nodes of [0, 1/9] (relative error 8e-9). Small t
+// keeps its relative precision, (8 + |z|) u in all.
+__device__ __forceinline__ float logsigmoid_series(float z, float& t) {
+    t = tc::exp2_ftz(-fabsf(z) * tc::kLog2e);
+    const float s = t * rcp(2.f + t), y = s * s;
+    float q = fmaf(0.140788898f, y, 0.139825791f);
+    q = fmaf(q, y, 0.200122982f);
+    q = fmaf(q, y, 0.333331615f);
+    q = fmaf(q, y, 1.f);
+    return fmaf(-2.f * s, q, fminf(z, 0.f));
+}
+
+// a_t and w_t from the gate argument; for a pre-activation also dlog a / dz = sigmoid(-z) / tau
+template <bool PREACT>
+__device__ __forceinline__ void gate_of(const GateForm& f, float g, float& a, float& w, float& dz) {
+    float la = g;
+    if constexpr (PREACT) {
+        float t;
+        la = logsigmoid_series(g, t) * f.inv_tau;
+        const float r = rcp(1.f + t);
+        dz = (g < 0.f ? r : t * r) * f.inv_tau;
+    }
+    decay_of(la, a, w);
+    if (!f.leak) w = 1.f;
 }
 
 // Maps of packed rows that hold a sequence's start forget everything in front of it, whatever that is: an infinity
@@ -104,7 +152,7 @@ __device__ __forceinline__ float join(float m, float s, float u) { return forget
 template <bool PACKED>
 __device__ __forceinline__ float join(float m, float f) { return forgets<PACKED>(m) ? m : m * f; }
 
-// What a warp knows of its 8 rows t0 .. t0+7: which belong to a sequence, which start or end one, and (per lane,
+// What a warp knows of its rows t0, t0 + 1, ...: which belong to a sequence, which start or end one, and (per lane,
 // for row t0 + lane) the sequence's number.
 struct RowInfo {
     uint32_t valid, start, end;
@@ -113,10 +161,11 @@ struct RowInfo {
 
 // Packed rows: the sequence of row t is the last one with cu[n] <= t. The search reads cu[0 .. B] only, whatever
 // the values are.
+template <int ROWS>
 __device__ __forceinline__ RowInfo rows_packed(const int32_t* __restrict__ cu, int B, int64_t t0, int64_t L, int lane) {
     int lo = 0, hi = B + 1;  // first entry above t lies in [lo, hi]
     const int64_t t = t0 + lane;
-    if (lane < kRows && t < L) {
+    if (lane < ROWS && t < L) {
         while (lo < hi) {
             const int mid = (lo + hi) >> 1;
             if (cu[mid] <= t) lo = mid + 1;
@@ -135,6 +184,15 @@ __device__ __forceinline__ RowInfo rows_packed(const int32_t* __restrict__ cu, i
     r.start = __ballot_sync(0xffffffffu, st);
     r.end = __ballot_sync(0xffffffffu, en);
     return r;
+}
+
+// row n of a [B,H,D] state tensor (NULL: zero)
+template <int VEC>
+__device__ __forceinline__ void state_of(const float* __restrict__ h, int64_t n, const ScanProblem& p, int64_t head,
+                                         int64_t c, float* y) {
+#pragma unroll
+    for (int v = 0; v < VEC; ++v) y[v] = 0.f;
+    if (h) ldv<VEC>(h + (n * p.H + head) * p.D + c, y);
 }
 
 // Empty sequences have no row that could write their end: out[n] = in[n] (or 0), spread over the cluster's warps.
@@ -158,14 +216,26 @@ __device__ __forceinline__ void copy_empty(const int32_t* __restrict__ cu, int B
     }
 }
 
+// A warp's rows of one tensor. Rows behind the last one repeat it, lanes behind the last channel repeat that one, so
+// the loads need no predicate; `off` is the row's offset from the warp's first row.
+template <int ROWS>
+struct RowOffsets {
+    uint32_t off[ROWS];
+    __device__ __forceinline__ RowOffsets(int64_t rows_left, int64_t D) {
+        const int last = int(rows_left < ROWS ? (rows_left < 1 ? 1 : rows_left) : ROWS) - 1;
+#pragma unroll
+        for (int j = 0; j < ROWS; ++j) off[j] = uint32_t(j < last ? j : last) * uint32_t(D);
+    }
+};
+
 // ---- forward ------------------------------------------------------------------------------
-// Grid: (sequence or head) x channel tile x cluster of `cl` blocks. Rows of round r and block q: (r cl + q) kTile.
-template <typename T, int VEC, bool PACKED>
-__global__ void __launch_bounds__(kThreads, VEC == 2 ? 3 : 4)
+// Grid: (sequence or head) x channel tile x cluster of `cl` blocks. Rows of round r and block q: from (r cl + q) TILE.
+template <typename T, int VEC, bool PACKED, bool PREACT, int ROWS>
+__global__ void __launch_bounds__(kThreads, ROWS * VEC <= 8 ? 4 : ROWS * VEC <= 16 ? 3 : 2)
     k_scan_fwd(ScanProblem p, GateForm f, int cl, const T* __restrict__ x, const float* __restrict__ la,
                const int32_t* __restrict__ cu, const float* __restrict__ h0, T* __restrict__ h, float* __restrict__ hT,
                float* __restrict__ seg) {
-    constexpr int CW = 32 * VEC;
+    constexpr int CW = 32 * VEC, TILE = kWarps * ROWS;
     __shared__ float2 agg[2][kWarps][CW];
     extern __shared__ float2 peer[];  // [2][cl][CW]
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
@@ -173,58 +243,62 @@ __global__ void __launch_bounds__(kThreads, VEC == 2 ? 3 : 4)
     const int64_t tiles = cdiv(p.D, CW);
     const int64_t id = blockIdx.x / cl, lead = id / tiles, c = (id % tiles) * CW + lane * VEC;
     const bool mine = c < p.D;
+    const int64_t cc = mine ? c : p.D - VEC;
     const int64_t head = PACKED ? lead : 0;
-    const int64_t row0 = lead * p.L;
     if (cl > 1) cluster_arrive();  // every block of the cluster has started before any puts data into it
     if constexpr (PACKED) copy_empty<VEC>(cu, int(p.B), p.H, head, p.D, c, h0, hT, rank * kWarps + warp, cl * kWarps, lane);
     float carry[VEC] = {};
-    if (!PACKED && h0 && mine) ldv<VEC>(h0 + lead * p.D + c, carry);
+    if (!PACKED && h0) ldv<VEC>(h0 + lead * p.D + cc, carry);
     if (cl > 1) cluster_wait();
-    const int64_t rounds = cdiv(p.L, int64_t(kTile) * cl), nseg = cdiv(p.L, kTile);
-    for (int64_t r = 0; r < rounds; ++r) {
-        const int par = int(r & 1);
-        const int64_t base = (r * cl + rank) * kTile, t0 = base + warp * kRows;
-        float a[kRows][VEC], b[kRows][VEC];
+    const int rounds = int(cdiv(p.L, int64_t(TILE) * cl));
+    const int64_t nseg = cdiv(p.L, kSeg);
+    for (int r = 0; r < rounds; ++r) {
+        const int par = r & 1;
+        const int64_t t0 = (int64_t(r) * cl + rank) * TILE + warp * ROWS;
+        const int64_t first = (lead * p.L + (t0 < p.L ? t0 : p.L - 1)) * p.D + cc;
+        const RowOffsets<ROWS> ro(p.L - t0, p.D);
+        float a[ROWS][VEC], b[ROWS][VEC];
 #pragma unroll
-        for (int j = 0; j < kRows; ++j) {
-            const int64_t i = (row0 + t0 + j) * p.D + c;
+        for (int j = 0; j < ROWS; ++j) ldv<VEC>(la + first + ro.off[j], a[j]);
 #pragma unroll
-            for (int v = 0; v < VEC; ++v) a[j][v] = b[j][v] = 0.f;
-            if (mine && t0 + j < p.L) {
-                ldv<VEC>(la + i, a[j]);
-                ldv<VEC>(x + i, b[j]);
+        for (int j = 0; j < ROWS; ++j) ldv<VEC>(x + first + ro.off[j], b[j]);
+        RowInfo ri{0, 0, 0, 0};
+        if constexpr (PACKED) ri = rows_packed<ROWS>(cu, int(p.B), t0, p.L, lane);
+        else ri.valid = t0 + ROWS <= p.L ? ~0u : t0 < p.L ? (1u << (p.L - t0)) - 1 : 0u;
+#pragma unroll
+        for (int j = 0; j < ROWS; ++j) {
+#pragma unroll
+            for (int v = 0; v < VEC; ++v) {
+                float w, dz;
+                gate_of<PREACT>(f, a[j][v], a[j][v], w, dz);
+                b[j][v] *= w;
             }
         }
-        RowInfo ri;
-        if constexpr (PACKED) ri = rows_packed(cu, int(p.B), t0, p.L, lane);
+        constexpr uint32_t kAll = ROWS == 32 ? ~0u : (1u << ROWS) - 1;
+        if ((ri.valid & kAll) != kAll) {
+#pragma unroll
+            for (int j = 0; j < ROWS; ++j) {
+                if (!(ri.valid >> j & 1)) {
+#pragma unroll
+                    for (int v = 0; v < VEC; ++v) a[j][v] = 1.f, b[j][v] = 0.f;
+                }
+            }
+        }
         float A[VEC], U[VEC];
 #pragma unroll
         for (int v = 0; v < VEC; ++v) A[v] = 1.f, U[v] = 0.f;
 #pragma unroll
-        for (int j = 0; j < kRows; ++j) {
-            const bool ok = PACKED ? (ri.valid >> j & 1) : t0 + j < p.L;
-            float s0[VEC] = {};
-            bool start = false;
-            if constexpr (PACKED) {
-                start = ri.start >> j & 1;
-                if (start) {
-                    const int64_t n = __shfl_sync(0xffffffffu, ri.n, j);
-                    if (h0 && mine) ldv<VEC>(h0 + (n * p.H + head) * p.D + c, s0);
-                }
-            }
+        for (int j = 0; j < ROWS; ++j) {
+            if (PACKED && (ri.start >> j & 1)) state_of<VEC>(h0, __shfl_sync(0xffffffffu, ri.n, j), p, head, cc, U);
 #pragma unroll
             for (int v = 0; v < VEC; ++v) {
-                float aa, w;
-                gate_of(f, a[j][v], aa, w);
-                b[j][v] = ok ? w * b[j][v] : 0.f;
-                a[j][v] = ok ? aa : 1.f;
-                if (start) {
-                    b[j][v] = fmaf(aa, s0[v], b[j][v]);
-                    a[j][v] = kForget;
-                }
-                A[v] = join<PACKED>(a[j][v], A[v]);
-                U[v] = join<PACKED>(a[j][v], U[v], b[j][v]);
+                A[v] *= a[j][v];
+                U[v] = fmaf(a[j][v], U[v], b[j][v]);
             }
+        }
+        if (PACKED && ri.start) {
+#pragma unroll
+            for (int v = 0; v < VEC; ++v) A[v] = kForget;
         }
 #pragma unroll
         for (int v = 0; v < VEC; ++v) agg[par][warp][v * 32 + lane] = make_float2(A[v], U[v]);
@@ -233,12 +307,15 @@ __global__ void __launch_bounds__(kThreads, VEC == 2 ? 3 : 4)
         float pa[VEC], pu[VEC];
 #pragma unroll
         for (int v = 0; v < VEC; ++v) pa[v] = 1.f, pu[v] = 0.f;
-        for (int w = 0; w < warp; ++w) {
 #pragma unroll
-            for (int v = 0; v < VEC; ++v) {
-                const float2 m = agg[par][w][v * 32 + lane];
-                pa[v] = join<PACKED>(m.x, pa[v]);
-                pu[v] = join<PACKED>(m.x, pu[v], m.y);
+        for (int w = 0; w < kWarps - 1; ++w) {
+            if (w < warp) {
+#pragma unroll
+                for (int v = 0; v < VEC; ++v) {
+                    const float2 m = agg[par][w][v * 32 + lane];
+                    pa[v] = join<PACKED>(m.x, pa[v]);
+                    pu[v] = join<PACKED>(m.x, pu[v], m.y);
+                }
             }
         }
         float in[VEC];  // state entering the block's rows
@@ -273,38 +350,36 @@ __global__ void __launch_bounds__(kThreads, VEC == 2 ? 3 : 4)
                 carry[v] = join<PACKED>(ta, in[v], tu);
             }
         }
-        if (seg && warp == 0 && mine && base < p.L) stv<VEC>(seg + (lead * nseg + base / kTile) * p.D + c, in);
         float s[VEC];
 #pragma unroll
         for (int v = 0; v < VEC; ++v) s[v] = join<PACKED>(pa[v], in[v], pu[v]);
+        if (seg && mine && t0 < p.L && t0 % kSeg == 0) stv<VEC>(seg + (lead * nseg + t0 / kSeg) * p.D + c, s);
 #pragma unroll
-        for (int j = 0; j < kRows; ++j) {
+        for (int j = 0; j < ROWS; ++j) {
+            if (PACKED && (ri.start >> j & 1)) state_of<VEC>(h0, __shfl_sync(0xffffffffu, ri.n, j), p, head, cc, s);
 #pragma unroll
-            for (int v = 0; v < VEC; ++v) s[v] = join<PACKED>(a[j][v], s[v], b[j][v]);
-            const bool ok = PACKED ? (ri.valid >> j & 1) : t0 + j < p.L;
-            if (h && ok && mine) stv<VEC>(h + (row0 + t0 + j) * p.D + c, s);
-            if constexpr (PACKED) {
-                if (ri.end >> j & 1) {
-                    const int64_t n = __shfl_sync(0xffffffffu, ri.n, j);
-                    if (hT && mine) stv<VEC>(hT + (n * p.H + head) * p.D + c, s);
-                }
+            for (int v = 0; v < VEC; ++v) s[v] = fmaf(a[j][v], s[v], b[j][v]);
+            if (h && mine && (ri.valid >> j & 1)) stv<VEC>(h + first + ro.off[j], s);
+            if (PACKED && (ri.end >> j & 1)) {
+                const int64_t n = __shfl_sync(0xffffffffu, ri.n, j);
+                if (hT && mine) stv<VEC>(hT + (n * p.H + head) * p.D + c, s);
             }
         }
-        // rows behind the last one leave the state as it is, so any warp from there on holds hT
-        if (!PACKED && hT && mine && t0 < p.L && t0 + kRows >= p.L) stv<VEC>(hT + lead * p.D + c, s);
+        // rows behind the last one leave the state as it is, so the warp with the last row holds hT
+        if (!PACKED && hT && mine && t0 < p.L && t0 + ROWS >= p.L) stv<VEC>(hT + lead * p.D + c, s);
     }
 }
 
 // ---- backward -----------------------------------------------------------------------------
 // Rounds, blocks and warps as in the forward, from the last round to the first. The states inside a block's rows
 // are recomputed in fp32 from the state that enters them (seg).
-template <typename T, int VEC, bool PACKED>
+template <typename T, int VEC, bool PACKED, bool PREACT>
 __global__ void __launch_bounds__(kThreads, 2)
     k_scan_bwd(ScanProblem p, GateForm f, int cl, const T* __restrict__ x, const float* __restrict__ la,
                const int32_t* __restrict__ cu, const float* __restrict__ h0, const T* __restrict__ dh,
                const float* __restrict__ dhT, T* __restrict__ dx, float* __restrict__ dla, float* __restrict__ dh0,
                const float* __restrict__ seg) {
-    constexpr int CW = 32 * VEC;
+    constexpr int CW = 32 * VEC, ROWS = kSeg / kWarps;
     __shared__ float2 aggu[2][kWarps][CW];
     __shared__ float aggy[2][kWarps][CW];
     extern __shared__ float2 peer[];  // [2][cl][CW]
@@ -313,71 +388,76 @@ __global__ void __launch_bounds__(kThreads, 2)
     const int64_t tiles = cdiv(p.D, CW);
     const int64_t id = blockIdx.x / cl, lead = id / tiles, c = (id % tiles) * CW + lane * VEC;
     const bool mine = c < p.D;
+    const int64_t cc = mine ? c : p.D - VEC;
     const int64_t head = PACKED ? lead : 0;
-    const int64_t row0 = lead * p.L;
     if (cl > 1) cluster_arrive();
     if constexpr (PACKED) copy_empty<VEC>(cu, int(p.B), p.H, head, p.D, c, dhT, dh0, rank * kWarps + warp, cl * kWarps, lane);
     float carry[VEC] = {};  // y of the row behind the round's last
-    if (!PACKED && dhT && mine) ldv<VEC>(dhT + lead * p.D + c, carry);
+    if (!PACKED && dhT) ldv<VEC>(dhT + lead * p.D + cc, carry);
     if (cl > 1) cluster_wait();
-    const int64_t rounds = cdiv(p.L, int64_t(kTile) * cl), nseg = cdiv(p.L, kTile);
-    for (int64_t r = rounds - 1; r >= 0; --r) {
-        const int par = int(r & 1);
-        const int64_t base = (r * cl + rank) * kTile, t0 = base + warp * kRows;
-        float a[kRows][VEC], b[kRows][VEC], z[kRows][VEC], xv[kRows][VEC], d[kRows][VEC], w[kRows][VEC];
-        float s[VEC] = {};  // state entering the block's rows
-        if (mine && base < p.L) ldv<VEC>(seg + (lead * nseg + base / kTile) * p.D + c, s);
+    const int rounds = int(cdiv(p.L, int64_t(kSeg) * cl));
+    const int64_t nseg = cdiv(p.L, kSeg);
+    for (int r = rounds - 1; r >= 0; --r) {
+        const int par = r & 1;
+        const int64_t tile = int64_t(r) * cl + rank, t0 = tile * kSeg + warp * ROWS;
+        const int64_t first = (lead * p.L + (t0 < p.L ? t0 : p.L - 1)) * p.D + cc;
+        const RowOffsets<ROWS> ro(p.L - t0, p.D);
+        float a[ROWS][VEC], w[ROWS][VEC], xv[ROWS][VEC], d[ROWS][VEC], dz[ROWS][VEC];
+        float s[VEC];  // state entering the block's rows
+        ldv<VEC>(seg + (lead * nseg + (tile < nseg ? tile : nseg - 1)) * p.D + cc, s);
 #pragma unroll
-        for (int j = 0; j < kRows; ++j) {
-            const int64_t i = (row0 + t0 + j) * p.D + c;
+        for (int j = 0; j < ROWS; ++j) ldv<VEC>(la + first + ro.off[j], a[j]);
 #pragma unroll
-            for (int v = 0; v < VEC; ++v) z[j][v] = xv[j][v] = d[j][v] = 0.f;
-            if (mine && t0 + j < p.L) {
-                ldv<VEC>(la + i, z[j]);
-                ldv<VEC>(x + i, xv[j]);
-                ldv<VEC>(dh + i, d[j]);
+        for (int j = 0; j < ROWS; ++j) ldv<VEC>(x + first + ro.off[j], xv[j]);
+#pragma unroll
+        for (int j = 0; j < ROWS; ++j) ldv<VEC>(dh + first + ro.off[j], d[j]);
+        RowInfo ri{0, 0, 0, 0};
+        if constexpr (PACKED) ri = rows_packed<ROWS>(cu, int(p.B), t0, p.L, lane);
+        else ri.valid = t0 + ROWS <= p.L ? ~0u : t0 < p.L ? (1u << (p.L - t0)) - 1 : 0u;
+#pragma unroll
+        for (int j = 0; j < ROWS; ++j) {
+#pragma unroll
+            for (int v = 0; v < VEC; ++v) gate_of<PREACT>(f, a[j][v], a[j][v], w[j][v], dz[j][v]);
+        }
+        constexpr uint32_t kAll = (1u << ROWS) - 1;
+        if ((ri.valid & kAll) != kAll) {
+#pragma unroll
+            for (int j = 0; j < ROWS; ++j) {
+                if (!(ri.valid >> j & 1)) {
+#pragma unroll
+                    for (int v = 0; v < VEC; ++v) a[j][v] = 1.f, w[j][v] = 0.f, xv[j][v] = 0.f, d[j][v] = 0.f;
+                }
             }
         }
-        RowInfo ri;
-        if constexpr (PACKED) ri = rows_packed(cu, int(p.B), t0, p.L, lane);
         float A[VEC], U[VEC], Y[VEC];
 #pragma unroll
         for (int v = 0; v < VEC; ++v) A[v] = 1.f, U[v] = 0.f, Y[v] = 0.f;
 #pragma unroll
-        for (int j = 0; j < kRows; ++j) {
-            const bool ok = PACKED ? (ri.valid >> j & 1) : t0 + j < p.L;
-            float s0[VEC] = {}, e0[VEC] = {};
-            bool start = false;
-            if constexpr (PACKED) {
-                start = ri.start >> j & 1;
-                const bool end = ri.end >> j & 1;
-                if (start || end) {
-                    const int64_t n = __shfl_sync(0xffffffffu, ri.n, j);
-                    if (start && h0 && mine) ldv<VEC>(h0 + (n * p.H + head) * p.D + c, s0);
-                    if (end && dhT && mine) ldv<VEC>(dhT + (n * p.H + head) * p.D + c, e0);
-                }
-            }
+        for (int j = 0; j < ROWS; ++j) {
+            if (PACKED && (ri.start >> j & 1)) state_of<VEC>(h0, __shfl_sync(0xffffffffu, ri.n, j), p, head, cc, U);
 #pragma unroll
             for (int v = 0; v < VEC; ++v) {
-                gate_of(f, z[j][v], a[j][v], w[j][v]);
-                if (!ok) a[j][v] = 1.f, w[j][v] = 0.f, xv[j][v] = 0.f, d[j][v] = 0.f;
-                d[j][v] += e0[v];
-                b[j][v] = w[j][v] * xv[j][v];
-                if (start) {
-                    b[j][v] = fmaf(a[j][v], s0[v], b[j][v]);
-                    A[v] = kForget;
-                    U[v] = b[j][v];
-                } else {
-                    A[v] = join<PACKED>(A[v], a[j][v]);  // of both directions: U and Y carry what the other rows hold
-                    U[v] = fmaf(a[j][v], U[v], b[j][v]);
-                }
+                A[v] *= a[j][v];
+                U[v] = fmaf(a[j][v], U[v], w[j][v] * xv[j][v]);
             }
         }
 #pragma unroll
-        for (int j = kRows - 1; j >= 0; --j) {
-            const bool start = PACKED ? (ri.start >> j & 1) : false;
+        for (int j = ROWS - 1; j >= 0; --j) {
+            if (PACKED && (ri.end >> j & 1)) {  // the gradient of the last state enters here, in place of the next row's
+                float e[VEC];
+                state_of<VEC>(dhT, __shfl_sync(0xffffffffu, ri.n, j), p, head, cc, e);
 #pragma unroll
-            for (int v = 0; v < VEC; ++v) Y[v] = start ? 0.f : a[j][v] * (d[j][v] + Y[v]);
+                for (int v = 0; v < VEC; ++v) d[j][v] += e[v];
+            }
+#pragma unroll
+            for (int v = 0; v < VEC; ++v) {
+                Y[v] = a[j][v] * (d[j][v] + Y[v]);
+                if (PACKED && (ri.start >> j & 1)) Y[v] = 0.f;
+            }
+        }
+        if (PACKED && ri.start) {  // of both directions: U and Y carry what the warp's other rows hold
+#pragma unroll
+            for (int v = 0; v < VEC; ++v) A[v] = kForget;
         }
 #pragma unroll
         for (int v = 0; v < VEC; ++v) {
@@ -385,23 +465,28 @@ __global__ void __launch_bounds__(kThreads, 2)
             aggy[par][warp][v * 32 + lane] = Y[v];
         }
         __syncthreads();
-        for (int q = 0; q < warp; ++q) {
-#pragma unroll
-            for (int v = 0; v < VEC; ++v) {
-                const float2 m = aggu[par][q][v * 32 + lane];
-                s[v] = join<PACKED>(m.x, s[v], m.y);
-            }
-        }
-        // the map (of y) of the block's rows behind this warp's
-        float pa[VEC], py[VEC];
+        float pa[VEC], py[VEC];  // the map (of y) of the block's rows behind this warp's
 #pragma unroll
         for (int v = 0; v < VEC; ++v) pa[v] = 1.f, py[v] = 0.f;
-        for (int q = kWarps - 1; q > warp; --q) {
 #pragma unroll
-            for (int v = 0; v < VEC; ++v) {
-                const float m = aggu[par][q][v * 32 + lane].x;
-                pa[v] = join<PACKED>(m, pa[v]);
-                py[v] = join<PACKED>(m, py[v], aggy[par][q][v * 32 + lane]);
+        for (int q = 0; q < kWarps; ++q) {
+            if (q < warp) {
+#pragma unroll
+                for (int v = 0; v < VEC; ++v) {
+                    const float2 m = aggu[par][q][v * 32 + lane];
+                    s[v] = join<PACKED>(m.x, s[v], m.y);
+                }
+            }
+        }
+#pragma unroll
+        for (int q = kWarps - 1; q > 0; --q) {
+            if (q > warp) {
+#pragma unroll
+                for (int v = 0; v < VEC; ++v) {
+                    const float m = aggu[par][q][v * 32 + lane].x;
+                    pa[v] = join<PACKED>(m, pa[v]);
+                    py[v] = join<PACKED>(m, py[v], aggy[par][q][v * 32 + lane]);
+                }
             }
         }
         float in[VEC];
@@ -436,47 +521,37 @@ __global__ void __launch_bounds__(kThreads, 2)
                 carry[v] = join<PACKED>(ta, in[v], ty);
             }
         }
-        float y[VEC], hp[kRows][VEC];
+        float y[VEC];
 #pragma unroll
         for (int v = 0; v < VEC; ++v) y[v] = join<PACKED>(pa[v], in[v], py[v]);
-        // states in front of each row
+        // xv becomes what dlog a_t multiplies: h_{t-1}, less x_t where the input's weight is 1 - a
 #pragma unroll
-        for (int j = 0; j < kRows; ++j) {
-            const bool start = PACKED ? (ri.start >> j & 1) : false;
+        for (int j = 0; j < ROWS; ++j) {
+            if (PACKED && (ri.start >> j & 1)) state_of<VEC>(h0, __shfl_sync(0xffffffffu, ri.n, j), p, head, cc, s);
 #pragma unroll
             for (int v = 0; v < VEC; ++v) {
-                hp[j][v] = s[v];
-                s[v] = start ? b[j][v] : fmaf(a[j][v], s[v], b[j][v]);
+                const float xj = xv[j][v];
+                xv[j][v] = f.leak ? s[v] - xj : s[v];
+                s[v] = fmaf(a[j][v], s[v], w[j][v] * xj);
             }
         }
 #pragma unroll
-        for (int j = kRows - 1; j >= 0; --j) {
-            const bool ok = PACKED ? (ri.valid >> j & 1) : t0 + j < p.L;
-            float o1[VEC], o2[VEC], s0[VEC] = {};
-            bool start = false;
-            int64_t n = 0;
-            if constexpr (PACKED) {
-                start = ri.start >> j & 1;
-                if (start) {
-                    n = __shfl_sync(0xffffffffu, ri.n, j);
-                    if (h0 && mine) ldv<VEC>(h0 + (n * p.H + head) * p.D + c, s0);
-                }
-            }
+        for (int j = ROWS - 1; j >= 0; --j) {
+            float o1[VEC], o2[VEC];
 #pragma unroll
             for (int v = 0; v < VEC; ++v) {
                 const float g = d[j][v] + y[v];
-                const float hm = start ? s0[v] : hp[j][v];
                 y[v] = a[j][v] * g;
                 o1[v] = w[j][v] * g;
-                o2[v] = y[v] * (f.leak ? hm - xv[j][v] : hm);
-                if (f.preact) o2[v] *= sigmoid_neg_f(z[j][v]) * f.inv_tau;
+                o2[v] = y[v] * xv[j][v];
+                if constexpr (PREACT) o2[v] *= dz[j][v];
             }
-            if (ok && mine) {
-                const int64_t i = (row0 + t0 + j) * p.D + c;
-                stv<VEC>(dx + i, o1);
-                stv<VEC>(dla + i, o2);
+            if (mine && (ri.valid >> j & 1)) {
+                stv<VEC>(dx + first + ro.off[j], o1);
+                stv<VEC>(dla + first + ro.off[j], o2);
             }
-            if (start) {
+            if (PACKED && (ri.start >> j & 1)) {
+                const int64_t n = __shfl_sync(0xffffffffu, ri.n, j);
                 if (dh0 && mine) stv<VEC>(dh0 + (n * p.H + head) * p.D + c, y);
 #pragma unroll
                 for (int v = 0; v < VEC; ++v) y[v] = 0.f;
@@ -518,7 +593,9 @@ __global__ void __launch_bounds__(kStepThreads) k_scan_step(ScanProblem p, GateF
     float y = 0.f;
     if (live) {
         float a, w;
-        gate_of(f, la[b * n + c], a, w);
+        float dz;
+        if (f.preact) gate_of<true>(f, la[b * n + c], a, w, dz);
+        else gate_of<false>(f, la[b * n + c], a, w, dz);
         y = fmaf(a, state[slot * n + c], w * ldf(x + b * n + c));
         state[slot * n + c] = y;
     }
@@ -529,8 +606,8 @@ GateForm form(const ScanProblem& p) { return GateForm{p.preact, p.leak, p.inv_ta
 
 // Blocks per cluster: enough to fill the SMs (three blocks of 256 threads on each) where the sequences and channel
 // tiles alone do not, but no more than there are row tiles.
-int cluster_size(int64_t groups, int64_t L) {
-    const int64_t tiles = cdiv(L, kTile);
+int cluster_size(int64_t groups, int64_t L, int tile) {
+    const int64_t tiles = cdiv(L, tile);
     int cl = 1;
     while (cl < kMaxCluster && cl < tiles && groups * cl < 148 * 3) cl *= 2;
     return cl;
@@ -557,22 +634,24 @@ gla_status launch_clusters(const char* name, K kernel, int64_t groups, int cl, i
     return launch_end(name, s);
 }
 
-template <typename T, int VEC, bool PACKED>
+constexpr int kFwdRows = 8;
+
+template <typename T, int VEC, bool PACKED, bool PREACT>
 gla_status fwd_typed(const ScanProblem& p, const void* x, const float* la, const int32_t* cu, const float* h0,
                      void* h, float* hT, float* seg, cudaStream_t s) {
     const int64_t groups = (PACKED ? p.H : p.B * p.H) * cdiv(p.D, 32 * VEC);
-    const int cl = cluster_size(groups, p.L);
-    return launch_clusters("scan_fwd", k_scan_fwd<T, VEC, PACKED>, groups, cl, VEC, s, p, form(p), cl,
+    const int cl = cluster_size(groups, p.L, kWarps * kFwdRows);
+    return launch_clusters("scan_fwd", k_scan_fwd<T, VEC, PACKED, PREACT, kFwdRows>, groups, cl, VEC, s, p, form(p), cl,
                            static_cast<const T*>(x), la, cu, h0, static_cast<T*>(h), hT, seg);
 }
 
-template <typename T, int VEC, bool PACKED>
+template <typename T, int VEC, bool PACKED, bool PREACT>
 gla_status bwd_typed(const ScanProblem& p, const void* x, const float* la, const int32_t* cu, const float* h0,
                      const void* dh, const float* dhT, void* dx, float* dla, float* dh0, const float* seg,
                      cudaStream_t s) {
     const int64_t groups = (PACKED ? p.H : p.B * p.H) * cdiv(p.D, 32 * VEC);
-    const int cl = cluster_size(groups, p.L);
-    return launch_clusters("scan_bwd", k_scan_bwd<T, VEC, PACKED>, groups, cl, VEC, s, p, form(p), cl,
+    const int cl = cluster_size(groups, p.L, kSeg);
+    return launch_clusters("scan_bwd", k_scan_bwd<T, VEC, PACKED, PREACT>, groups, cl, VEC, s, p, form(p), cl,
                            static_cast<const T*>(x), la, cu, h0, static_cast<const T*>(dh), dhT, static_cast<T*>(dx),
                            dla, dh0, seg);
 }
@@ -586,25 +665,34 @@ gla_status step_typed(const ScanProblem& p, const void* x, const float* la, cons
     return GLA_OK;
 }
 
-// Two channels a lane where the rows' pairs are aligned (an even width), else one.
-#define GLA_SCAN_DISPATCH(fn, ...)                                                                         \
-    (p.bf16 ? (p.D % 2 == 0 ? (p.packed ? fn<__nv_bfloat16, 2, true>(__VA_ARGS__)                          \
-                                        : fn<__nv_bfloat16, 2, false>(__VA_ARGS__))                        \
-                            : (p.packed ? fn<__nv_bfloat16, 1, true>(__VA_ARGS__)                          \
-                                        : fn<__nv_bfloat16, 1, false>(__VA_ARGS__)))                       \
-            : (p.D % 2 == 0 ? (p.packed ? fn<float, 2, true>(__VA_ARGS__) : fn<float, 2, false>(__VA_ARGS__)) \
-                            : (p.packed ? fn<float, 1, true>(__VA_ARGS__) : fn<float, 1, false>(__VA_ARGS__))))
+// Calls fn(type tag, channels a lane, packed, pre-activation) with compile-time values: two channels a lane where the
+// rows' pairs are aligned (an even width), else one.
+template <typename F>
+gla_status dispatch(const ScanProblem& p, F fn) {
+    const auto by_form = [&](auto type, auto vec) {
+        if (p.packed) return p.preact ? fn(type, vec, std::true_type{}, std::true_type{})
+                                      : fn(type, vec, std::true_type{}, std::false_type{});
+        return p.preact ? fn(type, vec, std::false_type{}, std::true_type{})
+                        : fn(type, vec, std::false_type{}, std::false_type{});
+    };
+    using One = std::integral_constant<int, 1>;
+    using Two = std::integral_constant<int, 2>;
+    if (p.bf16) return p.D % 2 == 0 ? by_form(__nv_bfloat16{}, Two{}) : by_form(__nv_bfloat16{}, One{});
+    return p.D % 2 == 0 ? by_form(float{}, Two{}) : by_form(float{}, One{});
+}
 
 }  // namespace
 
 size_t scan_workspace(const ScanProblem& p, Arena& a) {
-    (void)a.take<float>(size_t((p.packed ? p.H : p.B * p.H) * cdiv(p.L, kTile) * p.D));
+    (void)a.take<float>(size_t((p.packed ? p.H : p.B * p.H) * cdiv(p.L, kSeg) * p.D));
     return a.used;
 }
 
 gla_status scan_fwd(const ScanProblem& p, const void* x, const float* la, const int32_t* cu, const float* h0, void* h,
                     float* hT, float* seg, cudaStream_t s) {
-    return GLA_SCAN_DISPATCH(fwd_typed, p, x, la, cu, h0, h, hT, seg, s);
+    return dispatch(p, [&](auto type, auto vec, auto packed, auto preact) {
+        return fwd_typed<decltype(type), vec(), packed(), preact()>(p, x, la, cu, h0, h, hT, seg, s);
+    });
 }
 
 gla_status scan_bwd(const ScanProblem& p, const void* x, const float* la, const int32_t* cu, const float* h0,
@@ -614,7 +702,9 @@ gla_status scan_bwd(const ScanProblem& p, const void* x, const float* la, const 
         const gla_status st = scan_fwd(p, x, la, cu, h0, nullptr, nullptr, seg, s);
         if (st != GLA_OK) return st;
     }
-    return GLA_SCAN_DISPATCH(bwd_typed, p, x, la, cu, h0, dh, dhT, dx, dla, dh0, seg, s);
+    return dispatch(p, [&](auto type, auto vec, auto packed, auto preact) {
+        return bwd_typed<decltype(type), vec(), packed(), preact()>(p, x, la, cu, h0, dh, dhT, dx, dla, dh0, seg, s);
+    });
 }
 
 gla_status scan_step(const ScanProblem& p, const void* x, const float* la, const int32_t* slots, int64_t pool,
