@@ -228,16 +228,52 @@ struct RowOffsets {
     }
 };
 
+// ---- staged loads -------------------------------------------------------------------------
+// The rows of the next round travel while this one is computed: every lane copies its own channels into its own
+// places of shared memory (cp.async, 4 or 8 bytes a row), so that no thread waits for another's copies and two
+// rounds' rows cost no registers. Single bf16 channels (an odd width) are too narrow for such a copy and are loaded
+// where they are used.
+template <int BYTES>
+__device__ __forceinline__ void copy_async(void* dst, const void* src) {
+    asm volatile("cp.async.ca.shared.global [%0], [%1], %2;" ::"r"(tc::smem_u32(dst)), "l"(src), "n"(BYTES) : "memory");
+}
+__device__ __forceinline__ void copies_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
+template <int N>
+__device__ __forceinline__ void copies_wait() { asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory"); }
+
+template <typename T, int VEC>
+constexpr bool kStaged = sizeof(T) * VEC >= 4;
+
+// A lane's rows of one tensor in shared memory: row j at [j][lane].
+template <typename T, int VEC, int ROWS>
+__device__ __forceinline__ void stage_rows(T* st, const T* src, const RowOffsets<ROWS>& ro) {
+    if constexpr (kStaged<T, VEC>) {
+#pragma unroll
+        for (int j = 0; j < ROWS; ++j) copy_async<sizeof(T) * VEC>(st + j * 32 * VEC, src + ro.off[j]);
+    }
+}
+template <typename T, int VEC>
+__device__ __forceinline__ void take_row(const T* st, const T* src, uint32_t off, int j, float* y) {
+    if constexpr (kStaged<T, VEC>) ldv<VEC>(st + j * 32 * VEC, y);
+    else ldv<VEC>(src + off, y);
+}
+
+// bytes a warp's stage takes
+template <typename T, int VEC, int ROWS>
+constexpr int kFwdStage = ROWS * 32 * VEC * int(4 + sizeof(T));
+template <typename T, int VEC, int ROWS>
+constexpr int kBwdStage = ROWS * 32 * VEC * int(4 + 2 * sizeof(T));
+
 // ---- forward ------------------------------------------------------------------------------
 // Grid: (sequence or head) x channel tile x cluster of `cl` blocks. Rows of round r and block q: from (r cl + q) TILE.
 template <typename T, int VEC, bool PACKED, bool PREACT, int ROWS>
-__global__ void __launch_bounds__(kThreads, ROWS * VEC <= 8 ? 4 : ROWS * VEC <= 16 ? 3 : 2)
+__global__ void __launch_bounds__(kThreads, ROWS * VEC <= 16 ? 3 : 2)
     k_scan_fwd(ScanProblem p, GateForm f, int cl, const T* __restrict__ x, const float* __restrict__ la,
                const int32_t* __restrict__ cu, const float* __restrict__ h0, T* __restrict__ h, float* __restrict__ hT,
                float* __restrict__ seg) {
     constexpr int CW = 32 * VEC, TILE = kWarps * ROWS;
     __shared__ float2 agg[2][kWarps][CW];
-    extern __shared__ float2 peer[];  // [2][cl][CW]
+    extern __shared__ float2 peer[];  // [2][cl][CW] the blocks' maps, then the warps' stages
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     const int rank = cl > 1 ? int(cluster_rank()) : 0;
     const int64_t tiles = cdiv(p.D, CW);
@@ -245,6 +281,21 @@ __global__ void __launch_bounds__(kThreads, ROWS * VEC <= 8 ? 4 : ROWS * VEC <= 
     const bool mine = c < p.D;
     const int64_t cc = mine ? c : p.D - VEC;
     const int64_t head = PACKED ? lead : 0;
+    char* stages = reinterpret_cast<char*>(peer + (cl > 1 ? 2 * cl * CW : 0)) + warp * 2 * kFwdStage<T, VEC, ROWS>;
+    const auto row_of = [&](int r) { return (int64_t(r) * cl + rank) * TILE + warp * ROWS; };
+    const auto first_of = [&](int64_t t) { return (lead * p.L + (t < p.L ? t : p.L - 1)) * p.D + cc; };
+    const auto gates_at = [&](int par) { return reinterpret_cast<float*>(stages + par * kFwdStage<T, VEC, ROWS>) + lane * VEC; };
+    const auto x_at = [&](int par) {
+        return reinterpret_cast<T*>(stages + par * kFwdStage<T, VEC, ROWS> + ROWS * CW * 4) + lane * VEC;
+    };
+    const auto stage = [&](int r) {
+        const int64_t t = row_of(r), i = first_of(t);
+        const RowOffsets<ROWS> ro(p.L - t, p.D);
+        stage_rows<float, VEC, ROWS>(gates_at(r & 1), la + i, ro);
+        stage_rows<T, VEC, ROWS>(x_at(r & 1), x + i, ro);
+    };
+    stage(0);
+    copies_commit();
     if (cl > 1) cluster_arrive();  // every block of the cluster has started before any puts data into it
     if constexpr (PACKED) copy_empty<VEC>(cu, int(p.B), p.H, head, p.D, c, h0, hT, rank * kWarps + warp, cl * kWarps, lane);
     float carry[VEC] = {};
@@ -254,14 +305,17 @@ __global__ void __launch_bounds__(kThreads, ROWS * VEC <= 8 ? 4 : ROWS * VEC <= 
     const int64_t nseg = cdiv(p.L, kSeg);
     for (int r = 0; r < rounds; ++r) {
         const int par = r & 1;
-        const int64_t t0 = (int64_t(r) * cl + rank) * TILE + warp * ROWS;
-        const int64_t first = (lead * p.L + (t0 < p.L ? t0 : p.L - 1)) * p.D + cc;
+        const int64_t t0 = row_of(r), first = first_of(t0);
         const RowOffsets<ROWS> ro(p.L - t0, p.D);
+        if (r + 1 < rounds) stage(r + 1);
+        copies_commit();
+        copies_wait<1>();
         float a[ROWS][VEC], b[ROWS][VEC];
 #pragma unroll
-        for (int j = 0; j < ROWS; ++j) ldv<VEC>(la + first + ro.off[j], a[j]);
-#pragma unroll
-        for (int j = 0; j < ROWS; ++j) ldv<VEC>(x + first + ro.off[j], b[j]);
+        for (int j = 0; j < ROWS; ++j) {
+            ldv<VEC>(gates_at(par) + j * CW, a[j]);
+            take_row<T, VEC>(x_at(par), x + first, ro.off[j], j, b[j]);
+        }
         RowInfo ri{0, 0, 0, 0};
         if constexpr (PACKED) ri = rows_packed<ROWS>(cu, int(p.B), t0, p.L, lane);
         else ri.valid = t0 + ROWS <= p.L ? ~0u : t0 < p.L ? (1u << (p.L - t0)) - 1 : 0u;
@@ -382,7 +436,7 @@ __global__ void __launch_bounds__(kThreads, 2)
     constexpr int CW = 32 * VEC, ROWS = kSeg / kWarps;
     __shared__ float2 aggu[2][kWarps][CW];
     __shared__ float aggy[2][kWarps][CW];
-    extern __shared__ float2 peer[];  // [2][cl][CW]
+    extern __shared__ float2 peer[];  // [2][cl][CW] the blocks' maps, then the warps' stages
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     const int rank = cl > 1 ? int(cluster_rank()) : 0;
     const int64_t tiles = cdiv(p.D, CW);
@@ -390,27 +444,46 @@ __global__ void __launch_bounds__(kThreads, 2)
     const bool mine = c < p.D;
     const int64_t cc = mine ? c : p.D - VEC;
     const int64_t head = PACKED ? lead : 0;
+    char* stages = reinterpret_cast<char*>(peer + (cl > 1 ? 2 * cl * CW : 0)) + warp * 2 * kBwdStage<T, VEC, ROWS>;
+    const auto row_of = [&](int r) { return (int64_t(r) * cl + rank) * kSeg + warp * ROWS; };
+    const auto first_of = [&](int64_t t) { return (lead * p.L + (t < p.L ? t : p.L - 1)) * p.D + cc; };
+    const auto gates_at = [&](int par) { return reinterpret_cast<float*>(stages + par * kBwdStage<T, VEC, ROWS>) + lane * VEC; };
+    const auto x_at = [&](int par) {
+        return reinterpret_cast<T*>(stages + par * kBwdStage<T, VEC, ROWS> + ROWS * CW * 4) + lane * VEC;
+    };
+    const auto dh_at = [&](int par) { return x_at(par) + ROWS * CW; };
+    const auto stage = [&](int r) {
+        const int64_t t = row_of(r), i = first_of(t);
+        const RowOffsets<ROWS> ro(p.L - t, p.D);
+        stage_rows<float, VEC, ROWS>(gates_at(r & 1), la + i, ro);
+        stage_rows<T, VEC, ROWS>(x_at(r & 1), x + i, ro);
+        stage_rows<T, VEC, ROWS>(dh_at(r & 1), dh + i, ro);
+    };
+    const int rounds = int(cdiv(p.L, int64_t(kSeg) * cl));
+    stage(rounds - 1);
+    copies_commit();
     if (cl > 1) cluster_arrive();
     if constexpr (PACKED) copy_empty<VEC>(cu, int(p.B), p.H, head, p.D, c, dhT, dh0, rank * kWarps + warp, cl * kWarps, lane);
     float carry[VEC] = {};  // y of the row behind the round's last
     if (!PACKED && dhT) ldv<VEC>(dhT + lead * p.D + cc, carry);
     if (cl > 1) cluster_wait();
-    const int rounds = int(cdiv(p.L, int64_t(kSeg) * cl));
     const int64_t nseg = cdiv(p.L, kSeg);
     for (int r = rounds - 1; r >= 0; --r) {
         const int par = r & 1;
-        const int64_t tile = int64_t(r) * cl + rank, t0 = tile * kSeg + warp * ROWS;
-        const int64_t first = (lead * p.L + (t0 < p.L ? t0 : p.L - 1)) * p.D + cc;
+        const int64_t tile = int64_t(r) * cl + rank, t0 = row_of(r), first = first_of(t0);
         const RowOffsets<ROWS> ro(p.L - t0, p.D);
         float a[ROWS][VEC], w[ROWS][VEC], xv[ROWS][VEC], d[ROWS][VEC], dz[ROWS][VEC];
         float s[VEC];  // state entering the block's rows
         ldv<VEC>(seg + (lead * nseg + (tile < nseg ? tile : nseg - 1)) * p.D + cc, s);
+        if (r > 0) stage(r - 1);
+        copies_commit();
+        copies_wait<1>();
 #pragma unroll
-        for (int j = 0; j < ROWS; ++j) ldv<VEC>(la + first + ro.off[j], a[j]);
-#pragma unroll
-        for (int j = 0; j < ROWS; ++j) ldv<VEC>(x + first + ro.off[j], xv[j]);
-#pragma unroll
-        for (int j = 0; j < ROWS; ++j) ldv<VEC>(dh + first + ro.off[j], d[j]);
+        for (int j = 0; j < ROWS; ++j) {
+            ldv<VEC>(gates_at(par) + j * CW, a[j]);
+            take_row<T, VEC>(x_at(par), x + first, ro.off[j], j, xv[j]);
+            take_row<T, VEC>(dh_at(par), dh + first, ro.off[j], j, d[j]);
+        }
         RowInfo ri{0, 0, 0, 0};
         if constexpr (PACKED) ri = rows_packed<ROWS>(cu, int(p.B), t0, p.L, lane);
         else ri.valid = t0 + ROWS <= p.L ? ~0u : t0 < p.L ? (1u << (p.L - t0)) - 1 : 0u;
@@ -604,25 +677,35 @@ __global__ void __launch_bounds__(kStepThreads) k_scan_step(ScanProblem p, GateF
 
 GateForm form(const ScanProblem& p) { return GateForm{p.preact, p.leak, p.inv_tau}; }
 
-// Blocks per cluster: enough to fill the SMs (three blocks of 256 threads on each) where the sequences and channel
-// tiles alone do not, but no more than there are row tiles.
-int cluster_size(int64_t groups, int64_t L, int tile) {
+// Blocks per cluster: as many as the SMs hold at once (`slots`) where the sequences and channel tiles alone do not
+// fill them, but no more than there are row tiles. A grid that just exceeds the slots would run a second, nearly
+// empty wave.
+int cluster_size(int64_t groups, int64_t L, int tile, int64_t slots) {
+    int64_t cl = slots / groups;
     const int64_t tiles = cdiv(L, tile);
-    int cl = 1;
-    while (cl < kMaxCluster && cl < tiles && groups * cl < 148 * 3) cl *= 2;
-    return cl;
+    cl = cl < tiles ? cl : tiles;
+    return int(cl < 1 ? 1 : cl < kMaxCluster ? cl : kMaxCluster);
+}
+
+constexpr int kSms = 148;
+
+template <int VEC>
+size_t smem_of(int cl, int stage_bytes) {
+    return (cl > 1 ? size_t(2) * cl * 32 * VEC * sizeof(float2) : 0) + size_t(2) * kWarps * stage_bytes;
 }
 
 template <typename K, typename... Args>
-gla_status launch_clusters(const char* name, K kernel, int64_t groups, int cl, int vec, cudaStream_t s, Args... args) {
+gla_status launch_clusters(const char* name, K kernel, int64_t groups, int cl, size_t smem, cudaStream_t s, Args... args) {
     if (groups * cl > (int64_t(1) << 31) - 1) return GLA_ERR_UNSUPPORTED;
     if (cl > 8 && cudaFuncSetAttribute(kernel, cudaFuncAttributeNonPortableClusterSizeAllowed, 1) != cudaSuccess)
+        return GLA_ERR_CUDA;
+    if (cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, int(smem)) != cudaSuccess)
         return GLA_ERR_CUDA;
     launch_begin(name, s);
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3(unsigned(groups * cl));
     cfg.blockDim = dim3(kThreads);
-    cfg.dynamicSmemBytes = cl > 1 ? size_t(2) * cl * 32 * vec * sizeof(float2) : 0;
+    cfg.dynamicSmemBytes = smem;
     cfg.stream = s;
     cudaLaunchAttribute attr[1];
     attr[0].id = cudaLaunchAttributeClusterDimension;
@@ -635,14 +718,16 @@ gla_status launch_clusters(const char* name, K kernel, int64_t groups, int cl, i
 }
 
 constexpr int kFwdRows = 8;
+constexpr int kFwdBlocks = 3, kBwdBlocks = 2;  // blocks per SM
 
 template <typename T, int VEC, bool PACKED, bool PREACT>
 gla_status fwd_typed(const ScanProblem& p, const void* x, const float* la, const int32_t* cu, const float* h0,
                      void* h, float* hT, float* seg, cudaStream_t s) {
     const int64_t groups = (PACKED ? p.H : p.B * p.H) * cdiv(p.D, 32 * VEC);
-    const int cl = cluster_size(groups, p.L, kWarps * kFwdRows);
-    return launch_clusters("scan_fwd", k_scan_fwd<T, VEC, PACKED, PREACT, kFwdRows>, groups, cl, VEC, s, p, form(p), cl,
-                           static_cast<const T*>(x), la, cu, h0, static_cast<T*>(h), hT, seg);
+    const int cl = cluster_size(groups, p.L, kWarps * kFwdRows, kSms * kFwdBlocks);
+    return launch_clusters("scan_fwd", k_scan_fwd<T, VEC, PACKED, PREACT, kFwdRows>, groups, cl,
+                           smem_of<VEC>(cl, kFwdStage<T, VEC, kFwdRows>), s, p, form(p), cl, static_cast<const T*>(x),
+                           la, cu, h0, static_cast<T*>(h), hT, seg);
 }
 
 template <typename T, int VEC, bool PACKED, bool PREACT>
@@ -650,8 +735,9 @@ gla_status bwd_typed(const ScanProblem& p, const void* x, const float* la, const
                      const void* dh, const float* dhT, void* dx, float* dla, float* dh0, const float* seg,
                      cudaStream_t s) {
     const int64_t groups = (PACKED ? p.H : p.B * p.H) * cdiv(p.D, 32 * VEC);
-    const int cl = cluster_size(groups, p.L, kSeg);
-    return launch_clusters("scan_bwd", k_scan_bwd<T, VEC, PACKED, PREACT>, groups, cl, VEC, s, p, form(p), cl,
+    const int cl = cluster_size(groups, p.L, kSeg, kSms * kBwdBlocks);
+    return launch_clusters("scan_bwd", k_scan_bwd<T, VEC, PACKED, PREACT>, groups, cl,
+                           smem_of<VEC>(cl, kBwdStage<T, VEC, kSeg / kWarps>), s, p, form(p), cl,
                            static_cast<const T*>(x), la, cu, h0, static_cast<const T*>(dh), dhT, static_cast<T*>(dx),
                            dla, dh0, seg);
 }
