@@ -35,11 +35,6 @@ constexpr int kThreads = kWarps * 32;
 constexpr int kSeg = 64;  // rows between the states kept for the backward, which takes a block's rows from one of them
 constexpr int kMaxCluster = 16;
 
-struct GateForm {
-    bool preact, leak;
-    float inv_tau;
-};
-
 // ---- cluster primitives -----------------------------------------------------------------
 __device__ __forceinline__ uint32_t cluster_rank() {
     uint32_t r;
@@ -48,43 +43,72 @@ __device__ __forceinline__ uint32_t cluster_rank() {
 }
 __device__ __forceinline__ void cluster_arrive() { asm volatile("barrier.cluster.arrive.release;" ::: "memory"); }
 __device__ __forceinline__ void cluster_wait() { asm volatile("barrier.cluster.wait.acquire;" ::: "memory"); }
-// store to the same shared-memory address in block `rank` of the cluster
-__device__ __forceinline__ void st_peer(float2* p, uint32_t rank, float2 x) {
-    uint32_t a = static_cast<uint32_t>(__cvta_generic_to_shared(p));
-    asm volatile(
-        "{\n\t.reg .b32 r;\n\t"
-        "mapa.shared::cluster.u32 r, %0, %1;\n\t"
-        "st.shared::cluster.v2.f32 [r], {%2, %3};\n\t}" ::"r"(a),
-        "r"(rank), "f"(x.x), "f"(x.y)
-        : "memory");
+
+// ---- one or two adjacent channels -------------------------------------------------------
+// Two channels are one packed operand: the packed fp32 instructions do both for one issue slot, and issue slots are
+// what these kernels run out of first (a wide batch spends about as long issuing as it does on memory).
+template <int VEC>
+struct VecOf {
+    using type = float;
+};
+template <>
+struct VecOf<2> {
+    using type = float2;
+};
+__device__ __forceinline__ uint64_t bits(float2 x) { return *reinterpret_cast<uint64_t*>(&x); }
+__device__ __forceinline__ float2 pair(uint64_t x) { return *reinterpret_cast<float2*>(&x); }
+__device__ __forceinline__ float vfma(float a, float b, float c) { return fmaf(a, b, c); }
+__device__ __forceinline__ float2 vfma(float2 a, float2 b, float2 c) {
+    uint64_t d;
+    asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(d) : "l"(bits(a)), "l"(bits(b)), "l"(bits(c)));
+    return pair(d);
+}
+__device__ __forceinline__ float vmul(float a, float b) { return a * b; }
+__device__ __forceinline__ float2 vmul(float2 a, float2 b) {
+    uint64_t d;
+    asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(d) : "l"(bits(a)), "l"(bits(b)));
+    return pair(d);
+}
+__device__ __forceinline__ float vadd(float a, float b) { return a + b; }
+__device__ __forceinline__ float2 vadd(float2 a, float2 b) {
+    uint64_t d;
+    asm("add.rn.f32x2 %0, %1, %2;" : "=l"(d) : "l"(bits(a)), "l"(bits(b)));
+    return pair(d);
+}
+template <typename V>
+__device__ __forceinline__ V vset(float x) {
+    if constexpr (sizeof(V) == 8) return make_float2(x, x);
+    else return x;
+}
+// f of each channel
+template <typename F>
+__device__ __forceinline__ float each(F f, float a) { return f(a); }
+template <typename F>
+__device__ __forceinline__ float2 each(F f, float2 a) { return make_float2(f(a.x), f(a.y)); }
+template <typename F>
+__device__ __forceinline__ float each(F f, float a, float b) { return f(a, b); }
+template <typename F>
+__device__ __forceinline__ float2 each(F f, float2 a, float2 b) { return make_float2(f(a.x, b.x), f(a.y, b.y)); }
+template <typename F>
+__device__ __forceinline__ float each(F f, float a, float b, float c) { return f(a, b, c); }
+template <typename F>
+__device__ __forceinline__ float2 each(F f, float2 a, float2 b, float2 c) {
+    return make_float2(f(a.x, b.x, c.x), f(a.y, b.y, c.y));
 }
 
-// ---- loads and stores of VEC adjacent channels ------------------------------------------
-template <int VEC>
-__device__ __forceinline__ void ldv(const float* p, float* y) {
-    if constexpr (VEC == 2) {
-        const float2 t = *reinterpret_cast<const float2*>(p);
-        y[0] = t.x;
-        y[1] = t.y;
-    } else y[0] = *p;
+template <typename V>
+__device__ __forceinline__ V ldv(const float* p) { return *reinterpret_cast<const V*>(p); }
+template <typename V>
+__device__ __forceinline__ V ldv(const __nv_bfloat16* p) {
+    if constexpr (sizeof(V) == 8) return __bfloat1622float2(*reinterpret_cast<const __nv_bfloat162*>(p));
+    else return __bfloat162float(*p);
 }
-template <int VEC>
-__device__ __forceinline__ void ldv(const __nv_bfloat16* p, float* y) {
-    if constexpr (VEC == 2) {
-        const __nv_bfloat162 t = *reinterpret_cast<const __nv_bfloat162*>(p);
-        y[0] = __bfloat162float(t.x);
-        y[1] = __bfloat162float(t.y);
-    } else y[0] = __bfloat162float(*p);
-}
-template <int VEC>
-__device__ __forceinline__ void stv(float* p, const float* y) {
-    if constexpr (VEC == 2) *reinterpret_cast<float2*>(p) = make_float2(y[0], y[1]);
-    else *p = y[0];
-}
-template <int VEC>
-__device__ __forceinline__ void stv(__nv_bfloat16* p, const float* y) {
-    if constexpr (VEC == 2) *reinterpret_cast<__nv_bfloat162*>(p) = __floats2bfloat162_rn(y[0], y[1]);
-    else *p = __float2bfloat16_rn(y[0]);
+template <typename V>
+__device__ __forceinline__ void stv(float* p, V y) { *reinterpret_cast<V*>(p) = y; }
+template <typename V>
+__device__ __forceinline__ void stv(__nv_bfloat16* p, V y) {
+    if constexpr (sizeof(V) == 8) *reinterpret_cast<__nv_bfloat162*>(p) = __floats2bfloat162_rn(y.x, y.y);
+    else *p = __float2bfloat16_rn(y);
 }
 
 // ---- gates --------------------------------------------------------------------------------
@@ -95,17 +119,19 @@ __device__ __forceinline__ void stv(__nv_bfloat16* p, const float* y) {
 // precision: 1 - a = -la q(la) with q = (e^x - 1) / x as a polynomial fitted at the Chebyshev nodes of [-1/2, 0]
 // (relative error 3e-9), so 1 - a is within 3 u and a = 1 - (1 - a) correctly rounded from it. Below -1/2 (a < 0.61,
 // no long products): the ex2 instruction, within (4 + |la|) u.
-__device__ __forceinline__ void decay_of(float la, float& a, float& one_minus_a) {
-    float q = fmaf(0.00112340425f, la, 0.00818961393f);
-    q = fmaf(q, la, 0.0416300744f);
-    q = fmaf(q, la, 0.166662425f);
-    q = fmaf(q, la, 0.499999821f);
-    q = fmaf(q, la, 1.f);
-    const float m = -la * q;
-    const float e = tc::exp2_ftz(la * tc::kLog2e);
-    const bool near = fabsf(la) < 0.5f;
-    a = near ? 1.f - m : e;
-    one_minus_a = near ? m : 1.f - e;
+template <typename V>
+__device__ __forceinline__ void decay_of(V la, V& a, V& one_minus_a) {
+    V q = vfma(vset<V>(-0.00112340425f), la, vset<V>(-0.00818961393f));
+    q = vfma(q, la, vset<V>(-0.0416300744f));
+    q = vfma(q, la, vset<V>(-0.166662425f));
+    q = vfma(q, la, vset<V>(-0.499999821f));
+    q = vfma(q, la, vset<V>(-1.f));
+    const V m = vmul(la, q);
+    const V e = each([](float t) { return tc::exp2_ftz(t); }, vmul(la, vset<V>(tc::kLog2e)));
+    const V am = vfma(m, vset<V>(-1.f), vset<V>(1.f)), me = vfma(e, vset<V>(-1.f), vset<V>(1.f));
+    const auto near = [](float l, float yes, float no) { return fabsf(l) < 0.5f ? yes : no; };
+    a = each(near, la, am, e);
+    one_minus_a = each(near, la, m, me);
 }
 
 __device__ __forceinline__ float rcp(float x) {
@@ -117,28 +143,29 @@ __device__ __forceinline__ float rcp(float x) {
 // logsigmoid(z) = min(z, 0) - log(1 + t), t = e^-|z| in [0, 1], with log(1 + t) = 2 atanh(s), s = t / (2 + t) <= 1/3:
 // atanh(s) / s as a polynomial in s^2 fitted at the Chebyshev nodes of [0, 1/9] (relative error 8e-9). Small t
 // keeps its relative precision, (8 + |z|) u in all.
-__device__ __forceinline__ float logsigmoid_series(float z, float& t) {
-    t = tc::exp2_ftz(-fabsf(z) * tc::kLog2e);
-    const float s = t * rcp(2.f + t), y = s * s;
-    float q = fmaf(0.140788898f, y, 0.139825791f);
-    q = fmaf(q, y, 0.200122982f);
-    q = fmaf(q, y, 0.333331615f);
-    q = fmaf(q, y, 1.f);
-    return fmaf(-2.f * s, q, fminf(z, 0.f));
+template <typename V>
+__device__ __forceinline__ V logsigmoid_series(V z, V& t) {
+    t = each([](float x) { return tc::exp2_ftz(-fabsf(x) * tc::kLog2e); }, z);
+    const V s = vmul(t, each([](float x) { return rcp(x); }, vadd(t, vset<V>(2.f)))), y = vmul(s, s);
+    V q = vfma(vset<V>(0.140788898f), y, vset<V>(0.139825791f));
+    q = vfma(q, y, vset<V>(0.200122982f));
+    q = vfma(q, y, vset<V>(0.333331615f));
+    q = vfma(q, y, vset<V>(1.f));
+    return vfma(vmul(s, vset<V>(-2.f)), q, each([](float x) { return fminf(x, 0.f); }, z));
 }
 
 // a_t and w_t from the gate argument; for a pre-activation also dlog a / dz = sigmoid(-z) / tau
-template <bool PREACT>
-__device__ __forceinline__ void gate_of(const GateForm& f, float g, float& a, float& w, float& dz) {
-    float la = g;
+template <bool PREACT, bool LEAK, typename V>
+__device__ __forceinline__ void gate_of(float inv_tau, V g, V& a, V& w, V& dz) {
+    V la = g;
     if constexpr (PREACT) {
-        float t;
-        la = logsigmoid_series(g, t) * f.inv_tau;
-        const float r = rcp(1.f + t);
-        dz = (g < 0.f ? r : t * r) * f.inv_tau;
+        V t;
+        la = vmul(logsigmoid_series(g, t), vset<V>(inv_tau));
+        const V r = each([](float x) { return rcp(x); }, vadd(t, vset<V>(1.f)));
+        dz = vmul(each([](float x, float yes, float no) { return x < 0.f ? yes : no; }, g, r, vmul(t, r)), vset<V>(inv_tau));
     }
     decay_of(la, a, w);
-    if (!f.leak) w = 1.f;
+    if constexpr (!LEAK) w = vset<V>(1.f);
 }
 
 // Maps of packed rows that hold a sequence's start forget everything in front of it, whatever that is: an infinity
@@ -147,10 +174,95 @@ __device__ __forceinline__ void gate_of(const GateForm& f, float g, float& a, fl
 constexpr float kForget = -0.f;
 template <bool PACKED>
 __device__ __forceinline__ bool forgets(float m) { return PACKED && __float_as_uint(m) == 0x80000000u; }
-template <bool PACKED>
-__device__ __forceinline__ float join(float m, float s, float u) { return forgets<PACKED>(m) ? u : fmaf(m, s, u); }
-template <bool PACKED>
-__device__ __forceinline__ float join(float m, float f) { return forgets<PACKED>(m) ? m : m * f; }
+template <bool PACKED, typename V>
+__device__ __forceinline__ V join(V m, V s, V u) {
+    const V y = vfma(m, s, u);
+    if constexpr (!PACKED) return y;
+    else return each([](float f, float yes, float no) { return forgets<true>(f) ? yes : no; }, m, u, y);
+}
+template <bool PACKED, typename V>
+__device__ __forceinline__ V join(V m, V f) {
+    const V y = vmul(m, f);
+    if constexpr (!PACKED) return y;
+    else return each([](float f2, float yes, float no) { return forgets<true>(f2) ? yes : no; }, m, m, y);
+}
+
+// The map of a span of rows, for one lane's channels.
+template <typename V>
+struct alignas(2 * sizeof(V)) Map {
+    V a, u;
+};
+
+// Put a map into the same place of block `rank`'s shared memory and count it on that block's barrier.
+template <typename V>
+__device__ __forceinline__ void send(Map<V>* place, uint64_t* bar, uint32_t rank, Map<V> m) {
+    if constexpr (sizeof(V) == 8) {
+        asm volatile(
+            "{\n\t.reg .b32 a, b;\n\t"
+            "mapa.shared::cluster.u32 a, %0, %2;\n\t"
+            "mapa.shared::cluster.u32 b, %1, %2;\n\t"
+            "st.async.shared::cluster.mbarrier::complete_tx::bytes.v4.f32 [a], {%3, %4, %5, %6}, [b];\n\t}" ::"r"(
+                tc::smem_u32(place)),
+            "r"(tc::smem_u32(bar)), "r"(rank), "f"(m.a.x), "f"(m.a.y), "f"(m.u.x), "f"(m.u.y)
+            : "memory");
+    } else {
+        asm volatile(
+            "{\n\t.reg .b32 a, b;\n\t"
+            "mapa.shared::cluster.u32 a, %0, %2;\n\t"
+            "mapa.shared::cluster.u32 b, %1, %2;\n\t"
+            "st.async.shared::cluster.mbarrier::complete_tx::bytes.v2.f32 [a], {%3, %4}, [b];\n\t}" ::"r"(
+                tc::smem_u32(place)),
+            "r"(tc::smem_u32(bar)), "r"(rank), "f"(m.a), "f"(m.u)
+            : "memory");
+    }
+}
+
+// The blocks' exchange of one cluster. Each round every block sends its rows' map to all blocks; a block waits for the
+// cl maps on its own barrier, of which there are two for alternate rounds. A map of round i + 2 cannot overtake the
+// reading of round i's: its sender has waited for this block's map of round i + 1, which left after all of this
+// block's warps were done with round i.
+template <typename V>
+struct Exchange {
+    Map<V>* maps;   // [2][cl][32]
+    uint64_t* bar;  // [2]
+    int* abort;
+    int* err;
+    int cl, rank, rounds;
+    __device__ __forceinline__ uint32_t bytes() const { return uint32_t(cl * 32 * sizeof(Map<V>)); }
+    __device__ __forceinline__ void begin() {
+        if (cl == 1) return;
+        if (threadIdx.x == 0) {
+            *abort = 0;
+            for (int i = 0; i < 2; ++i) tc::mbar_init(bar + i, 1);
+            tc::fence_barrier_init();
+            for (int i = 0; i < 2; ++i) tc::mbar_arrive_expect_tx(bar + i, bytes());
+        }
+        __syncthreads();
+        cluster_arrive();  // completed by ready(): every block's barriers exist before any block sends
+    }
+    __device__ __forceinline__ void ready() const {
+        if (cl > 1) cluster_wait();
+    }
+    // one warp sends its block's map of round `it`
+    __device__ __forceinline__ void put(int it, Map<V> m) const {
+        const int par = it & 1;
+        for (int q = 0; q < cl; ++q) send(maps + (par * cl + rank) * 32 + (threadIdx.x & 31), bar + par, uint32_t(q), m);
+    }
+    // every thread waits for the maps of round `it`
+    __device__ __forceinline__ const Map<V>* get(int it) const {
+        const int par = it & 1;
+        (void)tc::mbar_wait(bar + par, uint32_t(it >> 1) & 1u, err, abort);
+        if (threadIdx.x == 0 && it + 2 < rounds) tc::mbar_arrive_expect_tx(bar + par, bytes());
+        return maps + par * cl * 32 + (threadIdx.x & 31);
+    }
+    // no block leaves while another may still send to it
+    __device__ __forceinline__ void end() const {
+        if (cl > 1) {
+            cluster_arrive();
+            cluster_wait();
+        }
+    }
+};
 
 // What a warp knows of its rows t0, t0 + 1, ...: which belong to a sequence, which start or end one, and (per lane,
 // for row t0 + lane) the sequence's number.
@@ -187,31 +299,26 @@ __device__ __forceinline__ RowInfo rows_packed(const int32_t* __restrict__ cu, i
 }
 
 // row n of a [B,H,D] state tensor (NULL: zero)
-template <int VEC>
-__device__ __forceinline__ void state_of(const float* __restrict__ h, int64_t n, const ScanProblem& p, int64_t head,
-                                         int64_t c, float* y) {
-#pragma unroll
-    for (int v = 0; v < VEC; ++v) y[v] = 0.f;
-    if (h) ldv<VEC>(h + (n * p.H + head) * p.D + c, y);
+template <typename V>
+__device__ __forceinline__ V state_of(const float* __restrict__ h, int64_t n, const ScanProblem& p, int64_t head,
+                                      int64_t c) {
+    return h ? ldv<V>(h + (n * p.H + head) * p.D + c) : vset<V>(0.f);
 }
 
 // Empty sequences have no row that could write their end: out[n] = in[n] (or 0), spread over the cluster's warps.
-template <int VEC>
-__device__ __forceinline__ void copy_empty(const int32_t* __restrict__ cu, int B, int64_t H, int64_t head, int64_t D,
-                                           int64_t c, const float* __restrict__ in, float* __restrict__ out, int first,
+template <typename V>
+__device__ __forceinline__ void copy_empty(const int32_t* __restrict__ cu, const ScanProblem& p, int64_t head, int64_t c,
+                                           bool mine, const float* __restrict__ in, float* __restrict__ out, int first,
                                            int stride, int lane) {
     if (!out) return;
+    const int B = int(p.B);
     for (int n0 = first * 32; n0 < B; n0 += stride * 32) {
         const int n = n0 + lane;
         uint32_t m = __ballot_sync(0xffffffffu, n < B && cu[n < B ? n : 0] >= cu[n < B ? n + 1 : 0]);
         while (m) {
             const int64_t e = n0 + __ffs(m) - 1;
             m &= m - 1;
-            if (c < D) {
-                float y[VEC] = {};
-                if (in) ldv<VEC>(in + (e * H + head) * D + c, y);
-                stv<VEC>(out + (e * H + head) * D + c, y);
-            }
+            if (mine) stv(out + (e * p.H + head) * p.D + c, state_of<V>(in, e, p, head, c));
         }
     }
 }
@@ -252,10 +359,11 @@ __device__ __forceinline__ void stage_rows(T* st, const T* src, const RowOffsets
         for (int j = 0; j < ROWS; ++j) copy_async<sizeof(T) * VEC>(st + j * 32 * VEC, src + ro.off[j]);
     }
 }
-template <typename T, int VEC>
-__device__ __forceinline__ void take_row(const T* st, const T* src, uint32_t off, int j, float* y) {
-    if constexpr (kStaged<T, VEC>) ldv<VEC>(st + j * 32 * VEC, y);
-    else ldv<VEC>(src + off, y);
+template <typename V, typename T>
+__device__ __forceinline__ V take_row(const T* st, const T* src, uint32_t off, int j) {
+    constexpr int VEC = int(sizeof(V) / 4);
+    if constexpr (kStaged<T, VEC>) return ldv<V>(st + j * 32 * VEC);
+    else return ldv<V>(src + off);
 }
 
 // bytes a warp's stage takes
@@ -264,374 +372,289 @@ constexpr int kFwdStage = ROWS * 32 * VEC * int(4 + sizeof(T));
 template <typename T, int VEC, int ROWS>
 constexpr int kBwdStage = ROWS * 32 * VEC * int(4 + 2 * sizeof(T));
 
+// What a block is to do and where its lanes' data are.
+template <typename T, int VEC, int ROWS, int STAGE>
+struct Place {
+    int lane, warp, rank, cl;
+    int64_t lead, c, cc, L, D;  // sequence or head; channel, and the nearest one that exists
+    bool mine;
+    char* stages;
+    __device__ __forceinline__ Place(const ScanProblem& p, int cl_, char* stages_) : cl(cl_), L(p.L), D(p.D) {
+        constexpr int CW = 32 * VEC;
+        lane = threadIdx.x & 31;
+        warp = __shfl_sync(0xffffffffu, int(threadIdx.x >> 5), 0);
+        rank = cl > 1 ? int(cluster_rank()) : 0;
+        const int64_t tiles = cdiv(p.D, CW), id = blockIdx.x / cl;
+        lead = id / tiles;
+        c = (id % tiles) * CW + lane * VEC;
+        mine = c < p.D;
+        cc = mine ? c : p.D - VEC;
+        stages = stages_ + warp * 2 * STAGE;
+    }
+    __device__ __forceinline__ int64_t row(int r) const { return (int64_t(r) * cl + rank) * (kWarps * ROWS) + warp * ROWS; }
+    __device__ __forceinline__ int64_t first(int64_t t) const { return (lead * L + (t < L ? t : L - 1)) * D + cc; }
+    __device__ __forceinline__ float* gates(int par) const {
+        return reinterpret_cast<float*>(stages + par * STAGE) + lane * VEC;
+    }
+    // k-th tensor of the element type
+    __device__ __forceinline__ T* elems(int par, int k) const {
+        return reinterpret_cast<T*>(stages + par * STAGE + ROWS * 32 * VEC * 4) + k * ROWS * 32 * VEC + lane * VEC;
+    }
+};
+
 // ---- forward ------------------------------------------------------------------------------
-// Grid: (sequence or head) x channel tile x cluster of `cl` blocks. Rows of round r and block q: from (r cl + q) TILE.
-template <typename T, int VEC, bool PACKED, bool PREACT, int ROWS>
+// Grid: (sequence or head) x channel tile x cluster of `cl` blocks. Rows of round r and block q: from
+// (r cl + q) kWarps ROWS.
+template <typename T, int VEC, bool PACKED, bool PREACT, bool LEAK, int ROWS>
 __global__ void __launch_bounds__(kThreads, ROWS * VEC <= 16 ? 3 : 2)
-    k_scan_fwd(ScanProblem p, GateForm f, int cl, const T* __restrict__ x, const float* __restrict__ la,
+    k_scan_fwd(ScanProblem p, int cl, const T* __restrict__ x, const float* __restrict__ la,
                const int32_t* __restrict__ cu, const float* __restrict__ h0, T* __restrict__ h, float* __restrict__ hT,
-               float* __restrict__ seg) {
-    constexpr int CW = 32 * VEC, TILE = kWarps * ROWS;
-    __shared__ float2 agg[2][kWarps][CW];
-    extern __shared__ float2 peer[];  // [2][cl][CW] the blocks' maps, then the warps' stages
-    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-    const int rank = cl > 1 ? int(cluster_rank()) : 0;
-    const int64_t tiles = cdiv(p.D, CW);
-    const int64_t id = blockIdx.x / cl, lead = id / tiles, c = (id % tiles) * CW + lane * VEC;
-    const bool mine = c < p.D;
-    const int64_t cc = mine ? c : p.D - VEC;
-    const int64_t head = PACKED ? lead : 0;
-    char* stages = reinterpret_cast<char*>(peer + (cl > 1 ? 2 * cl * CW : 0)) + warp * 2 * kFwdStage<T, VEC, ROWS>;
-    const auto row_of = [&](int r) { return (int64_t(r) * cl + rank) * TILE + warp * ROWS; };
-    const auto first_of = [&](int64_t t) { return (lead * p.L + (t < p.L ? t : p.L - 1)) * p.D + cc; };
-    const auto gates_at = [&](int par) { return reinterpret_cast<float*>(stages + par * kFwdStage<T, VEC, ROWS>) + lane * VEC; };
-    const auto x_at = [&](int par) {
-        return reinterpret_cast<T*>(stages + par * kFwdStage<T, VEC, ROWS> + ROWS * CW * 4) + lane * VEC;
-    };
+               float* __restrict__ seg, int* err) {
+    using V = typename VecOf<VEC>::type;
+    constexpr int STAGE = kFwdStage<T, VEC, ROWS>;
+    __shared__ Map<V> agg[2][kWarps][32];
+    __shared__ uint64_t bar[2];
+    __shared__ int abort_flag;
+    extern __shared__ __align__(16) char dyn[];  // the cluster's maps, then the warps' stages
+    const Place<T, VEC, ROWS, STAGE> at(p, cl, dyn + (cl > 1 ? 2 * cl * 32 * sizeof(Map<V>) : 0));
+    const int lane = at.lane, warp = at.warp, rank = at.rank;
+    const int64_t lead = at.lead, c = at.c, cc = at.cc, head = PACKED ? lead : 0;
+    const bool mine = at.mine;
+    const int rounds = int(cdiv(p.L, int64_t(kWarps * ROWS) * cl));
+    Exchange<V> ex{reinterpret_cast<Map<V>*>(dyn), bar, &abort_flag, err, cl, rank, rounds};
     const auto stage = [&](int r) {
-        const int64_t t = row_of(r), i = first_of(t);
+        const int64_t t = at.row(r), i = at.first(t);
         const RowOffsets<ROWS> ro(p.L - t, p.D);
-        stage_rows<float, VEC, ROWS>(gates_at(r & 1), la + i, ro);
-        stage_rows<T, VEC, ROWS>(x_at(r & 1), x + i, ro);
+        stage_rows<float, VEC, ROWS>(at.gates(r & 1), la + i, ro);
+        stage_rows<T, VEC, ROWS>(at.elems(r & 1, 0), x + i, ro);
     };
     stage(0);
     copies_commit();
-    if (cl > 1) cluster_arrive();  // every block of the cluster has started before any puts data into it
-    if constexpr (PACKED) copy_empty<VEC>(cu, int(p.B), p.H, head, p.D, c, h0, hT, rank * kWarps + warp, cl * kWarps, lane);
-    float carry[VEC] = {};
-    if (!PACKED && h0) ldv<VEC>(h0 + lead * p.D + cc, carry);
-    if (cl > 1) cluster_wait();
-    const int rounds = int(cdiv(p.L, int64_t(TILE) * cl));
+    ex.begin();
+    if constexpr (PACKED) copy_empty<V>(cu, p, head, c, mine, h0, hT, rank * kWarps + warp, cl * kWarps, lane);
+    V carry = vset<V>(0.f);
+    if (!PACKED && h0) carry = ldv<V>(h0 + lead * p.D + cc);
+    ex.ready();
     const int64_t nseg = cdiv(p.L, kSeg);
     for (int r = 0; r < rounds; ++r) {
         const int par = r & 1;
-        const int64_t t0 = row_of(r), first = first_of(t0);
+        const int64_t t0 = at.row(r), first = at.first(t0);
         const RowOffsets<ROWS> ro(p.L - t0, p.D);
         if (r + 1 < rounds) stage(r + 1);
         copies_commit();
         copies_wait<1>();
-        float a[ROWS][VEC], b[ROWS][VEC];
-#pragma unroll
-        for (int j = 0; j < ROWS; ++j) {
-            ldv<VEC>(gates_at(par) + j * CW, a[j]);
-            take_row<T, VEC>(x_at(par), x + first, ro.off[j], j, b[j]);
-        }
         RowInfo ri{0, 0, 0, 0};
         if constexpr (PACKED) ri = rows_packed<ROWS>(cu, int(p.B), t0, p.L, lane);
         else ri.valid = t0 + ROWS <= p.L ? ~0u : t0 < p.L ? (1u << (p.L - t0)) - 1 : 0u;
+        V a[ROWS], b[ROWS];
 #pragma unroll
         for (int j = 0; j < ROWS; ++j) {
-#pragma unroll
-            for (int v = 0; v < VEC; ++v) {
-                float w, dz;
-                gate_of<PREACT>(f, a[j][v], a[j][v], w, dz);
-                b[j][v] *= w;
-            }
+            V w, dz;
+            gate_of<PREACT, LEAK>(p.inv_tau, ldv<V>(at.gates(par) + j * 32 * VEC), a[j], w, dz);
+            b[j] = take_row<V>(at.elems(par, 0), x + first, ro.off[j], j);
+            if constexpr (LEAK) b[j] = vmul(b[j], w);
         }
-        constexpr uint32_t kAll = ROWS == 32 ? ~0u : (1u << ROWS) - 1;
+        constexpr uint32_t kAll = (1u << ROWS) - 1;
         if ((ri.valid & kAll) != kAll) {
 #pragma unroll
-            for (int j = 0; j < ROWS; ++j) {
-                if (!(ri.valid >> j & 1)) {
-#pragma unroll
-                    for (int v = 0; v < VEC; ++v) a[j][v] = 1.f, b[j][v] = 0.f;
-                }
-            }
+            for (int j = 0; j < ROWS; ++j)
+                if (!(ri.valid >> j & 1)) a[j] = vset<V>(1.f), b[j] = vset<V>(0.f);
         }
-        float A[VEC], U[VEC];
-#pragma unroll
-        for (int v = 0; v < VEC; ++v) A[v] = 1.f, U[v] = 0.f;
+        Map<V> own{vset<V>(1.f), vset<V>(0.f)};
 #pragma unroll
         for (int j = 0; j < ROWS; ++j) {
-            if (PACKED && (ri.start >> j & 1)) state_of<VEC>(h0, __shfl_sync(0xffffffffu, ri.n, j), p, head, cc, U);
-#pragma unroll
-            for (int v = 0; v < VEC; ++v) {
-                A[v] *= a[j][v];
-                U[v] = fmaf(a[j][v], U[v], b[j][v]);
-            }
+            if (PACKED && (ri.start >> j & 1)) own.u = state_of<V>(h0, __shfl_sync(0xffffffffu, ri.n, j), p, head, cc);
+            own.a = vmul(own.a, a[j]);
+            own.u = vfma(a[j], own.u, b[j]);
         }
-        if (PACKED && ri.start) {
-#pragma unroll
-            for (int v = 0; v < VEC; ++v) A[v] = kForget;
-        }
-#pragma unroll
-        for (int v = 0; v < VEC; ++v) agg[par][warp][v * 32 + lane] = make_float2(A[v], U[v]);
+        if (PACKED && ri.start) own.a = vset<V>(kForget);
+        agg[par][warp][lane] = own;
         __syncthreads();
-        // the map of the block's rows in front of this warp's
-        float pa[VEC], pu[VEC];
-#pragma unroll
-        for (int v = 0; v < VEC; ++v) pa[v] = 1.f, pu[v] = 0.f;
+        Map<V> pre{vset<V>(1.f), vset<V>(0.f)};  // of the block's rows in front of this warp's
 #pragma unroll
         for (int w = 0; w < kWarps - 1; ++w) {
             if (w < warp) {
-#pragma unroll
-                for (int v = 0; v < VEC; ++v) {
-                    const float2 m = agg[par][w][v * 32 + lane];
-                    pa[v] = join<PACKED>(m.x, pa[v]);
-                    pu[v] = join<PACKED>(m.x, pu[v], m.y);
-                }
+                const Map<V> m = agg[par][w][lane];
+                pre = Map<V>{join<PACKED>(m.a, pre.a), join<PACKED>(m.a, pre.u, m.u)};
             }
         }
-        float in[VEC];  // state entering the block's rows
+        V in = carry;  // state entering the block's rows
         if (cl > 1) {
-            if (warp == kWarps - 1) {
-#pragma unroll
-                for (int v = 0; v < VEC; ++v) {
-                    const float2 m = make_float2(join<PACKED>(A[v], pa[v]), join<PACKED>(A[v], pu[v], U[v]));
-                    for (int q = 0; q < cl; ++q) st_peer(peer + (par * cl + rank) * CW + v * 32 + lane, q, m);
-                }
-            }
-            cluster_arrive();
-            cluster_wait();
+            if (warp == kWarps - 1) ex.put(r, Map<V>{join<PACKED>(own.a, pre.a), join<PACKED>(own.a, pre.u, own.u)});
+            const Map<V>* m = ex.get(r);
             for (int q = 0; q < cl; ++q) {
-#pragma unroll
-                for (int v = 0; v < VEC; ++v) {
-                    if (q == rank) in[v] = carry[v];
-                    const float2 m = peer[(par * cl + q) * CW + v * 32 + lane];
-                    carry[v] = join<PACKED>(m.x, carry[v], m.y);
-                }
+                if (q == rank) in = carry;
+                carry = join<PACKED>(m[q * 32].a, carry, m[q * 32].u);
             }
         } else {
-#pragma unroll
-            for (int v = 0; v < VEC; ++v) {
-                in[v] = carry[v];
-                float ta = pa[v], tu = pu[v];
-                for (int w = warp; w < kWarps; ++w) {
-                    const float2 m = agg[par][w][v * 32 + lane];
-                    ta = join<PACKED>(m.x, ta);
-                    tu = join<PACKED>(m.x, tu, m.y);
-                }
-                carry[v] = join<PACKED>(ta, in[v], tu);
+            Map<V> t = pre;
+            for (int w = warp; w < kWarps; ++w) {
+                const Map<V> m = agg[par][w][lane];
+                t = Map<V>{join<PACKED>(m.a, t.a), join<PACKED>(m.a, t.u, m.u)};
             }
+            carry = join<PACKED>(t.a, in, t.u);
         }
-        float s[VEC];
-#pragma unroll
-        for (int v = 0; v < VEC; ++v) s[v] = join<PACKED>(pa[v], in[v], pu[v]);
-        if (seg && mine && t0 < p.L && t0 % kSeg == 0) stv<VEC>(seg + (lead * nseg + t0 / kSeg) * p.D + c, s);
+        V s = join<PACKED>(pre.a, in, pre.u);
+        if (seg && mine && t0 < p.L && t0 % kSeg == 0) stv(seg + (lead * nseg + t0 / kSeg) * p.D + c, s);
 #pragma unroll
         for (int j = 0; j < ROWS; ++j) {
-            if (PACKED && (ri.start >> j & 1)) state_of<VEC>(h0, __shfl_sync(0xffffffffu, ri.n, j), p, head, cc, s);
-#pragma unroll
-            for (int v = 0; v < VEC; ++v) s[v] = fmaf(a[j][v], s[v], b[j][v]);
-            if (h && mine && (ri.valid >> j & 1)) stv<VEC>(h + first + ro.off[j], s);
+            if (PACKED && (ri.start >> j & 1)) s = state_of<V>(h0, __shfl_sync(0xffffffffu, ri.n, j), p, head, cc);
+            s = vfma(a[j], s, b[j]);
+            if (h && mine && (ri.valid >> j & 1)) stv(h + first + ro.off[j], s);
             if (PACKED && (ri.end >> j & 1)) {
                 const int64_t n = __shfl_sync(0xffffffffu, ri.n, j);
-                if (hT && mine) stv<VEC>(hT + (n * p.H + head) * p.D + c, s);
+                if (hT && mine) stv(hT + (n * p.H + head) * p.D + c, s);
             }
         }
         // rows behind the last one leave the state as it is, so the warp with the last row holds hT
-        if (!PACKED && hT && mine && t0 < p.L && t0 + ROWS >= p.L) stv<VEC>(hT + lead * p.D + c, s);
+        if (!PACKED && hT && mine && t0 < p.L && t0 + ROWS >= p.L) stv(hT + lead * p.D + c, s);
     }
+    ex.end();
 }
 
 // ---- backward -----------------------------------------------------------------------------
 // Rounds, blocks and warps as in the forward, from the last round to the first. The states inside a block's rows
 // are recomputed in fp32 from the state that enters them (seg).
-template <typename T, int VEC, bool PACKED, bool PREACT>
+template <typename T, int VEC, bool PACKED, bool PREACT, bool LEAK>
 __global__ void __launch_bounds__(kThreads, 2)
-    k_scan_bwd(ScanProblem p, GateForm f, int cl, const T* __restrict__ x, const float* __restrict__ la,
+    k_scan_bwd(ScanProblem p, int cl, const T* __restrict__ x, const float* __restrict__ la,
                const int32_t* __restrict__ cu, const float* __restrict__ h0, const T* __restrict__ dh,
                const float* __restrict__ dhT, T* __restrict__ dx, float* __restrict__ dla, float* __restrict__ dh0,
-               const float* __restrict__ seg) {
-    constexpr int CW = 32 * VEC, ROWS = kSeg / kWarps;
-    __shared__ float2 aggu[2][kWarps][CW];
-    __shared__ float aggy[2][kWarps][CW];
-    extern __shared__ float2 peer[];  // [2][cl][CW] the blocks' maps, then the warps' stages
-    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-    const int rank = cl > 1 ? int(cluster_rank()) : 0;
-    const int64_t tiles = cdiv(p.D, CW);
-    const int64_t id = blockIdx.x / cl, lead = id / tiles, c = (id % tiles) * CW + lane * VEC;
-    const bool mine = c < p.D;
-    const int64_t cc = mine ? c : p.D - VEC;
-    const int64_t head = PACKED ? lead : 0;
-    char* stages = reinterpret_cast<char*>(peer + (cl > 1 ? 2 * cl * CW : 0)) + warp * 2 * kBwdStage<T, VEC, ROWS>;
-    const auto row_of = [&](int r) { return (int64_t(r) * cl + rank) * kSeg + warp * ROWS; };
-    const auto first_of = [&](int64_t t) { return (lead * p.L + (t < p.L ? t : p.L - 1)) * p.D + cc; };
-    const auto gates_at = [&](int par) { return reinterpret_cast<float*>(stages + par * kBwdStage<T, VEC, ROWS>) + lane * VEC; };
-    const auto x_at = [&](int par) {
-        return reinterpret_cast<T*>(stages + par * kBwdStage<T, VEC, ROWS> + ROWS * CW * 4) + lane * VEC;
-    };
-    const auto dh_at = [&](int par) { return x_at(par) + ROWS * CW; };
-    const auto stage = [&](int r) {
-        const int64_t t = row_of(r), i = first_of(t);
-        const RowOffsets<ROWS> ro(p.L - t, p.D);
-        stage_rows<float, VEC, ROWS>(gates_at(r & 1), la + i, ro);
-        stage_rows<T, VEC, ROWS>(x_at(r & 1), x + i, ro);
-        stage_rows<T, VEC, ROWS>(dh_at(r & 1), dh + i, ro);
-    };
+               const float* __restrict__ seg, int* err) {
+    using V = typename VecOf<VEC>::type;
+    constexpr int ROWS = kSeg / kWarps, STAGE = kBwdStage<T, VEC, ROWS>;
+    __shared__ Map<V> agg[2][kWarps][32];
+    __shared__ V aggy[2][kWarps][32];
+    __shared__ uint64_t bar[2];
+    __shared__ int abort_flag;
+    extern __shared__ __align__(16) char dyn[];  // the cluster's maps, then the warps' stages
+    const Place<T, VEC, ROWS, STAGE> at(p, cl, dyn + (cl > 1 ? 2 * cl * 32 * sizeof(Map<V>) : 0));
+    const int lane = at.lane, warp = at.warp, rank = at.rank;
+    const int64_t lead = at.lead, c = at.c, cc = at.cc, head = PACKED ? lead : 0;
+    const bool mine = at.mine;
     const int rounds = int(cdiv(p.L, int64_t(kSeg) * cl));
+    Exchange<V> ex{reinterpret_cast<Map<V>*>(dyn), bar, &abort_flag, err, cl, rank, rounds};
+    const auto stage = [&](int r) {
+        const int64_t t = at.row(r), i = at.first(t);
+        const RowOffsets<ROWS> ro(p.L - t, p.D);
+        stage_rows<float, VEC, ROWS>(at.gates(r & 1), la + i, ro);
+        stage_rows<T, VEC, ROWS>(at.elems(r & 1, 0), x + i, ro);
+        stage_rows<T, VEC, ROWS>(at.elems(r & 1, 1), dh + i, ro);
+    };
     stage(rounds - 1);
     copies_commit();
-    if (cl > 1) cluster_arrive();
-    if constexpr (PACKED) copy_empty<VEC>(cu, int(p.B), p.H, head, p.D, c, dhT, dh0, rank * kWarps + warp, cl * kWarps, lane);
-    float carry[VEC] = {};  // y of the row behind the round's last
-    if (!PACKED && dhT) ldv<VEC>(dhT + lead * p.D + cc, carry);
-    if (cl > 1) cluster_wait();
+    ex.begin();
+    if constexpr (PACKED) copy_empty<V>(cu, p, head, c, mine, dhT, dh0, rank * kWarps + warp, cl * kWarps, lane);
+    V carry = vset<V>(0.f);  // y of the row behind the round's last
+    if (!PACKED && dhT) carry = ldv<V>(dhT + lead * p.D + cc);
+    ex.ready();
     const int64_t nseg = cdiv(p.L, kSeg);
-    for (int r = rounds - 1; r >= 0; --r) {
-        const int par = r & 1;
-        const int64_t tile = int64_t(r) * cl + rank, t0 = row_of(r), first = first_of(t0);
+    for (int it = 0; it < rounds; ++it) {
+        const int r = rounds - 1 - it, par = r & 1;
+        const int64_t t0 = at.row(r), first = at.first(t0), tile = int64_t(r) * cl + rank;
         const RowOffsets<ROWS> ro(p.L - t0, p.D);
-        float a[ROWS][VEC], w[ROWS][VEC], xv[ROWS][VEC], d[ROWS][VEC], dz[ROWS][VEC];
-        float s[VEC];  // state entering the block's rows
-        ldv<VEC>(seg + (lead * nseg + (tile < nseg ? tile : nseg - 1)) * p.D + cc, s);
+        V s = ldv<V>(seg + (lead * nseg + (tile < nseg ? tile : nseg - 1)) * p.D + cc);  // entering the block's rows
         if (r > 0) stage(r - 1);
         copies_commit();
         copies_wait<1>();
-#pragma unroll
-        for (int j = 0; j < ROWS; ++j) {
-            ldv<VEC>(gates_at(par) + j * CW, a[j]);
-            take_row<T, VEC>(x_at(par), x + first, ro.off[j], j, xv[j]);
-            take_row<T, VEC>(dh_at(par), dh + first, ro.off[j], j, d[j]);
-        }
         RowInfo ri{0, 0, 0, 0};
         if constexpr (PACKED) ri = rows_packed<ROWS>(cu, int(p.B), t0, p.L, lane);
         else ri.valid = t0 + ROWS <= p.L ? ~0u : t0 < p.L ? (1u << (p.L - t0)) - 1 : 0u;
+        V a[ROWS], w[ROWS], xv[ROWS], d[ROWS], dz[ROWS];
 #pragma unroll
         for (int j = 0; j < ROWS; ++j) {
-#pragma unroll
-            for (int v = 0; v < VEC; ++v) gate_of<PREACT>(f, a[j][v], a[j][v], w[j][v], dz[j][v]);
+            gate_of<PREACT, LEAK>(p.inv_tau, ldv<V>(at.gates(par) + j * 32 * VEC), a[j], w[j], dz[j]);
+            xv[j] = take_row<V>(at.elems(par, 0), x + first, ro.off[j], j);
+            d[j] = take_row<V>(at.elems(par, 1), dh + first, ro.off[j], j);
         }
         constexpr uint32_t kAll = (1u << ROWS) - 1;
         if ((ri.valid & kAll) != kAll) {
 #pragma unroll
             for (int j = 0; j < ROWS; ++j) {
                 if (!(ri.valid >> j & 1)) {
-#pragma unroll
-                    for (int v = 0; v < VEC; ++v) a[j][v] = 1.f, w[j][v] = 0.f, xv[j][v] = 0.f, d[j][v] = 0.f;
+                    a[j] = vset<V>(1.f);
+                    w[j] = xv[j] = d[j] = vset<V>(0.f);
                 }
             }
         }
-        float A[VEC], U[VEC], Y[VEC];
-#pragma unroll
-        for (int v = 0; v < VEC; ++v) A[v] = 1.f, U[v] = 0.f, Y[v] = 0.f;
+        Map<V> own{vset<V>(1.f), vset<V>(0.f)};
+        V Y = vset<V>(0.f);
 #pragma unroll
         for (int j = 0; j < ROWS; ++j) {
-            if (PACKED && (ri.start >> j & 1)) state_of<VEC>(h0, __shfl_sync(0xffffffffu, ri.n, j), p, head, cc, U);
-#pragma unroll
-            for (int v = 0; v < VEC; ++v) {
-                A[v] *= a[j][v];
-                U[v] = fmaf(a[j][v], U[v], w[j][v] * xv[j][v]);
-            }
+            if (PACKED && (ri.start >> j & 1)) own.u = state_of<V>(h0, __shfl_sync(0xffffffffu, ri.n, j), p, head, cc);
+            own.a = vmul(own.a, a[j]);
+            own.u = vfma(a[j], own.u, LEAK ? vmul(w[j], xv[j]) : xv[j]);
         }
 #pragma unroll
         for (int j = ROWS - 1; j >= 0; --j) {
-            if (PACKED && (ri.end >> j & 1)) {  // the gradient of the last state enters here, in place of the next row's
-                float e[VEC];
-                state_of<VEC>(dhT, __shfl_sync(0xffffffffu, ri.n, j), p, head, cc, e);
-#pragma unroll
-                for (int v = 0; v < VEC; ++v) d[j][v] += e[v];
-            }
-#pragma unroll
-            for (int v = 0; v < VEC; ++v) {
-                Y[v] = a[j][v] * (d[j][v] + Y[v]);
-                if (PACKED && (ri.start >> j & 1)) Y[v] = 0.f;
-            }
+            if (PACKED && (ri.end >> j & 1))  // the gradient of the last state enters here, in place of the next row's
+                d[j] = vadd(d[j], state_of<V>(dhT, __shfl_sync(0xffffffffu, ri.n, j), p, head, cc));
+            Y = vmul(a[j], vadd(d[j], Y));
+            if (PACKED && (ri.start >> j & 1)) Y = vset<V>(0.f);
         }
-        if (PACKED && ri.start) {  // of both directions: U and Y carry what the warp's other rows hold
-#pragma unroll
-            for (int v = 0; v < VEC; ++v) A[v] = kForget;
-        }
-#pragma unroll
-        for (int v = 0; v < VEC; ++v) {
-            aggu[par][warp][v * 32 + lane] = make_float2(A[v], U[v]);
-            aggy[par][warp][v * 32 + lane] = Y[v];
-        }
+        // forgetting holds in both directions: u and Y carry what the warp's other rows hold
+        if (PACKED && ri.start) own.a = vset<V>(kForget);
+        agg[par][warp][lane] = own;
+        aggy[par][warp][lane] = Y;
         __syncthreads();
-        float pa[VEC], py[VEC];  // the map (of y) of the block's rows behind this warp's
+        Map<V> post{vset<V>(1.f), vset<V>(0.f)};  // the map (of y) of the block's rows behind this warp's
 #pragma unroll
-        for (int v = 0; v < VEC; ++v) pa[v] = 1.f, py[v] = 0.f;
-#pragma unroll
-        for (int q = 0; q < kWarps; ++q) {
+        for (int q = 0; q < kWarps - 1; ++q) {
             if (q < warp) {
-#pragma unroll
-                for (int v = 0; v < VEC; ++v) {
-                    const float2 m = aggu[par][q][v * 32 + lane];
-                    s[v] = join<PACKED>(m.x, s[v], m.y);
-                }
+                const Map<V> m = agg[par][q][lane];
+                s = join<PACKED>(m.a, s, m.u);
             }
         }
 #pragma unroll
         for (int q = kWarps - 1; q > 0; --q) {
             if (q > warp) {
-#pragma unroll
-                for (int v = 0; v < VEC; ++v) {
-                    const float m = aggu[par][q][v * 32 + lane].x;
-                    pa[v] = join<PACKED>(m, pa[v]);
-                    py[v] = join<PACKED>(m, py[v], aggy[par][q][v * 32 + lane]);
-                }
+                const V m = agg[par][q][lane].a;
+                post = Map<V>{join<PACKED>(m, post.a), join<PACKED>(m, post.u, aggy[par][q][lane])};
             }
         }
-        float in[VEC];
+        V in = carry;
         if (cl > 1) {
-            if (warp == 0) {
-#pragma unroll
-                for (int v = 0; v < VEC; ++v) {
-                    const float2 m = make_float2(join<PACKED>(A[v], pa[v]), join<PACKED>(A[v], py[v], Y[v]));
-                    for (int q = 0; q < cl; ++q) st_peer(peer + (par * cl + rank) * CW + v * 32 + lane, q, m);
-                }
-            }
-            cluster_arrive();
-            cluster_wait();
+            if (warp == 0) ex.put(it, Map<V>{join<PACKED>(own.a, post.a), join<PACKED>(own.a, post.u, Y)});
+            const Map<V>* m = ex.get(it);
             for (int q = cl - 1; q >= 0; --q) {
-#pragma unroll
-                for (int v = 0; v < VEC; ++v) {
-                    if (q == rank) in[v] = carry[v];
-                    const float2 m = peer[(par * cl + q) * CW + v * 32 + lane];
-                    carry[v] = join<PACKED>(m.x, carry[v], m.y);
-                }
+                if (q == rank) in = carry;
+                carry = join<PACKED>(m[q * 32].a, carry, m[q * 32].u);
             }
         } else {
-#pragma unroll
-            for (int v = 0; v < VEC; ++v) {
-                in[v] = carry[v];
-                float ta = pa[v], ty = py[v];
-                for (int q = warp; q >= 0; --q) {
-                    const float m = aggu[par][q][v * 32 + lane].x;
-                    ta = join<PACKED>(m, ta);
-                    ty = join<PACKED>(m, ty, aggy[par][q][v * 32 + lane]);
-                }
-                carry[v] = join<PACKED>(ta, in[v], ty);
+            Map<V> t = post;
+            for (int q = warp; q >= 0; --q) {
+                const V m = agg[par][q][lane].a;
+                t = Map<V>{join<PACKED>(m, t.a), join<PACKED>(m, t.u, aggy[par][q][lane])};
             }
+            carry = join<PACKED>(t.a, in, t.u);
         }
-        float y[VEC];
-#pragma unroll
-        for (int v = 0; v < VEC; ++v) y[v] = join<PACKED>(pa[v], in[v], py[v]);
+        V y = join<PACKED>(post.a, in, post.u);
         // xv becomes what dlog a_t multiplies: h_{t-1}, less x_t where the input's weight is 1 - a
 #pragma unroll
         for (int j = 0; j < ROWS; ++j) {
-            if (PACKED && (ri.start >> j & 1)) state_of<VEC>(h0, __shfl_sync(0xffffffffu, ri.n, j), p, head, cc, s);
-#pragma unroll
-            for (int v = 0; v < VEC; ++v) {
-                const float xj = xv[j][v];
-                xv[j][v] = f.leak ? s[v] - xj : s[v];
-                s[v] = fmaf(a[j][v], s[v], w[j][v] * xj);
-            }
+            if (PACKED && (ri.start >> j & 1)) s = state_of<V>(h0, __shfl_sync(0xffffffffu, ri.n, j), p, head, cc);
+            const V xj = xv[j];
+            xv[j] = LEAK ? vfma(xj, vset<V>(-1.f), s) : s;
+            s = vfma(a[j], s, LEAK ? vmul(w[j], xj) : xj);
         }
 #pragma unroll
         for (int j = ROWS - 1; j >= 0; --j) {
-            float o1[VEC], o2[VEC];
-#pragma unroll
-            for (int v = 0; v < VEC; ++v) {
-                const float g = d[j][v] + y[v];
-                y[v] = a[j][v] * g;
-                o1[v] = w[j][v] * g;
-                o2[v] = y[v] * xv[j][v];
-                if constexpr (PREACT) o2[v] *= dz[j][v];
-            }
+            const V g = vadd(d[j], y);
+            y = vmul(a[j], g);
             if (mine && (ri.valid >> j & 1)) {
-                stv<VEC>(dx + first + ro.off[j], o1);
-                stv<VEC>(dla + first + ro.off[j], o2);
+                stv(dx + first + ro.off[j], LEAK ? vmul(w[j], g) : g);
+                const V o = vmul(y, xv[j]);
+                stv(dla + first + ro.off[j], PREACT ? vmul(o, dz[j]) : o);
             }
             if (PACKED && (ri.start >> j & 1)) {
                 const int64_t n = __shfl_sync(0xffffffffu, ri.n, j);
-                if (dh0 && mine) stv<VEC>(dh0 + (n * p.H + head) * p.D + c, y);
-#pragma unroll
-                for (int v = 0; v < VEC; ++v) y[v] = 0.f;
+                if (dh0 && mine) stv(dh0 + (n * p.H + head) * p.D + c, y);
+                y = vset<V>(0.f);
             }
         }
-        if (!PACKED && dh0 && mine && t0 == 0) stv<VEC>(dh0 + lead * p.D + c, y);
+        if (!PACKED && dh0 && mine && t0 == 0) stv(dh0 + lead * p.D + c, y);
     }
+    ex.end();
 }
 
 // ---- one token ----------------------------------------------------------------------------
@@ -645,7 +668,7 @@ __device__ __forceinline__ bool named_before(const int32_t* slots, int64_t b, in
 }
 
 template <typename T>
-__global__ void __launch_bounds__(kStepThreads) k_scan_step(ScanProblem p, GateForm f, const T* __restrict__ x,
+__global__ void __launch_bounds__(kStepThreads) k_scan_step(ScanProblem p, const T* __restrict__ x,
                                                         const float* __restrict__ la,
                                                         const int32_t* __restrict__ slots, int64_t pool,
                                                         float* __restrict__ state, T* __restrict__ h, int* err) {
@@ -665,17 +688,15 @@ __global__ void __launch_bounds__(kStepThreads) k_scan_step(ScanProblem p, GateF
     if (c >= n) return;
     float y = 0.f;
     if (live) {
-        float a, w;
-        float dz;
-        if (f.preact) gate_of<true>(f, la[b * n + c], a, w, dz);
-        else gate_of<false>(f, la[b * n + c], a, w, dz);
-        y = fmaf(a, state[slot * n + c], w * ldf(x + b * n + c));
+        float a, w, dz;
+        const float g = la[b * n + c], xv = ldf(x + b * n + c);
+        if (p.preact) gate_of<true, true>(p.inv_tau, g, a, w, dz);
+        else gate_of<false, true>(p.inv_tau, g, a, w, dz);
+        y = fmaf(a, state[slot * n + c], p.leak ? w * xv : xv);
         state[slot * n + c] = y;
     }
     stf(h + b * n + c, y);
 }
-
-GateForm form(const ScanProblem& p) { return GateForm{p.preact, p.leak, p.inv_tau}; }
 
 // Blocks per cluster: as many as the SMs hold at once (`slots`) where the sequences and channel tiles alone do not
 // fill them, but no more than there are row tiles. A grid that just exceeds the slots would run a second, nearly
@@ -691,7 +712,7 @@ constexpr int kSms = 148;
 
 template <int VEC>
 size_t smem_of(int cl, int stage_bytes) {
-    return (cl > 1 ? size_t(2) * cl * 32 * VEC * sizeof(float2) : 0) + size_t(2) * kWarps * stage_bytes;
+    return (cl > 1 ? size_t(2) * cl * 32 * sizeof(Map<typename VecOf<VEC>::type>) : 0) + size_t(2) * kWarps * stage_bytes;
 }
 
 template <typename K, typename... Args>
@@ -720,46 +741,48 @@ gla_status launch_clusters(const char* name, K kernel, int64_t groups, int cl, s
 constexpr int kFwdRows = 8;
 constexpr int kFwdBlocks = 3, kBwdBlocks = 2;  // blocks per SM
 
-template <typename T, int VEC, bool PACKED, bool PREACT>
+template <typename T, int VEC, bool PACKED, bool PREACT, bool LEAK>
 gla_status fwd_typed(const ScanProblem& p, const void* x, const float* la, const int32_t* cu, const float* h0,
                      void* h, float* hT, float* seg, cudaStream_t s) {
     const int64_t groups = (PACKED ? p.H : p.B * p.H) * cdiv(p.D, 32 * VEC);
     const int cl = cluster_size(groups, p.L, kWarps * kFwdRows, kSms * kFwdBlocks);
-    return launch_clusters("scan_fwd", k_scan_fwd<T, VEC, PACKED, PREACT, kFwdRows>, groups, cl,
-                           smem_of<VEC>(cl, kFwdStage<T, VEC, kFwdRows>), s, p, form(p), cl, static_cast<const T*>(x),
-                           la, cu, h0, static_cast<T*>(h), hT, seg);
+    return launch_clusters("scan_fwd", k_scan_fwd<T, VEC, PACKED, PREACT, LEAK, kFwdRows>, groups, cl,
+                           smem_of<VEC>(cl, kFwdStage<T, VEC, kFwdRows>), s, p, cl, static_cast<const T*>(x), la, cu, h0,
+                           static_cast<T*>(h), hT, seg, device_error_word());
 }
 
-template <typename T, int VEC, bool PACKED, bool PREACT>
+template <typename T, int VEC, bool PACKED, bool PREACT, bool LEAK>
 gla_status bwd_typed(const ScanProblem& p, const void* x, const float* la, const int32_t* cu, const float* h0,
                      const void* dh, const float* dhT, void* dx, float* dla, float* dh0, const float* seg,
                      cudaStream_t s) {
     const int64_t groups = (PACKED ? p.H : p.B * p.H) * cdiv(p.D, 32 * VEC);
     const int cl = cluster_size(groups, p.L, kSeg, kSms * kBwdBlocks);
-    return launch_clusters("scan_bwd", k_scan_bwd<T, VEC, PACKED, PREACT>, groups, cl,
-                           smem_of<VEC>(cl, kBwdStage<T, VEC, kSeg / kWarps>), s, p, form(p), cl,
-                           static_cast<const T*>(x), la, cu, h0, static_cast<const T*>(dh), dhT, static_cast<T*>(dx),
-                           dla, dh0, seg);
+    return launch_clusters("scan_bwd", k_scan_bwd<T, VEC, PACKED, PREACT, LEAK>, groups, cl,
+                           smem_of<VEC>(cl, kBwdStage<T, VEC, kSeg / kWarps>), s, p, cl, static_cast<const T*>(x),
+                           la, cu, h0, static_cast<const T*>(dh), dhT, static_cast<T*>(dx), dla, dh0, seg,
+                           device_error_word());
 }
 
 template <typename T>
 gla_status step_typed(const ScanProblem& p, const void* x, const float* la, const int32_t* slots, int64_t pool,
                       float* state, void* h, cudaStream_t s) {
     const dim3 grid(unsigned(cdiv(p.H * p.D, kStepThreads)), unsigned(p.B));
-    GLA_LAUNCH("scan_step", k_scan_step<T>, grid, kStepThreads, 0, s, p, form(p), static_cast<const T*>(x), la, slots,
+    GLA_LAUNCH("scan_step", k_scan_step<T>, grid, kStepThreads, 0, s, p, static_cast<const T*>(x), la, slots,
                pool, state, static_cast<T*>(h), device_error_word());
     return GLA_OK;
 }
 
-// Calls fn(type tag, channels a lane, packed, pre-activation) with compile-time values: two channels a lane where the
-// rows' pairs are aligned (an even width), else one.
+// Calls fn(type tag, channels a lane, packed, pre-activation, leak) with compile-time values: two channels a lane where
+// the rows' pairs are aligned (an even width), else one.
 template <typename F>
 gla_status dispatch(const ScanProblem& p, F fn) {
+    const auto flag = [](bool b, auto then) { return b ? then(std::true_type{}) : then(std::false_type{}); };
     const auto by_form = [&](auto type, auto vec) {
-        if (p.packed) return p.preact ? fn(type, vec, std::true_type{}, std::true_type{})
-                                      : fn(type, vec, std::true_type{}, std::false_type{});
-        return p.preact ? fn(type, vec, std::false_type{}, std::true_type{})
-                        : fn(type, vec, std::false_type{}, std::false_type{});
+        return flag(p.packed, [&](auto packed) {
+            return flag(p.preact, [&](auto preact) {
+                return flag(p.leak, [&](auto leak) { return fn(type, vec, packed, preact, leak); });
+            });
+        });
     };
     using One = std::integral_constant<int, 1>;
     using Two = std::integral_constant<int, 2>;
@@ -776,8 +799,8 @@ size_t scan_workspace(const ScanProblem& p, Arena& a) {
 
 gla_status scan_fwd(const ScanProblem& p, const void* x, const float* la, const int32_t* cu, const float* h0, void* h,
                     float* hT, float* seg, cudaStream_t s) {
-    return dispatch(p, [&](auto type, auto vec, auto packed, auto preact) {
-        return fwd_typed<decltype(type), vec(), packed(), preact()>(p, x, la, cu, h0, h, hT, seg, s);
+    return dispatch(p, [&](auto type, auto vec, auto packed, auto preact, auto leak) {
+        return fwd_typed<decltype(type), vec(), packed(), preact(), leak()>(p, x, la, cu, h0, h, hT, seg, s);
     });
 }
 
@@ -788,8 +811,8 @@ gla_status scan_bwd(const ScanProblem& p, const void* x, const float* la, const 
         const gla_status st = scan_fwd(p, x, la, cu, h0, nullptr, nullptr, seg, s);
         if (st != GLA_OK) return st;
     }
-    return dispatch(p, [&](auto type, auto vec, auto packed, auto preact) {
-        return bwd_typed<decltype(type), vec(), packed(), preact()>(p, x, la, cu, h0, dh, dhT, dx, dla, dh0, seg, s);
+    return dispatch(p, [&](auto type, auto vec, auto packed, auto preact, auto leak) {
+        return bwd_typed<decltype(type), vec(), packed(), preact(), leak()>(p, x, la, cu, h0, dh, dhT, dx, dla, dh0, seg, s);
     });
 }
 
