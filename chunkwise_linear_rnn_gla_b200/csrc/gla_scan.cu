@@ -698,30 +698,59 @@ __global__ void __launch_bounds__(kStepThreads) k_scan_step(ScanProblem p, const
     stf(h + b * n + c, y);
 }
 
-// Blocks per cluster: as many as the SMs hold at once (`slots`) where the sequences and channel tiles alone do not
-// fill them, but no more than there are row tiles. A grid that just exceeds the slots would run a second, nearly
-// empty wave.
-int cluster_size(int64_t groups, int64_t L, int tile, int64_t slots) {
-    int64_t cl = slots / groups;
-    const int64_t tiles = cdiv(L, tile);
-    cl = cl < tiles ? cl : tiles;
-    return int(cl < 1 ? 1 : cl < kMaxCluster ? cl : kMaxCluster);
+template <typename V>
+size_t smem_of(int cl, int stage_bytes) {
+    return (cl > 1 ? size_t(2) * cl * 32 * sizeof(Map<V>) : 0) + size_t(2) * kWarps * stage_bytes;
 }
 
-constexpr int kSms = 148;
+// How many clusters of each size the device holds at once, per kernel: a cluster sits inside one GPC, so large ones
+// leave some SMs empty. Asked once per kernel (the answer depends on nothing else).
+struct ClusterFit {
+    int fit[kMaxCluster + 1] = {};
+};
+template <typename K>
+ClusterFit ask_fit(K kernel, size_t (*smem)(int, int), int stage_bytes) {
+    ClusterFit f;
+    if (cudaFuncSetAttribute(kernel, cudaFuncAttributeNonPortableClusterSizeAllowed, 1) != cudaSuccess ||
+        cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, int(smem(kMaxCluster, stage_bytes))) !=
+            cudaSuccess)
+        return f;
+    for (int cl = 1; cl <= kMaxCluster; ++cl) {
+        cudaLaunchConfig_t cfg = {};
+        cfg.gridDim = dim3(unsigned(cl));
+        cfg.blockDim = dim3(kThreads);
+        cfg.dynamicSmemBytes = smem(cl, stage_bytes);
+        cudaLaunchAttribute attr[1];
+        attr[0].id = cudaLaunchAttributeClusterDimension;
+        attr[0].val.clusterDim.x = unsigned(cl);
+        attr[0].val.clusterDim.y = attr[0].val.clusterDim.z = 1;
+        cfg.attrs = attr;
+        cfg.numAttrs = 1;
+        int n = 0;
+        if (cudaOccupancyMaxActiveClusters(&n, kernel, &cfg) == cudaSuccess) f.fit[cl] = n;
+    }
+    return f;
+}
 
-template <int VEC>
-size_t smem_of(int cl, int stage_bytes) {
-    return (cl > 1 ? size_t(2) * cl * 32 * sizeof(Map<typename VecOf<VEC>::type>) : 0) + size_t(2) * kWarps * stage_bytes;
+// Blocks per cluster. A block's time goes by its rounds, and clusters that do not fit at once run in further waves:
+// the least waves x rounds, and of those the smallest cluster.
+int cluster_size(const ClusterFit& f, int64_t groups, int64_t L, int tile) {
+    const int64_t tiles = cdiv(L, tile);
+    int best = 1;
+    int64_t cost = INT64_MAX;
+    for (int cl = 1; cl <= kMaxCluster; ++cl) {
+        if (f.fit[cl] < 1 || cl > tiles) continue;
+        const int64_t c = cdiv(groups, int64_t(f.fit[cl])) * cdiv(tiles, int64_t(cl));
+        if (c < cost) cost = c, best = cl;
+    }
+    return best;
 }
 
 template <typename K, typename... Args>
-gla_status launch_clusters(const char* name, K kernel, int64_t groups, int cl, size_t smem, cudaStream_t s, Args... args) {
+gla_status launch_clusters(const char* name, K kernel, const ClusterFit& f, int64_t groups, int cl, size_t smem,
+                           cudaStream_t s, Args... args) {
+    if (f.fit[1] < 1) return GLA_ERR_CUDA;
     if (groups * cl > (int64_t(1) << 31) - 1) return GLA_ERR_UNSUPPORTED;
-    if (cl > 8 && cudaFuncSetAttribute(kernel, cudaFuncAttributeNonPortableClusterSizeAllowed, 1) != cudaSuccess)
-        return GLA_ERR_CUDA;
-    if (cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, int(smem)) != cudaSuccess)
-        return GLA_ERR_CUDA;
     launch_begin(name, s);
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3(unsigned(groups * cl));
@@ -739,15 +768,17 @@ gla_status launch_clusters(const char* name, K kernel, int64_t groups, int cl, s
 }
 
 constexpr int kFwdRows = 8;
-constexpr int kFwdBlocks = 3, kBwdBlocks = 2;  // blocks per SM
 
 template <typename T, int VEC, bool PACKED, bool PREACT, bool LEAK>
 gla_status fwd_typed(const ScanProblem& p, const void* x, const float* la, const int32_t* cu, const float* h0,
                      void* h, float* hT, float* seg, cudaStream_t s) {
     const int64_t groups = (PACKED ? p.H : p.B * p.H) * cdiv(p.D, 32 * VEC);
-    const int cl = cluster_size(groups, p.L, kWarps * kFwdRows, kSms * kFwdBlocks);
-    return launch_clusters("scan_fwd", k_scan_fwd<T, VEC, PACKED, PREACT, LEAK, kFwdRows>, groups, cl,
-                           smem_of<VEC>(cl, kFwdStage<T, VEC, kFwdRows>), s, p, cl, static_cast<const T*>(x), la, cu, h0,
+    using V = typename VecOf<VEC>::type;
+    const auto kernel = k_scan_fwd<T, VEC, PACKED, PREACT, LEAK, kFwdRows>;
+    constexpr int stage = kFwdStage<T, VEC, kFwdRows>;
+    static const ClusterFit fit = ask_fit(kernel, smem_of<V>, stage);
+    const int cl = cluster_size(fit, groups, p.L, kWarps * kFwdRows);
+    return launch_clusters("scan_fwd", kernel, fit, groups, cl, smem_of<V>(cl, stage), s, p, cl, static_cast<const T*>(x), la, cu, h0,
                            static_cast<T*>(h), hT, seg, device_error_word());
 }
 
@@ -756,9 +787,12 @@ gla_status bwd_typed(const ScanProblem& p, const void* x, const float* la, const
                      const void* dh, const float* dhT, void* dx, float* dla, float* dh0, const float* seg,
                      cudaStream_t s) {
     const int64_t groups = (PACKED ? p.H : p.B * p.H) * cdiv(p.D, 32 * VEC);
-    const int cl = cluster_size(groups, p.L, kSeg, kSms * kBwdBlocks);
-    return launch_clusters("scan_bwd", k_scan_bwd<T, VEC, PACKED, PREACT, LEAK>, groups, cl,
-                           smem_of<VEC>(cl, kBwdStage<T, VEC, kSeg / kWarps>), s, p, cl, static_cast<const T*>(x),
+    using V = typename VecOf<VEC>::type;
+    const auto kernel = k_scan_bwd<T, VEC, PACKED, PREACT, LEAK>;
+    constexpr int stage = kBwdStage<T, VEC, kSeg / kWarps>;
+    static const ClusterFit fit = ask_fit(kernel, smem_of<V>, stage);
+    const int cl = cluster_size(fit, groups, p.L, kSeg);
+    return launch_clusters("scan_bwd", kernel, fit, groups, cl, smem_of<V>(cl, stage), s, p, cl, static_cast<const T*>(x),
                            la, cu, h0, static_cast<const T*>(dh), dhT, static_cast<T*>(dx), dla, dh0, seg,
                            device_error_word());
 }
