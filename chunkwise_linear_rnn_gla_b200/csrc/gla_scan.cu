@@ -406,7 +406,7 @@ struct Place {
 // Grid: (sequence or head) x channel tile x cluster of `cl` blocks. Rows of round r and block q: from
 // (r cl + q) kWarps ROWS.
 template <typename T, int VEC, bool PACKED, bool PREACT, bool LEAK, int ROWS>
-__global__ void __launch_bounds__(kThreads, ROWS * VEC <= 16 ? 3 : 2)
+__global__ void __launch_bounds__(kThreads, 2)
     k_scan_fwd(ScanProblem p, int cl, const T* __restrict__ x, const float* __restrict__ la,
                const int32_t* __restrict__ cu, const float* __restrict__ h0, T* __restrict__ h, float* __restrict__ hT,
                float* __restrict__ seg, int* err) {
