@@ -62,6 +62,27 @@ def _need(t, name, shape, dtype, dev):
         raise ValueError("%s must be contiguous" % name)
 
 
+def _same(t, name, shape, dtype, dev):
+    """_need with a quick way through for the usual case (shape: a tuple or torch.Size)."""
+    if not (isinstance(t, torch.Tensor) and t.shape == shape and t.dtype is dtype and t.device == dev
+            and t.is_contiguous()):
+        _need(t, name, shape, dtype, dev)
+
+
+def _enqueue(dev: torch.device, what: str, fn, *args):
+    """fn(*args, stream) on dev's current stream with dev current; raises on a bad status. A decode step is a few
+    microseconds of device time, so the device is switched only where another one is current."""
+    if dev.type != "cuda":
+        raise ValueError("%s needs CUDA tensors, got %s" % (what, dev))
+    if dev.index == torch.cuda.current_device():
+        st = fn(*args, torch.cuda.current_stream().cuda_stream)
+    else:
+        with torch.cuda.device(dev):
+            st = fn(*args, torch.cuda.current_stream().cuda_stream)
+    if st != _lib.GLA_OK:
+        raise GlaError(st, what)
+
+
 def make_desc(B, H, L, Dk, Dv, dtype="bf16", chunk=0, subchunk=0, state_mode="auto", impl="auto",
               flags=0, gate="channel", tau=0.0) -> GlaDesc:
     """Problem descriptor. gate: what log_a holds -- "channel" (log alpha [B,H,L,Dk]), "scalar"

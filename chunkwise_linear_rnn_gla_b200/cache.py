@@ -19,7 +19,7 @@ import ctypes
 
 import torch
 
-from . import _check, _dt, _finish_checks, _lib, _need, _ptr, _stream, gate_shape, make_desc
+from . import _dt, _enqueue, _finish_checks, _lib, _need, _same, gate_shape, make_desc
 from ._lib import load
 
 __all__ = ["StateCache", "cache_store", "cache_load", "cache_step"]
@@ -49,10 +49,32 @@ class StateCache:
         _need(k, "k", (self.slots, self.H, self.window, self.Dk), k.dtype, dev)
         _need(v, "v", (self.slots, self.H, self.window, self.Dv), k.dtype, dev)
         _need(log_a, "log_a", k.shape, torch.float32, dev)
-        self.codes, self.scale, self.k, self.v, self.log_a = codes, scale, k, v, log_a
+        self._tensors = (codes, scale, k, v, log_a)  # fixed: the pool's addresses are handed to every call
         self.format, self.dtype, self.device = _FORMATS[codes.dtype], k.dtype, dev
+        self._descs = {}
         self._c = _lib.GlaCache(codes.data_ptr(), scale.data_ptr(), k.data_ptr(), v.data_ptr(), log_a.data_ptr(),
                                 self.slots, self.window, _lib.CACHE_FORMAT[self.format])
+        self._ref = ctypes.byref(self._c)
+
+    @property
+    def codes(self):
+        return self._tensors[0]
+
+    @property
+    def scale(self):
+        return self._tensors[1]
+
+    @property
+    def k(self):
+        return self._tensors[2]
+
+    @property
+    def v(self):
+        return self._tensors[3]
+
+    @property
+    def log_a(self):
+        return self._tensors[4]
 
     @classmethod
     def empty(cls, slots, H, Dk, Dv, *, window=16, format="int8", dtype=torch.bfloat16, device="cuda"):
@@ -67,8 +89,14 @@ class StateCache:
                    torch.zeros(slots, H, window, Dk, **f32))
 
     def _desc(self, B, gate="channel", tau=0.0, checks=False):
-        return make_desc(B, self.H, 1, self.Dk, self.Dv, "bf16" if self.dtype == torch.bfloat16 else "f32",
-                         flags=_lib.FLAG_CHECKS if checks else 0, gate=gate, tau=tau)
+        """A descriptor (which the library only reads) as an argument; made once per batch size and options."""
+        key = (B, gate, tau, checks)
+        d = self._descs.get(key)
+        if d is None:
+            d = self._descs[key] = ctypes.byref(make_desc(
+                B, self.H, 1, self.Dk, self.Dv, "bf16" if self.dtype == torch.bfloat16 else "f32",
+                flags=_lib.FLAG_CHECKS if checks else 0, gate=gate, tau=tau))
+        return d
 
 
 def _rows(cache, slots, lengths=None):
@@ -76,10 +104,16 @@ def _rows(cache, slots, lengths=None):
         raise TypeError("cache must be a StateCache")
     if not isinstance(slots, torch.Tensor) or slots.dim() != 1:
         raise ValueError("slots must be an int32 [B] tensor")
-    _need(slots, "slots", slots.shape, torch.int32, cache.device)
+    _same(slots, "slots", slots.shape, torch.int32, cache.device)
     if lengths is not None:
-        _need(lengths, "lengths", slots.shape, torch.int32, cache.device)
+        _same(lengths, "lengths", slots.shape, torch.int32, cache.device)
     return slots.shape[0]
+
+
+def _finish(dev, checks, what):
+    if checks:
+        with torch.cuda.device(dev):
+            _finish_checks([], what)
 
 
 def cache_store(cache, S, slots, *, checks=False):
@@ -87,13 +121,10 @@ def cache_store(cache, S, slots, *, checks=False):
     lib = load()
     B = _rows(cache, slots)
     dev = cache.device
-    _need(S, "S", (B, cache.H, cache.Dk, cache.Dv), torch.float32, dev)
+    _same(S, "S", (B, cache.H, cache.Dk, cache.Dv), torch.float32, dev)
     desc = cache._desc(B, checks=checks)
-    with torch.cuda.device(dev):
-        st = lib.gla_cache_store(ctypes.byref(desc), ctypes.byref(cache._c), _ptr(S), _ptr(slots), _stream(dev))
-        _check(st, "gla_cache_store")
-        if checks:
-            _finish_checks([], "gla_cache_store")
+    _enqueue(dev, "gla_cache_store", lib.gla_cache_store, desc, cache._ref, S.data_ptr(), slots.data_ptr())
+    _finish(dev, checks, "gla_cache_store")
 
 
 def cache_load(cache, slots, lengths=None, S=None, *, checks=False):
@@ -104,14 +135,11 @@ def cache_load(cache, slots, lengths=None, S=None, *, checks=False):
     dev = cache.device
     if S is None:
         S = torch.empty(B, cache.H, cache.Dk, cache.Dv, dtype=torch.float32, device=dev)
-    _need(S, "S", (B, cache.H, cache.Dk, cache.Dv), torch.float32, dev)
+    _same(S, "S", (B, cache.H, cache.Dk, cache.Dv), torch.float32, dev)
     desc = cache._desc(B, checks=checks)
-    with torch.cuda.device(dev):
-        st = lib.gla_cache_load(ctypes.byref(desc), ctypes.byref(cache._c), _ptr(slots), _ptr(lengths), _ptr(S),
-                                _stream(dev))
-        _check(st, "gla_cache_load")
-        if checks:
-            _finish_checks([], "gla_cache_load")
+    _enqueue(dev, "gla_cache_load", lib.gla_cache_load, desc, cache._ref, slots.data_ptr(),
+             None if lengths is None else lengths.data_ptr(), S.data_ptr())
+    _finish(dev, checks, "gla_cache_load")
     return S
 
 
@@ -123,18 +151,15 @@ def cache_step(cache, q, k, v, log_a, slots, lengths, o=None, *, gate="channel",
     if lengths is None:
         raise TypeError("cache_step needs lengths")
     dev, dt, H, Dk, Dv = cache.device, cache.dtype, cache.H, cache.Dk, cache.Dv
-    _need(q, "q", (B, H, Dk), dt, dev)
-    _need(k, "k", (B, H, Dk), dt, dev)
-    _need(v, "v", (B, H, Dv), dt, dev)
+    _same(q, "q", (B, H, Dk), dt, dev)
+    _same(k, "k", (B, H, Dk), dt, dev)
+    _same(v, "v", (B, H, Dv), dt, dev)
     desc = cache._desc(B, gate, tau, checks)
-    _need(log_a, "log_a", gate_shape(gate, B, H, None, Dk), torch.float32, dev)
+    _same(log_a, "log_a", gate_shape(gate, B, H, None, Dk), torch.float32, dev)
     if o is None:
         o = torch.empty(B, H, Dv, dtype=dt, device=dev)
-    _need(o, "o", (B, H, Dv), dt, dev)
-    with torch.cuda.device(dev):
-        st = lib.gla_cache_step(ctypes.byref(desc), ctypes.byref(cache._c), _ptr(q), _ptr(k), _ptr(v), _ptr(log_a),
-                                _ptr(slots), _ptr(lengths), _ptr(o), _stream(dev))
-        _check(st, "gla_cache_step")
-        if checks:
-            _finish_checks([], "gla_cache_step")
+    _same(o, "o", (B, H, Dv), dt, dev)
+    _enqueue(dev, "gla_cache_step", lib.gla_cache_step, desc, cache._ref, q.data_ptr(), k.data_ptr(), v.data_ptr(),
+             log_a.data_ptr(), slots.data_ptr(), lengths.data_ptr(), o.data_ptr())
+    _finish(dev, checks, "gla_cache_step")
     return o

@@ -17,24 +17,30 @@ gate="preact": log_a holds the gate's argument z, log a = logsigmoid(z) / tau.
 from __future__ import annotations
 
 import ctypes
+import functools
 from typing import Optional
 
 import torch
 
-from . import _check, _dt, _finish_checks, _lib, _need, _ptr, _stream, _workspace, make_desc
+from . import _dt, _enqueue, _finish_checks, _lib, _same, _workspace, make_desc
 from ._lib import load
 
 __all__ = ["scan_fwd", "scan_bwd", "scan_step", "scan_workspace_size", "scan_workspace"]
 
 
 def _write(write: str) -> int:
-    if write not in _lib.SCAN_WRITE:
+    w = _lib.SCAN_WRITE.get(write)
+    if w is None:
         raise ValueError("write must be one of %s, got %r" % (sorted(_lib.SCAN_WRITE), write))
-    return _lib.SCAN_WRITE[write]
+    return w
+
+
+def _addr(t):
+    return None if t is None else t.data_ptr()
 
 
 def _index(t, name, n, dev):
-    _need(t, name, (n,), torch.int32, dev)
+    _same(t, name, (n,), torch.int32, dev)
 
 
 def _sizes(x, cu_seqlens):
@@ -54,8 +60,24 @@ def _sizes(x, cu_seqlens):
     return cu_seqlens.numel() - 1, H, L, D
 
 
+@functools.lru_cache(maxsize=256)
+def _desc_ref(B, H, L, D, dtype, gate, tau, flags):
+    """A descriptor (which the library only reads) as an argument; made once per set of sizes and options."""
+    return ctypes.byref(make_desc(B, H, L, D, 1, dtype, flags=flags, gate=gate, tau=tau))
+
+
 def _desc(x, B, H, L, D, gate, tau, flags):
-    return make_desc(B, H, L, D, 1, _dt(x), flags=flags, gate=gate, tau=tau)
+    return _desc_ref(B, H, L, D, _dt(x), gate, tau, flags)
+
+
+def _flags(checks, ws_from_fwd=False):
+    return (_lib.FLAG_WS_FROM_FWD if ws_from_fwd else 0) | (_lib.FLAG_CHECKS if checks else 0)
+
+
+def _finish(dev, checks, what):
+    if checks:
+        with torch.cuda.device(dev):
+            _finish_checks([], what)
 
 
 def scan_workspace_size(desc, packed: bool = False) -> int:
@@ -66,14 +88,14 @@ def scan_workspace_size(desc, packed: bool = False) -> int:
 def scan_workspace(x, cu_seqlens=None, checks=False) -> torch.Tensor:
     """A workspace for scan_fwd and the scan_bwd that follows it."""
     B, H, L, D = _sizes(x, cu_seqlens)
-    d = _desc(x, B, H, L, D, "channel", 0.0, _lib.FLAG_CHECKS if checks else 0)
-    return torch.empty(scan_workspace_size(d, cu_seqlens is not None), dtype=torch.uint8, device=x.device)
+    n = load().gla_scan_workspace_size(_desc(x, B, H, L, D, "channel", 0.0, _flags(checks)), cu_seqlens is not None)
+    return torch.empty(n, dtype=torch.uint8, device=x.device)
 
 
 def _buffer(t, like, name, packed):
     if t is None:
         return torch.zeros_like(like) if packed else torch.empty_like(like)
-    _need(t, name, like.shape, like.dtype, like.device)
+    _same(t, name, like.shape, like.dtype, like.device)
     return t
 
 
@@ -85,24 +107,21 @@ def scan_fwd(x, log_a, h0=None, *, cu_seqlens=None, write="input", gate="channel
     lib = load()
     B, H, L, D = _sizes(x, cu_seqlens)
     dev = x.device
-    _need(log_a, "log_a", x.shape, torch.float32, dev)
+    _same(log_a, "log_a", x.shape, torch.float32, dev)
     if h0 is not None:
-        _need(h0, "h0", (B, H, D), torch.float32, dev)
-    desc = _desc(x, B, H, L, D, gate, tau, _lib.FLAG_CHECKS if checks else 0)
+        _same(h0, "h0", (B, H, D), torch.float32, dev)
+    desc = _desc(x, B, H, L, D, gate, tau, _flags(checks))
     h = _buffer(h, x, "h", cu_seqlens is not None)
     if hT is None and want_hT:
         hT = torch.empty(B, H, D, dtype=torch.float32, device=dev)
     if hT is not None:
-        _need(hT, "hT", (B, H, D), torch.float32, dev)
+        _same(hT, "hT", (B, H, D), torch.float32, dev)
     ws, nbytes = None, 0
     if workspace is not None:
-        ws, nbytes = _workspace(scan_workspace_size(desc, cu_seqlens is not None), dev, workspace)
-    with torch.cuda.device(dev):
-        st = lib.gla_scan_fwd(ctypes.byref(desc), _write(write), _ptr(x), _ptr(log_a), _ptr(cu_seqlens), _ptr(h0),
-                              _ptr(h), _ptr(hT), _ptr(ws), nbytes, _stream(dev))
-        _check(st, "gla_scan_fwd")
-        if checks:
-            _finish_checks([], "gla_scan_fwd")
+        ws, nbytes = _workspace(lib.gla_scan_workspace_size(desc, cu_seqlens is not None), dev, workspace)
+    _enqueue(dev, "gla_scan_fwd", lib.gla_scan_fwd, desc, _write(write), x.data_ptr(), log_a.data_ptr(),
+             _addr(cu_seqlens), _addr(h0), h.data_ptr(), _addr(hT), _addr(ws), nbytes)
+    _finish(dev, checks, "gla_scan_fwd")
     return h, hT
 
 
@@ -116,15 +135,14 @@ def scan_bwd(x, log_a, dh, h0=None, dhT=None, *, cu_seqlens=None, write="input",
     B, H, L, D = _sizes(x, cu_seqlens)
     dev = x.device
     packed = cu_seqlens is not None
-    _need(log_a, "log_a", x.shape, torch.float32, dev)
-    _need(dh, "dh", x.shape, x.dtype, dev)
+    _same(log_a, "log_a", x.shape, torch.float32, dev)
+    _same(dh, "dh", x.shape, x.dtype, dev)
     for t, n in ((h0, "h0"), (dhT, "dhT")):
         if t is not None:
-            _need(t, n, (B, H, D), torch.float32, dev)
+            _same(t, n, (B, H, D), torch.float32, dev)
     if ws_from_fwd and workspace is None:
         raise ValueError("ws_from_fwd needs the forward's workspace")
-    flags = (_lib.FLAG_WS_FROM_FWD if ws_from_fwd else 0) | (_lib.FLAG_CHECKS if checks else 0)
-    desc = _desc(x, B, H, L, D, gate, tau, flags)
+    desc = _desc(x, B, H, L, D, gate, tau, _flags(checks, ws_from_fwd))
     out = dict(out or {})
     dx = _buffer(out.get("dx"), x, "dx", packed)
     dla = _buffer(out.get("dlog_a"), log_a, "dlog_a", packed)
@@ -132,14 +150,12 @@ def scan_bwd(x, log_a, dh, h0=None, dhT=None, *, cu_seqlens=None, write="input",
     if dh0 is None and want_dh0:
         dh0 = torch.empty(B, H, D, dtype=torch.float32, device=dev)
     if dh0 is not None:
-        _need(dh0, "dh0", (B, H, D), torch.float32, dev)
-    ws, nbytes = _workspace(scan_workspace_size(desc, packed), dev, workspace)
-    with torch.cuda.device(dev):
-        st = lib.gla_scan_bwd(ctypes.byref(desc), _write(write), _ptr(x), _ptr(log_a), _ptr(cu_seqlens), _ptr(h0),
-                              _ptr(dh), _ptr(dhT), _ptr(dx), _ptr(dla), _ptr(dh0), _ptr(ws), nbytes, _stream(dev))
-        _check(st, "gla_scan_bwd")
-        if checks:
-            _finish_checks([], "gla_scan_bwd")
+        _same(dh0, "dh0", (B, H, D), torch.float32, dev)
+    ws, nbytes = _workspace(lib.gla_scan_workspace_size(desc, packed), dev, workspace)
+    _enqueue(dev, "gla_scan_bwd", lib.gla_scan_bwd, desc, _write(write), x.data_ptr(), log_a.data_ptr(),
+             _addr(cu_seqlens), _addr(h0), dh.data_ptr(), _addr(dhT), dx.data_ptr(), dla.data_ptr(), _addr(dh0),
+             _addr(ws), nbytes)
+    _finish(dev, checks, "gla_scan_bwd")
     return {"dx": dx, "dlog_a": dla, "dh0": dh0}
 
 
@@ -153,23 +169,20 @@ def scan_step(x, log_a, state, slots=None, *, write="input", gate="channel", tau
         raise ValueError("x must be a [B, H, D] tensor")
     dev = x.device
     B, H, D = x.shape
-    _need(x, "x", x.shape, x.dtype, dev)
-    _need(log_a, "log_a", x.shape, torch.float32, dev)
+    _same(x, "x", x.shape, x.dtype, dev)
+    _same(log_a, "log_a", x.shape, torch.float32, dev)
     if not isinstance(state, torch.Tensor) or state.dim() != 3:
         raise ValueError("state must be a [pool, H, D] tensor")
-    _need(state, "state", (state.shape[0], H, D), torch.float32, dev)
+    _same(state, "state", (state.shape[0], H, D), torch.float32, dev)
     if slots is not None:
         _index(slots, "slots", B, dev)
     elif state.shape[0] < B:
         raise ValueError("state has %d entries for %d rows" % (state.shape[0], B))
     if h is None:
         h = torch.empty_like(x)
-    _need(h, "h", x.shape, x.dtype, dev)
-    desc = _desc(x, B, H, 1, D, gate, tau, _lib.FLAG_CHECKS if checks else 0)
-    with torch.cuda.device(dev):
-        st = lib.gla_scan_step(ctypes.byref(desc), _write(write), _ptr(x), _ptr(log_a), _ptr(slots), state.shape[0],
-                               _ptr(state), _ptr(h), _stream(dev))
-        _check(st, "gla_scan_step")
-        if checks:
-            _finish_checks([], "gla_scan_step")
+    _same(h, "h", x.shape, x.dtype, dev)
+    desc = _desc(x, B, H, 1, D, gate, tau, _flags(checks))
+    _enqueue(dev, "gla_scan_step", lib.gla_scan_step, desc, _write(write), x.data_ptr(), log_a.data_ptr(),
+             _addr(slots), state.shape[0], state.data_ptr(), h.data_ptr())
+    _finish(dev, checks, "gla_scan_step")
     return h
