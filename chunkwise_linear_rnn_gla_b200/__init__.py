@@ -69,16 +69,20 @@ def _same(t, name, shape, dtype, dev):
         _need(t, name, shape, dtype, dev)
 
 
+# the current stream's handle without a Stream object around it, where torch offers that
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None) or (lambda i: torch.cuda.current_stream(i).cuda_stream)
+
+
 def _enqueue(dev: torch.device, what: str, fn, *args):
     """fn(*args, stream) on dev's current stream with dev current; raises on a bad status. A decode step is a few
     microseconds of device time, so the device is switched only where another one is current."""
     if dev.type != "cuda":
         raise ValueError("%s needs CUDA tensors, got %s" % (what, dev))
     if dev.index == torch.cuda.current_device():
-        st = fn(*args, torch.cuda.current_stream().cuda_stream)
+        st = fn(*args, _raw_stream(dev.index))
     else:
         with torch.cuda.device(dev):
-            st = fn(*args, torch.cuda.current_stream().cuda_stream)
+            st = fn(*args, _raw_stream(dev.index))
     if st != _lib.GLA_OK:
         raise GlaError(st, what)
 

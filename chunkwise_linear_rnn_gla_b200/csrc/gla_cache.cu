@@ -43,26 +43,28 @@ struct Pool {
 };
 
 // ---- 8-bit codes --------------------------------------------------------------------------
-// Four codes to fp32, exactly.
+// Four codes to fp32, exactly. int8: 2^23 + 128 + code has the biased code in its low byte, and the subtraction is
+// exact.
 template <bool INT8>
-__device__ __forceinline__ void decode4(uint32_t x, float* y) {
+__device__ __forceinline__ void decode4(uint32_t x, float2* y) {
     if constexpr (INT8) {
-        // 2^23 + 128 + code has the biased code in its low byte; the subtraction is exact
         const uint32_t u = x ^ 0x80808080u;
-#pragma unroll
-        for (int e = 0; e < 4; ++e)
-            y[e] = __uint_as_float(__byte_perm(u, 0x4B000000u, 0x7440u + e)) - 8388736.f;
+        const float2 off = make_float2(-8388736.f, -8388736.f);
+        y[0] = add2(make_float2(__uint_as_float(__byte_perm(u, 0x4B000000u, 0x7440u)),
+                                __uint_as_float(__byte_perm(u, 0x4B000000u, 0x7441u))), off);
+        y[1] = add2(make_float2(__uint_as_float(__byte_perm(u, 0x4B000000u, 0x7442u)),
+                                __uint_as_float(__byte_perm(u, 0x4B000000u, 0x7443u))), off);
     } else {
-        const __half2_raw lo = __nv_cvt_fp8x2_to_halfraw2(__nv_fp8x2_storage_t(x & 0xffffu), __NV_E4M3);
-        const __half2_raw hi = __nv_cvt_fp8x2_to_halfraw2(__nv_fp8x2_storage_t(x >> 16), __NV_E4M3);
-        const float2 a = __half22float2(__half2(lo)), b = __half22float2(__half2(hi));
-        y[0] = a.x;
-        y[1] = a.y;
-        y[2] = b.x;
-        y[3] = b.y;
+        y[0] = __half22float2(__half2(__nv_cvt_fp8x2_to_halfraw2(__nv_fp8x2_storage_t(x & 0xffffu), __NV_E4M3)));
+        y[1] = __half22float2(__half2(__nv_cvt_fp8x2_to_halfraw2(__nv_fp8x2_storage_t(x >> 16), __NV_E4M3)));
     }
 }
-
+template <bool INT8>
+__device__ __forceinline__ void decode4(uint32_t x, float* y) {
+    float2 t[2];
+    decode4<INT8>(x, t);
+    y[0] = t[0].x, y[1] = t[0].y, y[2] = t[1].x, y[3] = t[1].y;
+}
 // scale of a group from the bits of its largest magnitude (NaN and inf order above every finite value)
 template <bool INT8>
 __device__ __forceinline__ float scale_of(uint32_t amax_bits) {
@@ -426,6 +428,285 @@ __global__ void __launch_bounds__(kThreads, 3) k_cache_step(Pool c, const T* __r
     }
 }
 
+// ---- step, streamed ---------------------------------------------------------------------------
+// For the shapes that bulk copies can move (stream_plan below). One persistent block per SM takes whole heads in turn. A
+// producer warp keeps copies in flight without a pause, across heads: a head's codes are one contiguous stretch,
+// fetched in chunks of about 16 KB through a ring, and the token, the window and the scales of the next head travel
+// while this one is computed. 16 warps read the chunks (16 codes a lane), so memory never waits for the window's
+// exponentials or the reductions. The kernel above spends most of a block's time on that chain of latencies: 101 us
+// against 35 us here for 1024 heads of 256 x 512 (134 MB of codes: 20.5 us at the measured copy bandwidth).
+constexpr int kStreamThreads = 512;           // readers
+constexpr int kStreamWarps = kStreamThreads / 32;
+constexpr int kMaxRing = 8;
+constexpr size_t kStreamSmem = 227 * 1024;
+
+struct StreamPlan {
+    int heads;        // stages of token, window and scales: 1 or 2
+    int ring;         // chunks in flight
+    int chunk_rows;   // state rows of a chunk
+    int lanes;        // lanes that share a group's row (16 codes each)
+    int slices;       // rows read at a time
+    int off_k, off_v, off_g, off_kw, off_gw, off_vw, off_sc, head_bytes;  // within a stage
+    int off_kt, off_dec, off_wq, off_p, off_red, off_ring, chunk_bytes;
+    size_t smem;
+};
+
+struct HeadInfo {
+    int64_t sh;  // slot * H + head
+    int n;       // tokens in the window
+    int live;
+};
+
+__device__ __forceinline__ void bulk_copy(void* dst, const void* src, uint32_t bytes, uint64_t* bar) {
+    asm volatile("cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];" ::"r"(
+                     tc::smem_u32(dst)),
+                 "l"(src), "r"(bytes), "r"(tc::smem_u32(bar))
+                 : "memory");
+}
+
+template <typename T, bool INT8>
+__global__ void __launch_bounds__(kStreamThreads + 32, 1)
+    k_cache_stream(Pool c, StreamPlan pl, int64_t items, const T* __restrict__ q, const T* __restrict__ k,
+                   const T* __restrict__ v, GateArgs ga, const int32_t* __restrict__ slots,
+                   const int32_t* __restrict__ lengths, T* __restrict__ o, int* err) {
+    extern __shared__ __align__(128) char dyn[];
+    __shared__ uint64_t head_full[2], head_empty[2], ring_full[kMaxRing], ring_empty[kMaxRing];
+    __shared__ HeadInfo info[2];
+    __shared__ int abort_flag;
+    const int tid = int(threadIdx.x), lane = tid & 31, warp = tid >> 5;
+    const int K = c.K, V = c.V, NG = c.NG;
+    const int chunks = (K + pl.chunk_rows - 1) / pl.chunk_rows;
+    const bool gate_rows = ga.kind == kGateChannel || ga.kind == kGatePreact;
+    if (tid == 0) {
+        abort_flag = 0;
+        for (int i = 0; i < 2; ++i) tc::mbar_init(head_full + i, 1), tc::mbar_init(head_empty + i, kStreamWarps);
+        for (int i = 0; i < kMaxRing; ++i) tc::mbar_init(ring_full + i, 1), tc::mbar_init(ring_empty + i, kStreamWarps);
+        tc::fence_barrier_init();
+    }
+    __syncthreads();
+    if (warp == kStreamWarps) {
+        // ---- producer: all lanes walk the items (they share the search for a slot named before), lane 0 copies
+        int it = 0;
+        uint32_t nch = 0;  // chunks issued
+        bool ok = true;
+        for (int64_t item = blockIdx.x; item < items && ok; item += gridDim.x, ++it) {
+            const int64_t b = item / c.H, head = item % c.H;
+            const int32_t slot = slots[b], len = lengths[b];
+            bool live = slot >= 0;
+            if (live) {
+                bool bad = slot >= c.slots || len < 0;
+                for (int64_t i = lane; i < b; i += 32) bad |= slots[i] == slot;
+                if (__any_sync(0xffffffffu, bad)) {
+                    live = false;
+                    if (lane == 0) atomicOr(err, kErrBadRow);
+                }
+            }
+            if (lane == 0) {
+                const int hs = it % pl.heads, turn = it / pl.heads;
+                if (turn > 0) ok = tc::mbar_wait(head_empty + hs, uint32_t(turn - 1) & 1u, err, &abort_flag);
+                const int n = live ? len % c.W : 0;
+                const int64_t sh = live ? slot * c.H + head : 0;
+                if (ok) {
+                    info[hs] = HeadInfo{sh, n, live ? 1 : 0};
+                    if (!live) tc::mbar_arrive(head_full + hs);
+                    else {
+                        char* st = dyn + hs * pl.head_bytes;
+                        const uint32_t kb = uint32_t(K) * sizeof(T), vb = uint32_t(V) * sizeof(T), gb = uint32_t(K) * 4u;
+                        const uint32_t sb = uint32_t(K) * NG * 4u;
+                        tc::mbar_arrive_expect_tx(head_full + hs, 2 * kb + vb + (gate_rows ? gb : 0u) + sb + n * (kb + gb + vb));
+                        bulk_copy(st, q + item * K, kb, head_full + hs);
+                        bulk_copy(st + pl.off_k, k + item * K, kb, head_full + hs);
+                        bulk_copy(st + pl.off_v, v + item * V, vb, head_full + hs);
+                        if (gate_rows) bulk_copy(st + pl.off_g, ga.g + item * K, gb, head_full + hs);
+                        bulk_copy(st + pl.off_sc, c.scale + sh * K * NG, sb, head_full + hs);
+                        if (n > 0) {
+                            bulk_copy(st + pl.off_kw, static_cast<T*>(c.k) + sh * c.W * K, n * kb, head_full + hs);
+                            bulk_copy(st + pl.off_gw, c.la + sh * c.W * K, n * gb, head_full + hs);
+                            bulk_copy(st + pl.off_vw, static_cast<T*>(c.v) + sh * c.W * V, n * vb, head_full + hs);
+                        }
+                    }
+                }
+                for (int ch = 0; ch < chunks && live && ok; ++ch, ++nch) {
+                    const uint32_t s = nch % pl.ring, t = nch / pl.ring;
+                    if (t > 0) ok = tc::mbar_wait(ring_empty + s, (t - 1) & 1u, err, &abort_flag);
+                    if (!ok) break;
+                    const int r0 = ch * pl.chunk_rows, rows = K - r0 < pl.chunk_rows ? K - r0 : pl.chunk_rows;
+                    tc::mbar_arrive_expect_tx(ring_full + s, uint32_t(rows) * V);
+                    bulk_copy(dyn + pl.off_ring + s * pl.chunk_bytes, c.codes + (sh * K + r0) * V, uint32_t(rows) * V,
+                              ring_full + s);
+                }
+            }
+            ok = __shfl_sync(0xffffffffu, int(ok), 0) != 0;
+        }
+        if (!ok && lane == 0) {  // a wait ran out: let the copies that were issued land before the block ends
+            for (int i = 0; i < pl.heads && i < it; ++i)
+                tc::mbar_drain(head_full + i, uint32_t((it - 1 - i) / pl.heads) & 1u);
+            for (uint32_t i = 0; i < uint32_t(pl.ring) && i < nch; ++i)
+                tc::mbar_drain(ring_full + i, ((nch - 1 - i) / pl.ring) & 1u);
+        }
+        return;
+    }
+    // ---- readers
+    float* kt = reinterpret_cast<float*>(dyn + pl.off_kt);    // [W][K] k_j e^{D_j}
+    float* dec = reinterpret_cast<float*>(dyn + pl.off_dec);  // [K] e^G
+    float* wq = reinterpret_cast<float*>(dyn + pl.off_wq);    // [groups][K] q e^G scale
+    float* ps = reinterpret_cast<float*>(dyn + pl.off_p);     // [64] scores
+    float* red = reinterpret_cast<float*>(dyn + pl.off_red);  // [slices][V]
+    const int unit = tid / pl.lanes, ugrp = unit % NG, slice = unit / NG;
+    const int ucol = ugrp * kG + (tid % pl.lanes) * 16;
+    const bool reads = slice < pl.slices;
+    int it = 0;
+    uint32_t nch = 0;
+    bool ok = true;
+    // a wait that ran out leaves `ok` false: the thread then writes nothing, but keeps step with the block's barriers
+    for (int64_t item = blockIdx.x; item < items; item += gridDim.x, ++it) {
+        const int hs = it % pl.heads;
+        ok = ok && tc::mbar_wait(head_full + hs, uint32_t(it / pl.heads) & 1u, err, &abort_flag);
+        HeadInfo hi{0, 0, 0};
+        if (ok) hi = info[hs];
+        const char* st = dyn + hs * pl.head_bytes;
+        const T* qb = reinterpret_cast<const T*>(st);
+        const T* kb = reinterpret_cast<const T*>(st + pl.off_k);
+        const T* vb = reinterpret_cast<const T*>(st + pl.off_v);
+        const float* gb = reinterpret_cast<const float*>(st + pl.off_g);
+        const T* kw = reinterpret_cast<const T*>(st + pl.off_kw);
+        const float* gw = reinterpret_cast<const float*>(st + pl.off_gw);
+        const T* vw = reinterpret_cast<const T*>(st + pl.off_vw);
+        const float* sc = reinterpret_cast<const float*>(st + pl.off_sc);
+        const int n = hi.n, used = n + 1;
+        if (hi.live) {
+            T* pk = static_cast<T*>(c.k) + (hi.sh * c.W + n) * K;
+            T* pv = static_cast<T*>(c.v) + (hi.sh * c.W + n) * V;
+            float* pg = c.la + (hi.sh * c.W + n) * K;
+            for (int r = tid; r < K; r += kStreamThreads) {
+                const float la = !gate_rows ? gate_log_alpha(ga, item, 0, r, 1, K)
+                                 : ga.kind == kGatePreact ? logsigmoid_f(gb[r]) * ga.inv_tau : gb[r];
+                kt[n * K + r] = ldf(kb + r);
+                pk[r] = kb[r];
+                pg[r] = la;
+                float D = la;
+#pragma unroll 4
+                for (int j = n - 1; j >= 0; --j) {
+                    kt[j * K + r] = ldf(kw + j * K + r) * tc::exp2_ftz(D * tc::kLog2e);
+                    D += gw[j * K + r];
+                }
+                const float d = tc::exp2_ftz(D * tc::kLog2e), qd = ldf(qb + r) * d;
+                dec[r] = d;
+                for (int g = 0; g < NG; ++g) wq[g * K + r] = qd * sc[r * NG + g];
+            }
+            for (int x = tid; x < V; x += kStreamThreads) pv[x] = vb[x];
+        }
+        tc::named_sync(1, kStreamThreads);
+        if (hi.live) {
+            for (int j = warp; j < used; j += kStreamWarps) {
+                float s = 0.f;
+                for (int r = lane; r < K; r += 32) s = fmaf(ldf(qb + r), kt[j * K + r], s);
+#pragma unroll
+                for (int d = 16; d > 0; d >>= 1) s += __shfl_xor_sync(0xffffffffu, s, d);
+                if (lane == 0) ps[j] = s;
+            }
+            float2 acc[8];
+#pragma unroll
+            for (int e = 0; e < 8; ++e) acc[e] = make_float2(0.f, 0.f);
+            for (int ch = 0; ch < chunks; ++ch, ++nch) {
+                const uint32_t s = nch % pl.ring;
+                ok = ok && tc::mbar_wait(ring_full + s, (nch / pl.ring) & 1u, err, &abort_flag);
+                const int r0 = ch * pl.chunk_rows, rows = K - r0 < pl.chunk_rows ? K - r0 : pl.chunk_rows;
+                const char* src = dyn + pl.off_ring + s * pl.chunk_bytes + ucol;
+                const float* w = wq + ugrp * K + r0;
+                if (reads && ok) {
+#pragma unroll 2
+                    for (int r = slice; r < rows; r += pl.slices) {
+                        const uint4 x = *reinterpret_cast<const uint4*>(src + r * V);
+                        const float2 w2 = make_float2(w[r], w[r]);
+                        float2 y[8];
+                        decode4<INT8>(x.x, y);
+                        decode4<INT8>(x.y, y + 2);
+                        decode4<INT8>(x.z, y + 4);
+                        decode4<INT8>(x.w, y + 6);
+#pragma unroll
+                        for (int e = 0; e < 8; ++e) acc[e] = fma2(w2, y[e], acc[e]);
+                    }
+                }
+                __syncwarp();
+                if (lane == 0) tc::mbar_arrive(ring_empty + s);
+            }
+            if (reads) {
+                float4* d = reinterpret_cast<float4*>(red + slice * V + ucol);
+#pragma unroll
+                for (int e = 0; e < 4; ++e) d[e] = make_float4(acc[2 * e].x, acc[2 * e].y, acc[2 * e + 1].x, acc[2 * e + 1].y);
+            }
+        }
+        tc::named_sync(1, kStreamThreads);
+        if (ok) {
+            for (int x = tid; x < V; x += kStreamThreads) {
+                float s = 0.f;
+                if (hi.live) {
+#pragma unroll 8
+                    for (int i = 0; i < pl.slices; ++i) s += red[i * V + x];
+                    for (int j = 0; j < n; ++j) s = fmaf(ps[j], ldf(vw + j * V + x), s);
+                    s = fmaf(ps[n], ldf(vb + x), s);
+                }
+                stf(o + item * V + x, s);
+            }
+        }
+        if (ok && hi.live && used == c.W) {
+            // the window is full: round the state back (its codes are in L2 by now)
+            uint8_t* codes = c.codes + hi.sh * K * V;
+            float* scale = c.scale + hi.sh * K * NG;
+            for (int u = warp; u < K / kBatch * NG; u += kStreamWarps) {
+                const int grp = u % NG, r = u / NG * kBatch;
+                const Cols<true> cols(grp, V);
+                uint32_t z[kBatch];
+                float2 y[kBatch][2];
+#pragma unroll
+                for (int i = 0; i < kBatch; ++i) z[i] = cols.codes(codes + int64_t(r + i) * V);
+#pragma unroll
+                for (int i = 0; i < kBatch; ++i) {
+                    decode4<INT8>(z[i], y[i]);
+                    const float f = sc[(r + i) * NG + grp], d = dec[r + i];
+#pragma unroll
+                    for (int e = 0; e < 2; ++e)
+                        y[i][e] = mul2(make_float2(d, d), mul2(make_float2(f, f), y[i][e]));
+                }
+                for (int j = 0; j < used; ++j) {
+                    const T* vr = (j < n ? vw + j * V : vb) + cols.col[0];
+                    float2 vv[2] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f)};
+                    if (cols.on[0]) {
+                        if constexpr (sizeof(T) == 2) {
+                            const uint2 t = *reinterpret_cast<const uint2*>(vr);
+                            vv[0] = __bfloat1622float2(*reinterpret_cast<const __nv_bfloat162*>(&t.x));
+                            vv[1] = __bfloat1622float2(*reinterpret_cast<const __nv_bfloat162*>(&t.y));
+                        } else {
+                            const float4 t = *reinterpret_cast<const float4*>(vr);
+                            vv[0] = make_float2(t.x, t.y);
+                            vv[1] = make_float2(t.z, t.w);
+                        }
+                    }
+                    const float4 ka = *reinterpret_cast<const float4*>(kt + j * K + r);
+                    const float4 kc = *reinterpret_cast<const float4*>(kt + j * K + r + 4);
+                    const float kk[kBatch] = {ka.x, ka.y, ka.z, ka.w, kc.x, kc.y, kc.z, kc.w};
+#pragma unroll
+                    for (int i = 0; i < kBatch; ++i) {
+                        const float2 k2 = make_float2(kk[i], kk[i]);
+                        y[i][0] = fma2(k2, vv[0], y[i][0]);
+                        y[i][1] = fma2(k2, vv[1], y[i][1]);
+                    }
+                }
+#pragma unroll
+                for (int i = 0; i < kBatch; ++i) {
+                    const float t[4] = {y[i][0].x, y[i][0].y, y[i][1].x, y[i][1].y};
+                    const float ns = scale_of<INT8>(warp_amax(t));
+                    cols.put_codes(codes + int64_t(r + i) * V, encode4<INT8>(t, ns));
+                    if (lane == 0) scale[int64_t(r + i) * NG + grp] = ns;
+                }
+            }
+        }
+        tc::named_sync(1, kStreamThreads);  // the next head overwrites kt and dec
+        if (lane == 0) tc::mbar_arrive(head_empty + hs);
+    }
+}
+
 Pool pool_of(const CacheProblem& p) {
     return Pool{static_cast<uint8_t*>(p.c.codes), p.c.scale, p.c.k, p.c.v, p.c.log_a, p.c.slots, p.c.window,
                 p.H, int(p.K), int(p.V), int(cdiv(p.V, kG))};
@@ -479,6 +760,67 @@ gla_status step_typed(const CacheProblem& p, const void* q, const void* k, const
     return GLA_OK;
 }
 
+// Shared memory and tiling of the streamed step, or heads = 0 where it does not apply: bulk copies want every stretch
+// (a token's k, v and log a, a window, a row of scales) to be a multiple of 16 bytes, groups want whole rows of lanes,
+// and a window must fit beside a ring of at least three chunks. Other shapes take k_cache_step.
+StreamPlan stream_plan(const CacheProblem& p) {
+    StreamPlan pl{};
+    const int K = int(p.K), V = int(p.V), W = p.c.window, e = p.bf16 ? 2 : 4;
+    if (K % 8 != 0 || K > 4096 || !(V % kG == 0 ? V <= 2048 : V < kG && V % 16 == 0)) return pl;
+    const int NG = int(cdiv(V, kG));
+    pl.lanes = V < kG ? V / 16 : kG / 16;
+    pl.slices = kStreamThreads / pl.lanes / NG;
+    int at = 0;
+    const auto take = [&](int bytes) {
+        const int here = at;
+        at += round_up(bytes, 128);
+        return here;
+    };
+    take(K * e);
+    pl.off_k = take(K * e);
+    pl.off_v = take(V * e);
+    pl.off_g = take(K * 4);
+    pl.off_kw = take((W - 1) * K * e);
+    pl.off_gw = take((W - 1) * K * 4);
+    pl.off_vw = take((W - 1) * V * e);
+    pl.off_sc = take(K * NG * 4);
+    pl.head_bytes = at;
+    const int pass = pl.slices * V;
+    pl.chunk_rows = (pass >= 16384 ? 1 : 16384 / pass) * pl.slices;
+    pl.chunk_bytes = round_up(pl.chunk_rows * V, 128);
+    for (int heads = 2; heads >= 1; --heads) {
+        at = heads * pl.head_bytes;
+        pl.off_kt = take(W * K * 4);
+        pl.off_dec = take(K * 4);
+        pl.off_wq = take(K * NG * 4);
+        pl.off_p = take(64 * 4);
+        pl.off_red = take(pl.slices * V * 4);
+        pl.off_ring = at;
+        const int64_t room = int64_t(kStreamSmem) - 1024 - at;
+        const int64_t ring = room > 0 ? room / pl.chunk_bytes : 0;
+        if (ring >= 3) {
+            pl.heads = heads;
+            pl.ring = int(ring < kMaxRing ? ring : kMaxRing);
+            pl.smem = size_t(at) + size_t(pl.ring) * pl.chunk_bytes;
+            return pl;
+        }
+    }
+    return pl;
+}
+
+template <typename T, bool INT8>
+gla_status stream_typed(const CacheProblem& p, const StreamPlan& pl, const void* q, const void* k, const void* v,
+                        const float* la, const int32_t* slots, const int32_t* lengths, void* o, cudaStream_t s) {
+    const Pool c = pool_of(p);
+    const GateArgs ga{la, p.gate, p.inv_tau, p.H};
+    if (!allow_smem(k_cache_stream<T, INT8>, pl.smem)) return GLA_ERR_CUDA;
+    const int64_t items = p.B * p.H;
+    GLA_LAUNCH("cache_step", (k_cache_stream<T, INT8>), unsigned(items < 148 ? items : 148), kStreamThreads + 32, pl.smem,
+               s, c, pl, items, static_cast<const T*>(q), static_cast<const T*>(k), static_cast<const T*>(v), ga, slots,
+               lengths, static_cast<T*>(o), device_error_word());
+    return GLA_OK;
+}
+
 // Four adjacent columns a lane where every row's fours are aligned (a width that is a multiple of 4).
 #define GLA_CACHE_DISPATCH(fn, T, ...)                                                                 \
     (p.c.format == GLA_CACHE_INT8 ? (p.V % 4 == 0 ? fn<T true, true>(__VA_ARGS__) : fn<T true, false>(__VA_ARGS__)) \
@@ -504,6 +846,15 @@ gla_status cache_load(const CacheProblem& p, const int32_t* slots, const int32_t
 
 gla_status cache_step(const CacheProblem& p, const void* q, const void* k, const void* v, const float* la,
                       const int32_t* slots, const int32_t* lengths, void* o, cudaStream_t s) {
+    const StreamPlan pl = stream_plan(p);
+    if (pl.heads > 0) {
+        const bool i8 = p.c.format == GLA_CACHE_INT8;
+        if (p.bf16)
+            return i8 ? stream_typed<__nv_bfloat16, true>(p, pl, q, k, v, la, slots, lengths, o, s)
+                      : stream_typed<__nv_bfloat16, false>(p, pl, q, k, v, la, slots, lengths, o, s);
+        return i8 ? stream_typed<float, true>(p, pl, q, k, v, la, slots, lengths, o, s)
+                  : stream_typed<float, false>(p, pl, q, k, v, la, slots, lengths, o, s);
+    }
     return p.bf16 ? GLA_CACHE_DISPATCH(step_typed, __nv_bfloat16 GLA_COMMA, p, q, k, v, la, slots, lengths, o, s)
                   : GLA_CACHE_DISPATCH(step_typed, float GLA_COMMA, p, q, k, v, la, slots, lengths, o, s);
 }

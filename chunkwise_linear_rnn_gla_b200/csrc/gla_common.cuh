@@ -21,6 +21,25 @@ __device__ __forceinline__ void stf<float>(float* p, float x) { *p = x; }
 template <>
 __device__ __forceinline__ void stf<__nv_bfloat16>(__nv_bfloat16* p, float x) { *p = __float2bfloat16_rn(x); }
 
+// Packed fp32 (sm_100): both halves for one issue slot.
+__device__ __forceinline__ uint64_t f32x2_bits(float2 x) { return *reinterpret_cast<uint64_t*>(&x); }
+__device__ __forceinline__ float2 f32x2_of(uint64_t x) { return *reinterpret_cast<float2*>(&x); }
+__device__ __forceinline__ float2 fma2(float2 a, float2 b, float2 c) {
+    uint64_t d;
+    asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(d) : "l"(f32x2_bits(a)), "l"(f32x2_bits(b)), "l"(f32x2_bits(c)));
+    return f32x2_of(d);
+}
+__device__ __forceinline__ float2 mul2(float2 a, float2 b) {
+    uint64_t d;
+    asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(d) : "l"(f32x2_bits(a)), "l"(f32x2_bits(b)));
+    return f32x2_of(d);
+}
+__device__ __forceinline__ float2 add2(float2 a, float2 b) {
+    uint64_t d;
+    asm("add.rn.f32x2 %0, %1, %2;" : "=l"(d) : "l"(f32x2_bits(a)), "l"(f32x2_bits(b)));
+    return f32x2_of(d);
+}
+
 __host__ __device__ constexpr int64_t cdiv(int64_t a, int64_t b) { return (a + b - 1) / b; }
 
 // Floor applied to every log alpha before it enters a per-chunk cumsum. A zero gate is given as a

@@ -55,26 +55,12 @@ template <>
 struct VecOf<2> {
     using type = float2;
 };
-__device__ __forceinline__ uint64_t bits(float2 x) { return *reinterpret_cast<uint64_t*>(&x); }
-__device__ __forceinline__ float2 pair(uint64_t x) { return *reinterpret_cast<float2*>(&x); }
 __device__ __forceinline__ float vfma(float a, float b, float c) { return fmaf(a, b, c); }
-__device__ __forceinline__ float2 vfma(float2 a, float2 b, float2 c) {
-    uint64_t d;
-    asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(d) : "l"(bits(a)), "l"(bits(b)), "l"(bits(c)));
-    return pair(d);
-}
+__device__ __forceinline__ float2 vfma(float2 a, float2 b, float2 c) { return fma2(a, b, c); }
 __device__ __forceinline__ float vmul(float a, float b) { return a * b; }
-__device__ __forceinline__ float2 vmul(float2 a, float2 b) {
-    uint64_t d;
-    asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(d) : "l"(bits(a)), "l"(bits(b)));
-    return pair(d);
-}
+__device__ __forceinline__ float2 vmul(float2 a, float2 b) { return mul2(a, b); }
 __device__ __forceinline__ float vadd(float a, float b) { return a + b; }
-__device__ __forceinline__ float2 vadd(float2 a, float2 b) {
-    uint64_t d;
-    asm("add.rn.f32x2 %0, %1, %2;" : "=l"(d) : "l"(bits(a)), "l"(bits(b)));
-    return pair(d);
-}
+__device__ __forceinline__ float2 vadd(float2 a, float2 b) { return add2(a, b); }
 template <typename V>
 __device__ __forceinline__ V vset(float x) {
     if constexpr (sizeof(V) == 8) return make_float2(x, x);
