@@ -73,20 +73,21 @@ __device__ __forceinline__ float scale_of(uint32_t amax_bits) {
     return m < kTiny ? 0.f : __fmul_rn(m, INT8 ? float(1.0 / 127) : float(1.0 / 448));
 }
 
+// Four values to codes: round(y inv), ties to even. |y inv| stays below the largest code plus half a step, so nothing
+// has to be clamped; the codes of a group held as zero or as NaN are 0 (inv = 0 gives 0, or NaN which is replaced).
 template <bool INT8>
-__device__ __forceinline__ uint32_t encode4(const float* y, float scale) {
-    // the codes of a group held as zero or as NaN are 0
-    const float inv = scale > 0.f ? __frcp_rn(scale) : 0.f;
-    uint32_t r = 0;
-    if (!(scale > 0.f)) return r;
-#pragma unroll
-    for (int e = 0; e < 4; ++e) {
-        const float t = __fmul_rn(y[e], inv);
-        const uint32_t b = INT8 ? uint32_t(int(fminf(fmaxf(rintf(t), -127.f), 127.f))) & 0xffu
-                                : uint32_t(__nv_cvt_float_to_fp8(t, __NV_SATFINITE, __NV_E4M3));
-        r |= b << (8 * e);
+__device__ __forceinline__ uint32_t encode4(const float* y, float inv) {
+    if (!(inv > 0.f)) return 0u;
+    const float t0 = __fmul_rn(y[0], inv), t1 = __fmul_rn(y[1], inv), t2 = __fmul_rn(y[2], inv), t3 = __fmul_rn(y[3], inv);
+    if constexpr (INT8) {
+        const uint32_t lo = __byte_perm(uint32_t(__float2int_rn(t0)), uint32_t(__float2int_rn(t1)), 0x0040);
+        const uint32_t hi = __byte_perm(uint32_t(__float2int_rn(t2)), uint32_t(__float2int_rn(t3)), 0x0040);
+        return __byte_perm(lo, hi, 0x5410);
+    } else {
+        const uint32_t lo = __nv_cvt_float2_to_fp8x2(make_float2(t0, t1), __NV_SATFINITE, __NV_E4M3);
+        const uint32_t hi = __nv_cvt_float2_to_fp8x2(make_float2(t2, t3), __NV_SATFINITE, __NV_E4M3);
+        return lo | hi << 16;
     }
-    return r;
 }
 
 // ---- a lane's four columns ------------------------------------------------------------------
@@ -138,7 +139,19 @@ struct Cols {
                 if (on[e]) row[col[e]] = y[e];
         }
     }
-    // place of the lane's e-th column in a [128] shared-memory row
+    // the lane's columns of a [128] shared-memory row
+    __device__ __forceinline__ void pairs(const float* row, float2* t) const {
+        const int lane = threadIdx.x & 31;
+        if constexpr (VEC) {
+            const float4 x = *reinterpret_cast<const float4*>(row + 4 * lane);
+            t[0] = make_float2(x.x, x.y);
+            t[1] = make_float2(x.z, x.w);
+        } else {
+            t[0] = make_float2(row[lane], row[lane + 32]);
+            t[1] = make_float2(row[lane + 64], row[lane + 96]);
+        }
+    }
+    // place of the lane's e-th column in such a row
     __device__ __forceinline__ int at(int e) const {
         const int lane = threadIdx.x & 31;
         return VEC ? 4 * lane + e : lane + 32 * e;
@@ -152,12 +165,28 @@ __device__ __forceinline__ bool named_before(const int32_t* slots, int64_t b, in
     return __syncthreads_or(dup) != 0;
 }
 
-// largest magnitude of the warp's columns, as bits
-__device__ __forceinline__ uint32_t warp_amax(const float* y) {
-    uint32_t m = 0;
+// Round `rows` <= 8 rows of a group (four columns a lane) into their codes and scales. Lane i works out row i's scale
+// and reciprocal for the whole warp.
+template <bool INT8, bool VEC>
+__device__ __forceinline__ void put_rows(const Cols<VEC>& cols, const float (*y)[4], int rows, uint8_t* codes, int64_t V,
+                                         float* scale, int64_t NG) {
+    const int lane = threadIdx.x & 31;
+    uint32_t mine = 0;
 #pragma unroll
-    for (int e = 0; e < 4; ++e) m = max(m, __float_as_uint(y[e]) & 0x7fffffffu);
-    return __reduce_max_sync(0xffffffffu, m);
+    for (int i = 0; i < kBatch; ++i) {
+        uint32_t m = 0;
+#pragma unroll
+        for (int e = 0; e < 4; ++e) m = max(m, __float_as_uint(y[i][e]) & 0x7fffffffu);
+        m = __reduce_max_sync(0xffffffffu, m);
+        if (lane == i) mine = m;
+    }
+    const float sc = scale_of<INT8>(mine), inv = sc > 0.f ? __frcp_rn(sc) : 0.f;
+#pragma unroll
+    for (int i = 0; i < kBatch; ++i) {
+        const float r = __shfl_sync(0xffffffffu, inv, i);
+        if (i < rows) cols.put_codes(codes + i * V, encode4<INT8>(y[i], r));
+    }
+    if (lane < rows) scale[lane * NG] = sc;
 }
 
 // ---- store ----------------------------------------------------------------------------------
@@ -171,8 +200,7 @@ __global__ void __launch_bounds__(kThreads) k_cache_store(Pool c, int parts, con
     const int r0 = part * kWarps * kBatch + int(threadIdx.x >> 5) * kBatch;
     float y[kBatch][4];
 #pragma unroll
-    for (int i = 0; i < kBatch; ++i)
-        if (r0 + i < c.K) cols.load(S + (bh * c.K + r0 + i) * c.V, y[i]);
+    for (int i = 0; i < kBatch; ++i) cols.load(S + (bh * c.K + (r0 + i < c.K ? r0 + i : c.K - 1)) * c.V, y[i]);
     const int32_t slot = slots[b];
     if (slot < 0) return;
     if (slot >= c.slots || named_before(slots, b, slot)) {
@@ -180,13 +208,9 @@ __global__ void __launch_bounds__(kThreads) k_cache_store(Pool c, int parts, con
         return;
     }
     const int64_t sh = slot * c.H + head;
-#pragma unroll
-    for (int i = 0; i < kBatch; ++i) {
-        if (r0 + i >= c.K) break;
-        const float sc = scale_of<INT8>(warp_amax(y[i]));
-        cols.put_codes(c.codes + (sh * c.K + r0 + i) * c.V, encode4<INT8>(y[i], sc));
-        if ((threadIdx.x & 31) == 0) c.scale[(sh * c.K + r0 + i) * c.NG + grp] = sc;
-    }
+    const int rows = c.K - r0 < kBatch ? c.K - r0 : kBatch;
+    if (rows <= 0) return;
+    put_rows<INT8, VEC>(cols, y, rows, c.codes + (sh * c.K + r0) * c.V, c.V, c.scale + (sh * c.K + r0) * c.NG + grp, c.NG);
 }
 
 // ---- the window -----------------------------------------------------------------------------
@@ -239,29 +263,33 @@ __device__ __forceinline__ void window_values(const Pool& c, int64_t sh, int64_t
     }
 }
 
-// Rows r .. r+7 (of those in kt) of the state: code x scale x decay + the window's outer products.
-template <bool INT8, bool VEC>
-__device__ __forceinline__ void form_rows(const Cols<VEC>& cols, const uint32_t* codes, const float* scale,
-                                          const float* decay, const float* kt, int ld, const float* vs, int used,
-                                          float (*y)[4]) {
+// Eight rows of the state: code x scale x decay + the window's outer products. value(j) gives the lane's four columns of
+// token j's v, kt + j ld its eight keys.
+template <bool INT8, typename F>
+__device__ __forceinline__ void form_rows(const uint32_t* codes, const float* scale, const float* decay, const float* kt,
+                                          int ld, int used, F value, float (*out)[4]) {
+    float2 y[kBatch][2];
 #pragma unroll
     for (int i = 0; i < kBatch; ++i) {
         decode4<INT8>(codes[i], y[i]);
-        const float f = decay[i];
-#pragma unroll
-        for (int e = 0; e < 4; ++e) y[i][e] = f * (scale[i] * y[i][e]);
+        const float2 f = make_float2(decay[i], decay[i]), g = make_float2(scale[i], scale[i]);
+        y[i][0] = mul2(f, mul2(g, y[i][0]));
+        y[i][1] = mul2(f, mul2(g, y[i][1]));
     }
     for (int j = 0; j < used; ++j) {
-        float v[4];
-#pragma unroll
-        for (int e = 0; e < 4; ++e) v[e] = vs[j * kG + cols.at(e)];
+        float2 v[2];
+        value(j, v);
         const float4 ka = *reinterpret_cast<const float4*>(kt + j * ld), kb = *reinterpret_cast<const float4*>(kt + j * ld + 4);
         const float k[kBatch] = {ka.x, ka.y, ka.z, ka.w, kb.x, kb.y, kb.z, kb.w};
 #pragma unroll
-        for (int i = 0; i < kBatch; ++i)
-#pragma unroll
-            for (int e = 0; e < 4; ++e) y[i][e] = fmaf(k[i], v[e], y[i][e]);
+        for (int i = 0; i < kBatch; ++i) {
+            const float2 k2 = make_float2(k[i], k[i]);
+            y[i][0] = fma2(k2, v[0], y[i][0]);
+            y[i][1] = fma2(k2, v[1], y[i][1]);
+        }
     }
+#pragma unroll
+    for (int i = 0; i < kBatch; ++i) out[i][0] = y[i][0].x, out[i][1] = y[i][0].y, out[i][2] = y[i][1].x, out[i][3] = y[i][1].y;
 }
 
 // ---- load -----------------------------------------------------------------------------------
@@ -302,7 +330,7 @@ __global__ void __launch_bounds__(kThreads) k_cache_load(Pool c, int parts, cons
         window_keys<T, false>(c, sh, bh, n, first, last, ROWS, nullptr, GateArgs{}, false, kt, decay);
         window_values<T, false>(c, sh, bh, n, grp, nullptr, vs);
         __syncthreads();
-        form_rows<INT8, VEC>(cols, x, sc, decay + w0, kt + w0, ROWS, vs, n, y);
+        form_rows<INT8>(x, sc, decay + w0, kt + w0, ROWS, n, [&](int j, float2* t) { cols.pairs(vs + j * kG, t); }, y);
     } else {
 #pragma unroll
         for (int i = 0; i < kBatch; ++i)
@@ -319,12 +347,12 @@ __global__ void __launch_bounds__(kThreads) k_cache_load(Pool c, int parts, cons
 __host__ __device__ constexpr int round_up(int x, int m) { return (x + m - 1) / m * m; }
 
 template <typename T, bool INT8, bool VEC>
-__global__ void __launch_bounds__(kThreads, 3) k_cache_step(Pool c, const T* __restrict__ q, const T* __restrict__ k,
+__global__ void __launch_bounds__(kThreads, 4) k_cache_step(Pool c, const T* __restrict__ q, const T* __restrict__ k,
                                                             const T* __restrict__ v, GateArgs ga,
                                                             const int32_t* __restrict__ slots,
                                                             const int32_t* __restrict__ lengths, T* __restrict__ o,
                                                             int* err) {
-    constexpr int PASS = 4;  // batches a warp has in flight: 256 rows a block
+    constexpr int PASS = 2;  // batches a warp has in flight: 128 rows a block
     extern __shared__ __align__(16) float sm[];
     const int64_t bh = blockIdx.x / c.NG, b = bh / c.H, head = bh % c.H;
     const int grp = int(blockIdx.x % c.NG), tid = int(threadIdx.x), lane = tid & 31, warp = tid >> 5;
@@ -377,7 +405,7 @@ __global__ void __launch_bounds__(kThreads, 3) k_cache_step(Pool c, const T* __r
         for (int d = 16; d > 0; d >>= 1) s += __shfl_xor_sync(0xffffffffu, s, d);
         if (lane == 0) p[j] = s;
     }
-    float acc[4] = {0.f, 0.f, 0.f, 0.f};
+    float2 acc[2] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f)};
     for (int r0 = 0; r0 < c.K; r0 += PASS * kWarps * kBatch) {
         if (r0) fetch(r0);
 #pragma unroll
@@ -388,16 +416,19 @@ __global__ void __launch_bounds__(kThreads, 3) k_cache_step(Pool c, const T* __r
                 const float w[kBatch] = {wa.x, wa.y, wa.z, wa.w, wb.x, wb.y, wb.z, wb.w};
 #pragma unroll
                 for (int i = 0; i < kBatch; ++i) {
-                    float y[4];
+                    float2 y[2];
                     decode4<INT8>(x[u][i], y);
-#pragma unroll
-                    for (int e = 0; e < 4; ++e) acc[e] = fmaf(w[i], y[e], acc[e]);
+                    const float2 w2 = make_float2(w[i], w[i]);
+                    acc[0] = fma2(w2, y[0], acc[0]);
+                    acc[1] = fma2(w2, y[1], acc[1]);
                 }
             }
         }
     }
-#pragma unroll
-    for (int e = 0; e < 4; ++e) red[warp * kG + cols.at(e)] = acc[e];
+    red[warp * kG + cols.at(0)] = acc[0].x;
+    red[warp * kG + cols.at(1)] = acc[0].y;
+    red[warp * kG + cols.at(2)] = acc[1].x;
+    red[warp * kG + cols.at(3)] = acc[1].y;
     __syncthreads();
     if (tid < kG && grp * kG + tid < c.V) {
         float s = 0.f;
@@ -417,27 +448,28 @@ __global__ void __launch_bounds__(kThreads, 3) k_cache_step(Pool c, const T* __r
             z[i] = cols.codes(codes + int64_t(ri) * c.V);
             sc[i] = scale[int64_t(ri) * c.NG];
         }
-        form_rows<INT8, VEC>(cols, z, sc, decay + r, kt + r, ld, vs, used, y);
-#pragma unroll
-        for (int i = 0; i < kBatch; ++i) {
-            if (r + i >= c.K) break;
-            const float ns = scale_of<INT8>(warp_amax(y[i]));
-            cols.put_codes(c.codes + (sh * c.K + r + i) * c.V, encode4<INT8>(y[i], ns));
-            if (lane == 0) scale[int64_t(r + i) * c.NG] = ns;
-        }
+        form_rows<INT8>(z, sc, decay + r, kt + r, ld, used, [&](int j, float2* t) { cols.pairs(vs + j * kG, t); }, y);
+        put_rows<INT8, VEC>(cols, y, c.K - r < kBatch ? c.K - r : kBatch, c.codes + (sh * c.K + r) * c.V, c.V,
+                            scale + int64_t(r) * c.NG, c.NG);
     }
 }
 
 // ---- step, streamed ---------------------------------------------------------------------------
-// For the shapes that bulk copies can move (stream_plan below). One persistent block per SM takes whole heads in turn. A
-// producer warp keeps copies in flight without a pause, across heads: a head's codes are one contiguous stretch,
+// For the shapes that bulk copies can move (stream_plan below). One persistent block per SM takes its share of the heads.
+// A producer warp keeps copies in flight without a pause, across heads: a head's codes are one contiguous stretch,
 // fetched in chunks of about 16 KB through a ring, and the token, the window and the scales of the next head travel
-// while this one is computed. 16 warps read the chunks (16 codes a lane), so memory never waits for the window's
-// exponentials or the reductions. The kernel above spends most of a block's time on that chain of latencies: 101 us
-// against 35 us here for 1024 heads of 256 x 512 (134 MB of codes: 20.5 us at the measured copy bandwidth).
+// while this one is computed. 16 warps read the chunks (16 codes a lane), so memory does not wait for the window's
+// exponentials or the reductions.
+//
+// A head whose window is full costs several times the others (every entry takes `window` multiply-adds and is rounded),
+// so it is split into its groups of 128 columns, which share nothing but the window: each is an item of its own that
+// forms its columns of S_t, reads o from them and rounds them back. The blocks' shares are cut by cost, from the lengths
+// that every block reads.
 constexpr int kStreamThreads = 512;           // readers
 constexpr int kStreamWarps = kStreamThreads / 32;
 constexpr int kMaxRing = 8;
+constexpr int kMaxRows = 1024;                // rows of a call in one launch
+constexpr int kFoldCost = 6;                  // of a folding group, where an ordinary head costs its number of groups
 constexpr size_t kStreamSmem = 227 * 1024;
 
 struct StreamPlan {
@@ -451,9 +483,10 @@ struct StreamPlan {
     size_t smem;
 };
 
-struct HeadInfo {
-    int64_t sh;  // slot * H + head
-    int n;       // tokens in the window
+struct Item {
+    int64_t bh, sh;  // row of the call x head; slot x head
+    int n;           // tokens in the window
+    int grp;         // >= 0: this group alone, and round it back; -1: the whole head
     int live;
 };
 
@@ -464,18 +497,52 @@ __device__ __forceinline__ void bulk_copy(void* dst, const void* src, uint32_t b
                  : "memory");
 }
 
+// A wait of a whole warp, which then agrees on its outcome.
+__device__ __forceinline__ bool warp_wait(uint64_t* bar, uint32_t parity, int* err, int* abort) {
+    const bool ok = tc::mbar_wait(bar, parity, err, abort);
+    return __all_sync(0xffffffffu, ok) != 0;
+}
+
+// A ring position: stage and the parity of its turn.
+struct Turn {
+    int s = 0;
+    uint32_t par = 0;
+    __device__ __forceinline__ void next(int stages) {
+        if (++s == stages) s = 0, par ^= 1u;
+    }
+};
+
+// This block's items: of the folding groups (all of them first, then the other heads, in the order of `rows`) those
+// whose cost begins in the block's share.
+struct Share {
+    int64_t f0, f1, h0, h1;
+    __device__ __forceinline__ Share(int folds, int B, int64_t H, int NG) {
+        const int64_t fg = folds * H * NG, hd = (B - folds) * H, total = fg * kFoldCost + hd * NG;
+        const int64_t lo = total * blockIdx.x / gridDim.x, hi = total * (blockIdx.x + 1) / gridDim.x;
+        const auto first = [](int64_t from, int64_t cost, int64_t most) {
+            const int64_t i = from <= 0 ? 0 : (from + cost - 1) / cost;
+            return i < most ? i : most;
+        };
+        f0 = first(lo, kFoldCost, fg);
+        f1 = first(hi, kFoldCost, fg);
+        h0 = first(lo - fg * kFoldCost, NG, hd);
+        h1 = first(hi - fg * kFoldCost, NG, hd);
+    }
+    __device__ __forceinline__ int64_t count() const { return (f1 - f0) + (h1 - h0); }
+};
+
 template <typename T, bool INT8>
 __global__ void __launch_bounds__(kStreamThreads + 32, 1)
-    k_cache_stream(Pool c, StreamPlan pl, int64_t items, const T* __restrict__ q, const T* __restrict__ k,
+    k_cache_stream(Pool c, StreamPlan pl, int B, int64_t b0, const T* __restrict__ q, const T* __restrict__ k,
                    const T* __restrict__ v, GateArgs ga, const int32_t* __restrict__ slots,
                    const int32_t* __restrict__ lengths, T* __restrict__ o, int* err) {
     extern __shared__ __align__(128) char dyn[];
     __shared__ uint64_t head_full[2], head_empty[2], ring_full[kMaxRing], ring_empty[kMaxRing];
-    __shared__ HeadInfo info[2];
-    __shared__ int abort_flag;
+    __shared__ Item info[2];
+    __shared__ uint16_t rows[kMaxRows];  // the call's rows, those whose window is full first
+    __shared__ int warp_folds[kStreamWarps], abort_flag;
     const int tid = int(threadIdx.x), lane = tid & 31, warp = tid >> 5;
     const int K = c.K, V = c.V, NG = c.NG;
-    const int chunks = (K + pl.chunk_rows - 1) / pl.chunk_rows;
     const bool gate_rows = ga.kind == kGateChannel || ga.kind == kGatePreact;
     if (tid == 0) {
         abort_flag = 0;
@@ -483,66 +550,125 @@ __global__ void __launch_bounds__(kStreamThreads + 32, 1)
         for (int i = 0; i < kMaxRing; ++i) tc::mbar_init(ring_full + i, 1), tc::mbar_init(ring_empty + i, kStreamWarps);
         tc::fence_barrier_init();
     }
-    __syncthreads();
+    // rows that fold, from the front; the others, from the back
+    int folds = 0;
+    {
+        static_assert(kMaxRows == 2 * kStreamThreads, "two rows a thread");
+        int mine[2] = {0, 0}, before[2] = {0, 0};
+        if (warp < kStreamWarps) {
+            int count = 0;
+#pragma unroll
+            for (int u = 0; u < 2; ++u) {
+                const int b = 64 * warp + 32 * u + lane;
+                if (b < B) {
+                    const int32_t len = lengths[b0 + b];
+                    mine[u] = len >= 0 && slots[b0 + b] >= 0 && len % c.W == c.W - 1;
+                }
+                const uint32_t m = __ballot_sync(0xffffffffu, mine[u]);
+                before[u] = count + __popc(m & ((1u << lane) - 1));
+                count += __popc(m);
+            }
+            if (lane == 0) warp_folds[warp] = count;
+        }
+        __syncthreads();
+        int first = 0;
+        for (int w = 0; w < kStreamWarps; ++w) {
+            if (w < warp) first += warp_folds[w];
+            folds += warp_folds[w];
+        }
+        if (warp < kStreamWarps) {
+#pragma unroll
+            for (int u = 0; u < 2; ++u) {
+                const int b = 64 * warp + 32 * u + lane;
+                const int f = first + before[u];  // folding rows in front of b
+                if (b < B) rows[mine[u] ? f : folds + b - f] = uint16_t(b);
+            }
+        }
+        __syncthreads();
+    }
+    const Share share(folds, B, c.H, NG);
+    const int items = int(share.count());
+    const int chunks = (K + pl.chunk_rows - 1) / pl.chunk_rows;
     if (warp == kStreamWarps) {
         // ---- producer: all lanes walk the items (they share the search for a slot named before), lane 0 copies
+        Turn ht, rt;
         int it = 0;
-        uint32_t nch = 0;  // chunks issued
+        int64_t nch = 0;
         bool ok = true;
-        for (int64_t item = blockIdx.x; item < items && ok; item += gridDim.x, ++it) {
-            const int64_t b = item / c.H, head = item % c.H;
-            const int32_t slot = slots[b], len = lengths[b];
+        for (; it < items && ok; ++it) {
+            Item x;
+            int b;
+            int64_t head;
+            if (it < share.f1 - share.f0) {
+                const int64_t f = share.f0 + it;
+                x.grp = int(f % NG);
+                b = rows[f / NG / c.H];
+                head = f / NG % c.H;
+            } else {
+                const int64_t h = share.h0 + it - (share.f1 - share.f0);
+                x.grp = -1;
+                b = rows[folds + h / c.H];
+                head = h % c.H;
+            }
+            const int32_t slot = slots[b0 + b], len = lengths[b0 + b];
             bool live = slot >= 0;
             if (live) {
                 bool bad = slot >= c.slots || len < 0;
-                for (int64_t i = lane; i < b; i += 32) bad |= slots[i] == slot;
+                for (int64_t i = lane; i < b0 + b; i += 32) bad |= slots[i] == slot;
                 if (__any_sync(0xffffffffu, bad)) {
                     live = false;
                     if (lane == 0) atomicOr(err, kErrBadRow);
                 }
             }
             if (lane == 0) {
-                const int hs = it % pl.heads, turn = it / pl.heads;
-                if (turn > 0) ok = tc::mbar_wait(head_empty + hs, uint32_t(turn - 1) & 1u, err, &abort_flag);
-                const int n = live ? len % c.W : 0;
-                const int64_t sh = live ? slot * c.H + head : 0;
+                const int hs = ht.s;
+                if (it >= pl.heads) ok = tc::mbar_wait(head_empty + hs, ht.par ^ 1u, err, &abort_flag);
+                x.bh = (b0 + b) * c.H + head;
+                x.sh = live ? slot * c.H + head : 0;
+                x.n = live ? len % c.W : 0;
+                x.live = live;
                 if (ok) {
-                    info[hs] = HeadInfo{sh, n, live ? 1 : 0};
+                    info[hs] = x;
                     if (!live) tc::mbar_arrive(head_full + hs);
                     else {
                         char* st = dyn + hs * pl.head_bytes;
                         const uint32_t kb = uint32_t(K) * sizeof(T), vb = uint32_t(V) * sizeof(T), gb = uint32_t(K) * 4u;
                         const uint32_t sb = uint32_t(K) * NG * 4u;
-                        tc::mbar_arrive_expect_tx(head_full + hs, 2 * kb + vb + (gate_rows ? gb : 0u) + sb + n * (kb + gb + vb));
-                        bulk_copy(st, q + item * K, kb, head_full + hs);
-                        bulk_copy(st + pl.off_k, k + item * K, kb, head_full + hs);
-                        bulk_copy(st + pl.off_v, v + item * V, vb, head_full + hs);
-                        if (gate_rows) bulk_copy(st + pl.off_g, ga.g + item * K, gb, head_full + hs);
-                        bulk_copy(st + pl.off_sc, c.scale + sh * K * NG, sb, head_full + hs);
-                        if (n > 0) {
-                            bulk_copy(st + pl.off_kw, static_cast<T*>(c.k) + sh * c.W * K, n * kb, head_full + hs);
-                            bulk_copy(st + pl.off_gw, c.la + sh * c.W * K, n * gb, head_full + hs);
-                            bulk_copy(st + pl.off_vw, static_cast<T*>(c.v) + sh * c.W * V, n * vb, head_full + hs);
+                        tc::mbar_arrive_expect_tx(head_full + hs,
+                                                  2 * kb + vb + (gate_rows ? gb : 0u) + sb + x.n * (kb + gb + vb));
+                        if (x.n > 0) {
+                            bulk_copy(st + pl.off_gw, c.la + x.sh * c.W * K, x.n * gb, head_full + hs);
+                            bulk_copy(st + pl.off_kw, static_cast<T*>(c.k) + x.sh * c.W * K, x.n * kb, head_full + hs);
+                            bulk_copy(st + pl.off_vw, static_cast<T*>(c.v) + x.sh * c.W * V, x.n * vb, head_full + hs);
                         }
+                        bulk_copy(st, q + x.bh * K, kb, head_full + hs);
+                        bulk_copy(st + pl.off_k, k + x.bh * K, kb, head_full + hs);
+                        bulk_copy(st + pl.off_v, v + x.bh * V, vb, head_full + hs);
+                        if (gate_rows) bulk_copy(st + pl.off_g, ga.g + x.bh * K, gb, head_full + hs);
+                        bulk_copy(st + pl.off_sc, c.scale + x.sh * K * NG, sb, head_full + hs);
                     }
                 }
-                for (int ch = 0; ch < chunks && live && ok; ++ch, ++nch) {
-                    const uint32_t s = nch % pl.ring, t = nch / pl.ring;
-                    if (t > 0) ok = tc::mbar_wait(ring_empty + s, (t - 1) & 1u, err, &abort_flag);
+                for (int ch = 0; ch < chunks && live && x.grp < 0 && ok; ++ch) {
+                    if (nch >= pl.ring) ok = tc::mbar_wait(ring_empty + rt.s, rt.par ^ 1u, err, &abort_flag);
                     if (!ok) break;
-                    const int r0 = ch * pl.chunk_rows, rows = K - r0 < pl.chunk_rows ? K - r0 : pl.chunk_rows;
-                    tc::mbar_arrive_expect_tx(ring_full + s, uint32_t(rows) * V);
-                    bulk_copy(dyn + pl.off_ring + s * pl.chunk_bytes, c.codes + (sh * K + r0) * V, uint32_t(rows) * V,
-                              ring_full + s);
+                    const int r0 = ch * pl.chunk_rows, n = K - r0 < pl.chunk_rows ? K - r0 : pl.chunk_rows;
+                    tc::mbar_arrive_expect_tx(ring_full + rt.s, uint32_t(n) * V);
+                    bulk_copy(dyn + pl.off_ring + rt.s * pl.chunk_bytes, c.codes + (x.sh * K + r0) * V, uint32_t(n) * V,
+                              ring_full + rt.s);
+                    rt.next(pl.ring);
+                    ++nch;
                 }
             }
+            ht.next(pl.heads);
             ok = __shfl_sync(0xffffffffu, int(ok), 0) != 0;
         }
-        if (!ok && lane == 0) {  // a wait ran out: let the copies that were issued land before the block ends
-            for (int i = 0; i < pl.heads && i < it; ++i)
-                tc::mbar_drain(head_full + i, uint32_t((it - 1 - i) / pl.heads) & 1u);
-            for (uint32_t i = 0; i < uint32_t(pl.ring) && i < nch; ++i)
-                tc::mbar_drain(ring_full + i, ((nch - 1 - i) / pl.ring) & 1u);
+        if (!ok && lane == 0) {
+            // a wait ran out: let the copies that were issued land (each wait with its limit) before the block ends
+            constexpr long long limit = 100000000LL;
+            for (uint32_t par = 0; par < 2; ++par) {
+                for (int i = 0; i < 2; ++i) tc::mbar_drain(head_full + i, par, limit);
+                for (int i = 0; i < pl.ring; ++i) tc::mbar_drain(ring_full + i, par, limit);
+            }
         }
         return;
     }
@@ -551,53 +677,63 @@ __global__ void __launch_bounds__(kStreamThreads + 32, 1)
     float* dec = reinterpret_cast<float*>(dyn + pl.off_dec);  // [K] e^G
     float* wq = reinterpret_cast<float*>(dyn + pl.off_wq);    // [groups][K] q e^G scale
     float* ps = reinterpret_cast<float*>(dyn + pl.off_p);     // [64] scores
-    float* red = reinterpret_cast<float*>(dyn + pl.off_red);  // [slices][V]
+    float* red = reinterpret_cast<float*>(dyn + pl.off_red);  // [slices][V], or [warps][128]
     const int unit = tid / pl.lanes, ugrp = unit % NG, slice = unit / NG;
     const int ucol = ugrp * kG + (tid % pl.lanes) * 16;
     const bool reads = slice < pl.slices;
-    int it = 0;
-    uint32_t nch = 0;
+    // the keys' phase: K channels (or as many as there are threads) x parts of the window
+    const int parts = K >= kStreamThreads ? 1 : kStreamThreads / K, part = K >= kStreamThreads ? 0 : tid / K;
+    Turn ht, rt;
     bool ok = true;
     // a wait that ran out leaves `ok` false: the thread then writes nothing, but keeps step with the block's barriers
-    for (int64_t item = blockIdx.x; item < items; item += gridDim.x, ++it) {
-        const int hs = it % pl.heads;
-        ok = ok && tc::mbar_wait(head_full + hs, uint32_t(it / pl.heads) & 1u, err, &abort_flag);
-        HeadInfo hi{0, 0, 0};
-        if (ok) hi = info[hs];
+    for (int it = 0; it < items; ++it) {
+        const int hs = ht.s;
+        ok = ok && warp_wait(head_full + hs, ht.par, err, &abort_flag);
+        Item x{0, 0, 0, -1, 0};
+        if (ok) x = info[hs];
         const char* st = dyn + hs * pl.head_bytes;
         const T* qb = reinterpret_cast<const T*>(st);
-        const T* kb = reinterpret_cast<const T*>(st + pl.off_k);
         const T* vb = reinterpret_cast<const T*>(st + pl.off_v);
-        const float* gb = reinterpret_cast<const float*>(st + pl.off_g);
-        const T* kw = reinterpret_cast<const T*>(st + pl.off_kw);
-        const float* gw = reinterpret_cast<const float*>(st + pl.off_gw);
         const T* vw = reinterpret_cast<const T*>(st + pl.off_vw);
         const float* sc = reinterpret_cast<const float*>(st + pl.off_sc);
-        const int n = hi.n, used = n + 1;
-        if (hi.live) {
-            T* pk = static_cast<T*>(c.k) + (hi.sh * c.W + n) * K;
-            T* pv = static_cast<T*>(c.v) + (hi.sh * c.W + n) * V;
-            float* pg = c.la + (hi.sh * c.W + n) * K;
-            for (int r = tid; r < K; r += kStreamThreads) {
-                const float la = !gate_rows ? gate_log_alpha(ga, item, 0, r, 1, K)
+        const int n = x.n, used = n + 1;
+        if (x.live) {
+            const T* kb = reinterpret_cast<const T*>(st + pl.off_k);
+            const float* gb = reinterpret_cast<const float*>(st + pl.off_g);
+            const T* kw = reinterpret_cast<const T*>(st + pl.off_kw);
+            const float* gw = reinterpret_cast<const float*>(st + pl.off_gw);
+            const int64_t place = x.sh * c.W + n;  // of the token in the window; its k and log a are put there once a head
+            for (int r = K >= kStreamThreads ? tid : tid - part * K; r < K && part < parts; r += kStreamThreads) {
+                // tokens [lo, hi) of the window; the sum of the log decays behind them first
+                const int lo = n * part / parts, hi = n * (part + 1) / parts;
+                const float la = !gate_rows ? gate_log_alpha(ga, x.bh, 0, r, 1, K)
                                  : ga.kind == kGatePreact ? logsigmoid_f(gb[r]) * ga.inv_tau : gb[r];
-                kt[n * K + r] = ldf(kb + r);
-                pk[r] = kb[r];
-                pg[r] = la;
                 float D = la;
+                for (int j = n - 1; j >= hi; --j) D += gw[j * K + r];
 #pragma unroll 4
-                for (int j = n - 1; j >= 0; --j) {
+                for (int j = hi - 1; j >= lo; --j) {
                     kt[j * K + r] = ldf(kw + j * K + r) * tc::exp2_ftz(D * tc::kLog2e);
                     D += gw[j * K + r];
                 }
-                const float d = tc::exp2_ftz(D * tc::kLog2e), qd = ldf(qb + r) * d;
-                dec[r] = d;
-                for (int g = 0; g < NG; ++g) wq[g * K + r] = qd * sc[r * NG + g];
+                if (part == parts - 1) {
+                    kt[n * K + r] = ldf(kb + r);
+                    if (x.grp <= 0) {
+                        static_cast<T*>(c.k)[place * K + r] = kb[r];
+                        c.la[place * K + r] = la;
+                    }
+                }
+                if (part == 0) {
+                    const float d = tc::exp2_ftz(D * tc::kLog2e), qd = ldf(qb + r) * d;
+                    dec[r] = d;
+                    if (x.grp < 0)
+                        for (int g = 0; g < NG; ++g) wq[g * K + r] = qd * sc[r * NG + g];
+                }
             }
-            for (int x = tid; x < V; x += kStreamThreads) pv[x] = vb[x];
+            const int v0 = x.grp < 0 ? 0 : x.grp * kG, v1 = x.grp < 0 || v0 + kG > V ? V : v0 + kG;
+            for (int i = v0 + tid; i < v1; i += kStreamThreads) static_cast<T*>(c.v)[place * V + i] = vb[i];
         }
         tc::named_sync(1, kStreamThreads);
-        if (hi.live) {
+        if (x.live && x.grp < 0) {
             for (int j = warp; j < used; j += kStreamWarps) {
                 float s = 0.f;
                 for (int r = lane; r < K; r += 32) s = fmaf(ldf(qb + r), kt[j * K + r], s);
@@ -608,102 +744,98 @@ __global__ void __launch_bounds__(kStreamThreads + 32, 1)
             float2 acc[8];
 #pragma unroll
             for (int e = 0; e < 8; ++e) acc[e] = make_float2(0.f, 0.f);
-            for (int ch = 0; ch < chunks; ++ch, ++nch) {
-                const uint32_t s = nch % pl.ring;
-                ok = ok && tc::mbar_wait(ring_full + s, (nch / pl.ring) & 1u, err, &abort_flag);
-                const int r0 = ch * pl.chunk_rows, rows = K - r0 < pl.chunk_rows ? K - r0 : pl.chunk_rows;
-                const char* src = dyn + pl.off_ring + s * pl.chunk_bytes + ucol;
-                const float* w = wq + ugrp * K + r0;
+            for (int ch = 0; ch < chunks; ++ch) {
+                ok = ok && warp_wait(ring_full + rt.s, rt.par, err, &abort_flag);
+                const int r0 = ch * pl.chunk_rows, rn = K - r0 < pl.chunk_rows ? K - r0 : pl.chunk_rows;
+                const char* src = dyn + pl.off_ring + rt.s * pl.chunk_bytes + ucol + slice * V;
+                const float* w = wq + ugrp * K + r0 + slice;
                 if (reads && ok) {
 #pragma unroll 2
-                    for (int r = slice; r < rows; r += pl.slices) {
-                        const uint4 x = *reinterpret_cast<const uint4*>(src + r * V);
-                        const float2 w2 = make_float2(w[r], w[r]);
+                    for (int r = slice; r < rn; r += pl.slices, src += pl.slices * V, w += pl.slices) {
+                        const uint4 z = *reinterpret_cast<const uint4*>(src);
+                        const float2 w2 = make_float2(*w, *w);
                         float2 y[8];
-                        decode4<INT8>(x.x, y);
-                        decode4<INT8>(x.y, y + 2);
-                        decode4<INT8>(x.z, y + 4);
-                        decode4<INT8>(x.w, y + 6);
+                        decode4<INT8>(z.x, y);
+                        decode4<INT8>(z.y, y + 2);
+                        decode4<INT8>(z.z, y + 4);
+                        decode4<INT8>(z.w, y + 6);
 #pragma unroll
                         for (int e = 0; e < 8; ++e) acc[e] = fma2(w2, y[e], acc[e]);
                     }
                 }
                 __syncwarp();
-                if (lane == 0) tc::mbar_arrive(ring_empty + s);
+                if (lane == 0) tc::mbar_arrive(ring_empty + rt.s);
+                rt.next(pl.ring);
             }
             if (reads) {
                 float4* d = reinterpret_cast<float4*>(red + slice * V + ucol);
 #pragma unroll
                 for (int e = 0; e < 4; ++e) d[e] = make_float4(acc[2 * e].x, acc[2 * e].y, acc[2 * e + 1].x, acc[2 * e + 1].y);
             }
+        } else if (x.live) {
+            // one group of a head whose window is full
+            uint8_t* codes = c.codes + x.sh * K * V;
+            float* scale = c.scale + x.sh * K * NG + x.grp;
+            const Cols<true> cols(x.grp, V);
+            float acc[4] = {0.f, 0.f, 0.f, 0.f};
+            for (int r = warp * kBatch; r < K; r += kStreamWarps * kBatch) {
+                uint32_t z[kBatch];
+                float f[kBatch], y[kBatch][4];
+#pragma unroll
+                for (int i = 0; i < kBatch; ++i) {
+                    z[i] = cols.codes(codes + int64_t(r + i) * V);
+                    f[i] = sc[(r + i) * NG + x.grp];
+                }
+                const auto value = [&](int j, float2* t) {
+                    const T* vr = (j < n ? vw + j * V : vb) + cols.col[0];
+                    t[0] = t[1] = make_float2(0.f, 0.f);
+                    if (!cols.on[0]) return;
+                    if constexpr (sizeof(T) == 2) {
+                        const uint2 w = *reinterpret_cast<const uint2*>(vr);
+                        t[0] = __bfloat1622float2(*reinterpret_cast<const __nv_bfloat162*>(&w.x));
+                        t[1] = __bfloat1622float2(*reinterpret_cast<const __nv_bfloat162*>(&w.y));
+                    } else {
+                        const float4 w = *reinterpret_cast<const float4*>(vr);
+                        t[0] = make_float2(w.x, w.y);
+                        t[1] = make_float2(w.z, w.w);
+                    }
+                };
+                form_rows<INT8>(z, f, dec + r, kt + r, K, used, value, y);
+#pragma unroll
+                for (int i = 0; i < kBatch; ++i) {
+                    const float qr = ldf(qb + r + i);
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) acc[e] = fmaf(qr, y[i][e], acc[e]);
+                }
+                put_rows<INT8, true>(cols, y, kBatch, codes + int64_t(r) * V, V, scale + int64_t(r) * NG, NG);
+            }
+            *reinterpret_cast<float4*>(red + warp * kG + 4 * lane) = make_float4(acc[0], acc[1], acc[2], acc[3]);
         }
         tc::named_sync(1, kStreamThreads);
-        if (ok) {
-            for (int x = tid; x < V; x += kStreamThreads) {
+        if (ok && x.grp < 0) {
+            for (int i = tid; i < V; i += kStreamThreads) {
                 float s = 0.f;
-                if (hi.live) {
+                if (x.live) {
 #pragma unroll 8
-                    for (int i = 0; i < pl.slices; ++i) s += red[i * V + x];
-                    for (int j = 0; j < n; ++j) s = fmaf(ps[j], ldf(vw + j * V + x), s);
-                    s = fmaf(ps[n], ldf(vb + x), s);
+                    for (int r = 0; r < pl.slices; ++r) s += red[r * V + i];
+                    for (int j = 0; j < n; ++j) s = fmaf(ps[j], ldf(vw + j * V + i), s);
+                    s = fmaf(ps[n], ldf(vb + i), s);
                 }
-                stf(o + item * V + x, s);
+                stf(o + x.bh * V + i, s);
             }
-        }
-        if (ok && hi.live && used == c.W) {
-            // the window is full: round the state back (its codes are in L2 by now)
-            uint8_t* codes = c.codes + hi.sh * K * V;
-            float* scale = c.scale + hi.sh * K * NG;
-            for (int u = warp; u < K / kBatch * NG; u += kStreamWarps) {
-                const int grp = u % NG, r = u / NG * kBatch;
-                const Cols<true> cols(grp, V);
-                uint32_t z[kBatch];
-                float2 y[kBatch][2];
+        } else if (ok && tid < kG && x.grp * kG + tid < V) {
+            float s = 0.f;
+            if (x.live) {
 #pragma unroll
-                for (int i = 0; i < kBatch; ++i) z[i] = cols.codes(codes + int64_t(r + i) * V);
-#pragma unroll
-                for (int i = 0; i < kBatch; ++i) {
-                    decode4<INT8>(z[i], y[i]);
-                    const float f = sc[(r + i) * NG + grp], d = dec[r + i];
-#pragma unroll
-                    for (int e = 0; e < 2; ++e)
-                        y[i][e] = mul2(make_float2(d, d), mul2(make_float2(f, f), y[i][e]));
-                }
-                for (int j = 0; j < used; ++j) {
-                    const T* vr = (j < n ? vw + j * V : vb) + cols.col[0];
-                    float2 vv[2] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f)};
-                    if (cols.on[0]) {
-                        if constexpr (sizeof(T) == 2) {
-                            const uint2 t = *reinterpret_cast<const uint2*>(vr);
-                            vv[0] = __bfloat1622float2(*reinterpret_cast<const __nv_bfloat162*>(&t.x));
-                            vv[1] = __bfloat1622float2(*reinterpret_cast<const __nv_bfloat162*>(&t.y));
-                        } else {
-                            const float4 t = *reinterpret_cast<const float4*>(vr);
-                            vv[0] = make_float2(t.x, t.y);
-                            vv[1] = make_float2(t.z, t.w);
-                        }
-                    }
-                    const float4 ka = *reinterpret_cast<const float4*>(kt + j * K + r);
-                    const float4 kc = *reinterpret_cast<const float4*>(kt + j * K + r + 4);
-                    const float kk[kBatch] = {ka.x, ka.y, ka.z, ka.w, kc.x, kc.y, kc.z, kc.w};
-#pragma unroll
-                    for (int i = 0; i < kBatch; ++i) {
-                        const float2 k2 = make_float2(kk[i], kk[i]);
-                        y[i][0] = fma2(k2, vv[0], y[i][0]);
-                        y[i][1] = fma2(k2, vv[1], y[i][1]);
-                    }
-                }
-#pragma unroll
-                for (int i = 0; i < kBatch; ++i) {
-                    const float t[4] = {y[i][0].x, y[i][0].y, y[i][1].x, y[i][1].y};
-                    const float ns = scale_of<INT8>(warp_amax(t));
-                    cols.put_codes(codes + int64_t(r + i) * V, encode4<INT8>(t, ns));
-                    if (lane == 0) scale[int64_t(r + i) * NG + grp] = ns;
-                }
+                for (int w = 0; w < kStreamWarps; ++w) s += red[w * kG + tid];
             }
+            stf(o + x.bh * V + x.grp * kG + tid, s);
         }
-        tc::named_sync(1, kStreamThreads);  // the next head overwrites kt and dec
+        // red is written again only behind the next head's first barrier, kt and dec were last read in front of this
+        // head's second one
+        __syncwarp();
         if (lane == 0) tc::mbar_arrive(head_empty + hs);
+        ht.next(pl.heads);
     }
 }
 
@@ -794,9 +926,9 @@ StreamPlan stream_plan(const CacheProblem& p) {
         pl.off_dec = take(K * 4);
         pl.off_wq = take(K * NG * 4);
         pl.off_p = take(64 * 4);
-        pl.off_red = take(pl.slices * V * 4);
+        pl.off_red = take((pl.slices * V > kStreamWarps * kG ? pl.slices * V : kStreamWarps * kG) * 4);
         pl.off_ring = at;
-        const int64_t room = int64_t(kStreamSmem) - 1024 - at;
+        const int64_t room = int64_t(kStreamSmem) - 4096 - at;
         const int64_t ring = room > 0 ? room / pl.chunk_bytes : 0;
         if (ring >= 3) {
             pl.heads = heads;
@@ -814,10 +946,13 @@ gla_status stream_typed(const CacheProblem& p, const StreamPlan& pl, const void*
     const Pool c = pool_of(p);
     const GateArgs ga{la, p.gate, p.inv_tau, p.H};
     if (!allow_smem(k_cache_stream<T, INT8>, pl.smem)) return GLA_ERR_CUDA;
-    const int64_t items = p.B * p.H;
-    GLA_LAUNCH("cache_step", (k_cache_stream<T, INT8>), unsigned(items < 148 ? items : 148), kStreamThreads + 32, pl.smem,
-               s, c, pl, items, static_cast<const T*>(q), static_cast<const T*>(k), static_cast<const T*>(v), ga, slots,
-               lengths, static_cast<T*>(o), device_error_word());
+    for (int64_t b0 = 0; b0 < p.B; b0 += kMaxRows) {
+        const int n = int(p.B - b0 < kMaxRows ? p.B - b0 : kMaxRows);
+        const int64_t most = n * p.H * c.NG;  // a block for every group, were they all to fold
+        GLA_LAUNCH("cache_step", (k_cache_stream<T, INT8>), unsigned(most < 148 ? most : 148), kStreamThreads + 32, pl.smem,
+                   s, c, pl, n, b0, static_cast<const T*>(q), static_cast<const T*>(k), static_cast<const T*>(v), ga, slots,
+                   lengths, static_cast<T*>(o), device_error_word());
+    }
     return GLA_OK;
 }
 
