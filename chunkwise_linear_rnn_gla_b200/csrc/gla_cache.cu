@@ -27,6 +27,7 @@ namespace {
 constexpr int kG = kCacheGroup;
 constexpr int kThreads = 256;
 constexpr int kWarps = kThreads / 32;
+constexpr int kSms = 148;
 constexpr int kBatch = 8;        // state rows a warp takes at a time
 constexpr float kTiny = 1e-30f;  // a group whose largest magnitude is below this is held as zero
 
@@ -455,32 +456,38 @@ __global__ void __launch_bounds__(kThreads, 4) k_cache_step(Pool c, const T* __r
 }
 
 // ---- step, streamed ---------------------------------------------------------------------------
-// For the shapes that bulk copies can move (stream_plan below). One persistent block per SM takes its share of the heads.
-// A producer warp keeps copies in flight without a pause, across heads: a head's codes are one contiguous stretch,
-// fetched in chunks of about 16 KB through a ring, and the token, the window and the scales of the next head travel
-// while this one is computed. 16 warps read the chunks (16 codes a lane), so memory does not wait for the window's
-// exponentials or the reductions.
+// For calls with heads enough to give every SM some, of shapes that bulk copies can move (stream_plan below). One
+// persistent block per SM takes its share of the heads; its warps have three parts, a head apart in time:
+//   1 producer   one thread keeps copies in flight across heads: a head's codes are one contiguous stretch, fetched in
+//                chunks through a ring, and its token, window and scales travel ahead of them;
+//   4 windows    form the keys k_j e^{D_j}, the scores p_j and the row weights q e^G scale of the next head;
+//  12 readers    multiply the chunks (16 codes a lane) with the row weights and add the window's part.
+// So memory does not wait for the window's exponentials, and the ring (about 100 KB in flight an SM) covers the latency
+// of DRAM and the readers' reductions. As one sequence of phases in one block the same work took twice the time.
 //
 // A head whose window is full costs several times the others (every entry takes `window` multiply-adds and is rounded),
 // so it is split into its groups of 128 columns, which share nothing but the window: each is an item of its own that
 // forms its columns of S_t, reads o from them and rounds them back. The blocks' shares are cut by cost, from the lengths
 // that every block reads.
-constexpr int kStreamThreads = 512;           // readers
-constexpr int kStreamWarps = kStreamThreads / 32;
-constexpr int kMaxRing = 8;
+constexpr int kReadWarps = 12, kWinWarps = 4;
+constexpr int kReadThreads = kReadWarps * 32, kWinThreads = kWinWarps * 32;
+constexpr int kStreamThreads = kReadThreads + kWinThreads + 32;
+constexpr int kMaxRing = 12;
 constexpr int kMaxRows = 1024;                // rows of a call in one launch
+constexpr int kDead = 255;
 constexpr int kFoldCost = 6;                  // of a folding group, where an ordinary head costs its number of groups
-constexpr size_t kStreamSmem = 227 * 1024;
+constexpr size_t kStreamSmem = 227 * 1024 - 8192;  // less the static part
 
 struct StreamPlan {
-    int heads;        // stages of token, window and scales: 1 or 2
     int ring;         // chunks in flight
     int chunk_rows;   // state rows of a chunk
     int lanes;        // lanes that share a group's row (16 codes each)
     int slices;       // rows read at a time
-    int off_k, off_v, off_g, off_kw, off_gw, off_vw, off_sc, head_bytes;  // within a stage
-    int off_kt, off_dec, off_wq, off_p, off_red, off_ring, chunk_bytes;
-    size_t smem;
+    int off_q, off_k, off_g, off_kw, off_gw, off_sc;   // what the window warps read
+    int off_v, off_vw;                                 // what the readers read
+    int off_kt, off_dec, off_wq, off_p, win_bytes;     // what the window warps leave (two heads' worth)
+    int off_red, off_ring, chunk_bytes;
+    size_t smem;      // 0: not for this shape
 };
 
 struct Item {
@@ -499,8 +506,12 @@ __device__ __forceinline__ void bulk_copy(void* dst, const void* src, uint32_t b
 
 // A wait of a whole warp, which then agrees on its outcome.
 __device__ __forceinline__ bool warp_wait(uint64_t* bar, uint32_t parity, int* err, int* abort) {
-    const bool ok = tc::mbar_wait(bar, parity, err, abort);
+    const bool ok = tc::mbar_wait_poll(bar, parity, err, abort);
     return __all_sync(0xffffffffu, ok) != 0;
+}
+__device__ __forceinline__ void warp_arrive(uint64_t* bar) {
+    __syncwarp();
+    if ((threadIdx.x & 31) == 0) tc::mbar_arrive(bar);
 }
 
 // A ring position: stage and the parity of its turn.
@@ -513,14 +524,14 @@ struct Turn {
 };
 
 // This block's items: of the folding groups (all of them first, then the other heads, in the order of `rows`) those
-// whose cost begins in the block's share.
+// whose cost begins in the block's share. The host keeps the total below 2^27.
 struct Share {
-    int64_t f0, f1, h0, h1;
-    __device__ __forceinline__ Share(int folds, int B, int64_t H, int NG) {
-        const int64_t fg = folds * H * NG, hd = (B - folds) * H, total = fg * kFoldCost + hd * NG;
-        const int64_t lo = total * blockIdx.x / gridDim.x, hi = total * (blockIdx.x + 1) / gridDim.x;
-        const auto first = [](int64_t from, int64_t cost, int64_t most) {
-            const int64_t i = from <= 0 ? 0 : (from + cost - 1) / cost;
+    int f0, f1, h0, h1;
+    __device__ __forceinline__ Share(int folds, int B, int H, int NG) {
+        const int fg = folds * H * NG, hd = (B - folds) * H, total = fg * kFoldCost + hd * NG;
+        const int per = (total + int(gridDim.x) - 1) / int(gridDim.x), lo = per * int(blockIdx.x), hi = lo + per;
+        const auto first = [](int from, int cost, int most) {
+            const int i = from <= 0 ? 0 : (from + cost - 1) / cost;
             return i < most ? i : most;
         };
         f0 = first(lo, kFoldCost, fg);
@@ -528,219 +539,262 @@ struct Share {
         h0 = first(lo - fg * kFoldCost, NG, hd);
         h1 = first(hi - fg * kFoldCost, NG, hd);
     }
-    __device__ __forceinline__ int64_t count() const { return (f1 - f0) + (h1 - h0); }
+    __device__ __forceinline__ int count() const { return (f1 - f0) + (h1 - h0); }
 };
 
 template <typename T, bool INT8>
-__global__ void __launch_bounds__(kStreamThreads + 32, 1)
+__global__ void __launch_bounds__(kStreamThreads, 1)
     k_cache_stream(Pool c, StreamPlan pl, int B, int64_t b0, const T* __restrict__ q, const T* __restrict__ k,
                    const T* __restrict__ v, GateArgs ga, const int32_t* __restrict__ slots,
                    const int32_t* __restrict__ lengths, T* __restrict__ o, int* err) {
     extern __shared__ __align__(128) char dyn[];
-    __shared__ uint64_t head_full[2], head_empty[2], ring_full[kMaxRing], ring_empty[kMaxRing];
-    __shared__ Item info[2];
-    __shared__ uint16_t rows[kMaxRows];  // the call's rows, those whose window is full first
-    __shared__ int warp_folds[kStreamWarps], abort_flag;
+    // a: the window warps' inputs; b: the readers' values; w: the window warps' results
+    __shared__ uint64_t a_full, a_empty, b_full, b_empty, w_full[2], w_empty[2], ring_full[kMaxRing], ring_empty[kMaxRing];
+    __shared__ Item a_info, w_info[2];
+    __shared__ __align__(16) int32_t row_slot[kMaxRows];
+    __shared__ uint16_t rows[kMaxRows];
+    __shared__ uint8_t row_n[kMaxRows];
+    __shared__ int warp_folds[16], abort_flag;
     const int tid = int(threadIdx.x), lane = tid & 31, warp = tid >> 5;
     const int K = c.K, V = c.V, NG = c.NG;
     const bool gate_rows = ga.kind == kGateChannel || ga.kind == kGatePreact;
-    if (tid == 0) {
-        abort_flag = 0;
-        for (int i = 0; i < 2; ++i) tc::mbar_init(head_full + i, 1), tc::mbar_init(head_empty + i, kStreamWarps);
-        for (int i = 0; i < kMaxRing; ++i) tc::mbar_init(ring_full + i, 1), tc::mbar_init(ring_empty + i, kStreamWarps);
-        tc::fence_barrier_init();
-    }
-    // rows that fold, from the front; the others, from the back
+    // What every row of the call asks for: its place in the window (kDead: nothing), and the order in which the blocks
+    // take the rows: those that fold first.
     int folds = 0;
     {
-        static_assert(kMaxRows == 2 * kStreamThreads, "two rows a thread");
-        int mine[2] = {0, 0}, before[2] = {0, 0};
-        if (warp < kStreamWarps) {
+        static_assert(kMaxRows == 2 * 16 * 32 && kReadWarps + kWinWarps == 16, "two rows a thread");
+        int fold[2] = {0, 0}, before[2] = {0, 0};
+        if (warp < 16) {
             int count = 0;
 #pragma unroll
             for (int u = 0; u < 2; ++u) {
                 const int b = 64 * warp + 32 * u + lane;
                 if (b < B) {
-                    const int32_t len = lengths[b0 + b];
-                    mine[u] = len >= 0 && slots[b0 + b] >= 0 && len % c.W == c.W - 1;
-                }
-                const uint32_t m = __ballot_sync(0xffffffffu, mine[u]);
+                    const int32_t len = lengths[b0 + b], slot = slots[b0 + b];
+                    const bool named = slot >= 0, good = slot < c.slots && len >= 0;
+                    if (named && !good && blockIdx.x == 0) atomicOr(err, kErrBadRow);
+                    const int n = named && good ? len % c.W : kDead;
+                    row_slot[b] = n == kDead ? -1 : slot;
+                    row_n[b] = uint8_t(n);
+                    fold[u] = n == c.W - 1;
+                } else row_slot[b] = -1;
+                const uint32_t m = __ballot_sync(0xffffffffu, fold[u]);
                 before[u] = count + __popc(m & ((1u << lane) - 1));
                 count += __popc(m);
             }
             if (lane == 0) warp_folds[warp] = count;
+        } else if (lane == 0) {
+            abort_flag = 0;
+            tc::mbar_init(&a_full, 1), tc::mbar_init(&a_empty, kWinWarps);
+            tc::mbar_init(&b_full, 1), tc::mbar_init(&b_empty, kReadWarps);
+            for (int i = 0; i < 2; ++i) tc::mbar_init(w_full + i, kWinWarps), tc::mbar_init(w_empty + i, kReadWarps);
+            for (int i = 0; i < pl.ring; ++i) tc::mbar_init(ring_full + i, 1), tc::mbar_init(ring_empty + i, kReadWarps);
+            tc::fence_barrier_init();
         }
         __syncthreads();
         int first = 0;
-        for (int w = 0; w < kStreamWarps; ++w) {
+        for (int w = 0; w < 16; ++w) {
             if (w < warp) first += warp_folds[w];
             folds += warp_folds[w];
         }
-        if (warp < kStreamWarps) {
+        if (warp < 16) {
 #pragma unroll
             for (int u = 0; u < 2; ++u) {
                 const int b = 64 * warp + 32 * u + lane;
-                const int f = first + before[u];  // folding rows in front of b
-                if (b < B) rows[mine[u] ? f : folds + b - f] = uint16_t(b);
+                if (b < B) {
+                    const int f = first + before[u];  // folding rows in front of b
+                    rows[fold[u] ? f : folds + b - f] = uint16_t(b);
+                    // a slot that an earlier row names too
+                    const int32_t slot = row_slot[b];
+                    bool twice = false;
+                    for (int i = 0; i < 64 * warp + 32 * u + 32; i += 4) {
+                        const int4 t = *reinterpret_cast<const int4*>(row_slot + i);
+                        twice |= (t.x == slot && i < b) | (t.y == slot && i + 1 < b) | (t.z == slot && i + 2 < b) |
+                                 (t.w == slot && i + 3 < b);
+                    }
+                    for (int64_t i = 0; i < b0; ++i) twice |= slots[i] == slot;
+                    if (twice && slot >= 0) {
+                        row_n[b] = kDead;
+                        if (blockIdx.x == 0) atomicOr(err, kErrBadRow);
+                    }
+                }
             }
         }
         __syncthreads();
     }
-    const Share share(folds, B, c.H, NG);
-    const int items = int(share.count());
+    const Share share(folds, B, int(c.H), NG);
+    const int items = share.count();
     const int chunks = (K + pl.chunk_rows - 1) / pl.chunk_rows;
-    if (warp == kStreamWarps) {
-        // ---- producer: all lanes walk the items (they share the search for a slot named before), lane 0 copies
-        Turn ht, rt;
-        int it = 0;
+    // A wait that ran out leaves a thread's `ok` false: it then writes nothing, but keeps step with the block's barriers.
+    bool ok = true;
+    if (warp == kReadWarps + kWinWarps) {
+        // ---- producer
+        if (lane != 0) return;
+        Turn rt;
+        uint32_t live_par = 0;  // of the values' stage, which only live items use
+        int lives = 0;
         int64_t nch = 0;
-        bool ok = true;
-        for (; it < items && ok; ++it) {
+        for (int it = 0; it < items && ok; ++it) {
             Item x;
-            int b;
-            int64_t head;
-            if (it < share.f1 - share.f0) {
-                const int64_t f = share.f0 + it;
-                x.grp = int(f % NG);
-                b = rows[f / NG / c.H];
-                head = f / NG % c.H;
+            int b, head;
+            const bool fold = it < share.f1 - share.f0;
+            if (fold) {
+                const int f = share.f0 + it;
+                x.grp = f % NG;
+                b = rows[f / NG / int(c.H)];
+                head = f / NG % int(c.H);
             } else {
-                const int64_t h = share.h0 + it - (share.f1 - share.f0);
+                const int h = share.h0 + it - (share.f1 - share.f0);
                 x.grp = -1;
-                b = rows[folds + h / c.H];
-                head = h % c.H;
+                b = rows[folds + h / int(c.H)];
+                head = h % int(c.H);
             }
-            const int32_t slot = slots[b0 + b], len = lengths[b0 + b];
-            bool live = slot >= 0;
-            if (live) {
-                bool bad = slot >= c.slots || len < 0;
-                for (int64_t i = lane; i < b0 + b; i += 32) bad |= slots[i] == slot;
-                if (__any_sync(0xffffffffu, bad)) {
-                    live = false;
-                    if (lane == 0) atomicOr(err, kErrBadRow);
-                }
+            x.live = row_n[b] != kDead;
+            x.bh = (b0 + b) * c.H + head;
+            x.sh = x.live ? row_slot[b] * c.H + head : 0;
+            x.n = x.live ? row_n[b] : 0;
+            const uint32_t n = uint32_t(x.n), kb = uint32_t(K) * sizeof(T), vb = uint32_t(V) * sizeof(T), gb = uint32_t(K) * 4u;
+            if (it > 0) ok = tc::mbar_wait_poll(&a_empty, uint32_t(it - 1) & 1u, err, &abort_flag);
+            if (!ok) break;
+            a_info = x;
+            if (!x.live) {
+                tc::mbar_arrive(&a_full);
+                continue;
             }
-            if (lane == 0) {
-                const int hs = ht.s;
-                if (it >= pl.heads) ok = tc::mbar_wait(head_empty + hs, ht.par ^ 1u, err, &abort_flag);
-                x.bh = (b0 + b) * c.H + head;
-                x.sh = live ? slot * c.H + head : 0;
-                x.n = live ? len % c.W : 0;
-                x.live = live;
-                if (ok) {
-                    info[hs] = x;
-                    if (!live) tc::mbar_arrive(head_full + hs);
-                    else {
-                        char* st = dyn + hs * pl.head_bytes;
-                        const uint32_t kb = uint32_t(K) * sizeof(T), vb = uint32_t(V) * sizeof(T), gb = uint32_t(K) * 4u;
-                        const uint32_t sb = uint32_t(K) * NG * 4u;
-                        tc::mbar_arrive_expect_tx(head_full + hs,
-                                                  2 * kb + vb + (gate_rows ? gb : 0u) + sb + x.n * (kb + gb + vb));
-                        if (x.n > 0) {
-                            bulk_copy(st + pl.off_gw, c.la + x.sh * c.W * K, x.n * gb, head_full + hs);
-                            bulk_copy(st + pl.off_kw, static_cast<T*>(c.k) + x.sh * c.W * K, x.n * kb, head_full + hs);
-                            bulk_copy(st + pl.off_vw, static_cast<T*>(c.v) + x.sh * c.W * V, x.n * vb, head_full + hs);
-                        }
-                        bulk_copy(st, q + x.bh * K, kb, head_full + hs);
-                        bulk_copy(st + pl.off_k, k + x.bh * K, kb, head_full + hs);
-                        bulk_copy(st + pl.off_v, v + x.bh * V, vb, head_full + hs);
-                        if (gate_rows) bulk_copy(st + pl.off_g, ga.g + x.bh * K, gb, head_full + hs);
-                        bulk_copy(st + pl.off_sc, c.scale + x.sh * K * NG, sb, head_full + hs);
-                    }
-                }
-                for (int ch = 0; ch < chunks && live && x.grp < 0 && ok; ++ch) {
-                    if (nch >= pl.ring) ok = tc::mbar_wait(ring_empty + rt.s, rt.par ^ 1u, err, &abort_flag);
-                    if (!ok) break;
-                    const int r0 = ch * pl.chunk_rows, n = K - r0 < pl.chunk_rows ? K - r0 : pl.chunk_rows;
-                    tc::mbar_arrive_expect_tx(ring_full + rt.s, uint32_t(n) * V);
-                    bulk_copy(dyn + pl.off_ring + rt.s * pl.chunk_bytes, c.codes + (x.sh * K + r0) * V, uint32_t(n) * V,
+            const uint32_t sb = uint32_t(K) * NG * 4u;
+            tc::mbar_arrive_expect_tx(&a_full, 2 * kb + (gate_rows ? gb : 0u) + sb + n * (kb + gb));
+            if (n > 0) {
+                bulk_copy(dyn + pl.off_gw, c.la + x.sh * c.W * K, n * gb, &a_full);
+                bulk_copy(dyn + pl.off_kw, static_cast<T*>(c.k) + x.sh * c.W * K, n * kb, &a_full);
+            }
+            bulk_copy(dyn + pl.off_q, q + x.bh * K, kb, &a_full);
+            bulk_copy(dyn + pl.off_k, k + x.bh * K, kb, &a_full);
+            if (gate_rows) bulk_copy(dyn + pl.off_g, ga.g + x.bh * K, gb, &a_full);
+            bulk_copy(dyn + pl.off_sc, c.scale + x.sh * K * NG, sb, &a_full);
+            const auto values = [&] {  // the values' stage is free once the head before has been written out
+                if (lives > 0) ok = tc::mbar_wait_poll(&b_empty, live_par ^ 1u, err, &abort_flag);
+                if (!ok) return;
+                tc::mbar_arrive_expect_tx(&b_full, (n + 1) * vb);
+                bulk_copy(dyn + pl.off_v, v + x.bh * V, vb, &b_full);
+                if (n > 0) bulk_copy(dyn + pl.off_vw, static_cast<T*>(c.v) + x.sh * c.W * V, n * vb, &b_full);
+                ++lives;
+                live_par ^= 1u;
+            };
+            // the readers free the values' stage behind the chunks of the head before: what of the ring is free goes first
+            int ch = 0;
+            const auto codes = [&](int upto) {
+                for (; ch < upto && ok; ++ch) {
+                    if (nch >= pl.ring) ok = tc::mbar_wait_poll(ring_empty + rt.s, rt.par ^ 1u, err, &abort_flag);
+                    if (!ok) return;
+                    const int r0 = ch * pl.chunk_rows, m = K - r0 < pl.chunk_rows ? K - r0 : pl.chunk_rows;
+                    tc::mbar_arrive_expect_tx(ring_full + rt.s, uint32_t(m) * V);
+                    bulk_copy(dyn + pl.off_ring + rt.s * pl.chunk_bytes, c.codes + (x.sh * K + r0) * V, uint32_t(m) * V,
                               ring_full + rt.s);
                     rt.next(pl.ring);
                     ++nch;
                 }
-            }
-            ht.next(pl.heads);
-            ok = __shfl_sync(0xffffffffu, int(ok), 0) != 0;
+            };
+            if (!fold) codes(chunks < pl.ring ? chunks : pl.ring);
+            if (ok) values();
+            if (!fold && ok) codes(chunks);
         }
-        if (!ok && lane == 0) {
+        if (!ok) {
             // a wait ran out: let the copies that were issued land (each wait with its limit) before the block ends
             constexpr long long limit = 100000000LL;
             for (uint32_t par = 0; par < 2; ++par) {
-                for (int i = 0; i < 2; ++i) tc::mbar_drain(head_full + i, par, limit);
+                tc::mbar_drain(&a_full, par, limit);
+                tc::mbar_drain(&b_full, par, limit);
                 for (int i = 0; i < pl.ring; ++i) tc::mbar_drain(ring_full + i, par, limit);
             }
         }
         return;
     }
-    // ---- readers
-    float* kt = reinterpret_cast<float*>(dyn + pl.off_kt);    // [W][K] k_j e^{D_j}
-    float* dec = reinterpret_cast<float*>(dyn + pl.off_dec);  // [K] e^G
-    float* wq = reinterpret_cast<float*>(dyn + pl.off_wq);    // [groups][K] q e^G scale
-    float* ps = reinterpret_cast<float*>(dyn + pl.off_p);     // [64] scores
-    float* red = reinterpret_cast<float*>(dyn + pl.off_red);  // [slices][V], or [warps][128]
-    const int unit = tid / pl.lanes, ugrp = unit % NG, slice = unit / NG;
-    const int ucol = ugrp * kG + (tid % pl.lanes) * 16;
-    const bool reads = slice < pl.slices;
-    // the keys' phase: K channels (or as many as there are threads) x parts of the window
-    const int parts = K >= kStreamThreads ? 1 : kStreamThreads / K, part = K >= kStreamThreads ? 0 : tid / K;
-    Turn ht, rt;
-    bool ok = true;
-    // a wait that ran out leaves `ok` false: the thread then writes nothing, but keeps step with the block's barriers
-    for (int it = 0; it < items; ++it) {
-        const int hs = ht.s;
-        ok = ok && warp_wait(head_full + hs, ht.par, err, &abort_flag);
-        Item x{0, 0, 0, -1, 0};
-        if (ok) x = info[hs];
-        const char* st = dyn + hs * pl.head_bytes;
-        const T* qb = reinterpret_cast<const T*>(st);
-        const T* vb = reinterpret_cast<const T*>(st + pl.off_v);
-        const T* vw = reinterpret_cast<const T*>(st + pl.off_vw);
-        const float* sc = reinterpret_cast<const float*>(st + pl.off_sc);
-        const int n = x.n, used = n + 1;
-        if (x.live) {
-            const T* kb = reinterpret_cast<const T*>(st + pl.off_k);
-            const float* gb = reinterpret_cast<const float*>(st + pl.off_g);
-            const T* kw = reinterpret_cast<const T*>(st + pl.off_kw);
-            const float* gw = reinterpret_cast<const float*>(st + pl.off_gw);
-            const int64_t place = x.sh * c.W + n;  // of the token in the window; its k and log a are put there once a head
-            for (int r = K >= kStreamThreads ? tid : tid - part * K; r < K && part < parts; r += kStreamThreads) {
-                // tokens [lo, hi) of the window; the sum of the log decays behind them first
-                const int lo = n * part / parts, hi = n * (part + 1) / parts;
-                const float la = !gate_rows ? gate_log_alpha(ga, x.bh, 0, r, 1, K)
-                                 : ga.kind == kGatePreact ? logsigmoid_f(gb[r]) * ga.inv_tau : gb[r];
-                float D = la;
-                for (int j = n - 1; j >= hi; --j) D += gw[j * K + r];
+    if (warp >= kReadWarps) {
+        // ---- window warps
+        const int t = tid - kReadThreads, w = warp - kReadWarps;
+        const T* qb = reinterpret_cast<const T*>(dyn + pl.off_q);
+        const T* kb = reinterpret_cast<const T*>(dyn + pl.off_k);
+        const float* gb = reinterpret_cast<const float*>(dyn + pl.off_g);
+        const T* kw = reinterpret_cast<const T*>(dyn + pl.off_kw);
+        const float* gw = reinterpret_cast<const float*>(dyn + pl.off_gw);
+        const float* sc = reinterpret_cast<const float*>(dyn + pl.off_sc);
+        Turn wt;
+        for (int it = 0; it < items; ++it) {
+            ok = ok && warp_wait(&a_full, uint32_t(it) & 1u, err, &abort_flag);
+            if (it >= 2) ok = ok && warp_wait(w_empty + wt.s, wt.par ^ 1u, err, &abort_flag);
+            Item x{0, 0, 0, -1, 0};
+            if (ok) x = a_info;
+            char* win = dyn + pl.off_kt + wt.s * pl.win_bytes;
+            float* kt = reinterpret_cast<float*>(win);                                // [W][K] k_j e^{D_j}
+            float* dec = reinterpret_cast<float*>(win + (pl.off_dec - pl.off_kt));    // [K] e^G
+            float* wq = reinterpret_cast<float*>(win + (pl.off_wq - pl.off_kt));      // [groups][K] q e^G scale; folding: q, scale
+            float* ps = reinterpret_cast<float*>(win + (pl.off_p - pl.off_kt));       // [64] scores
+            const int n = x.n;
+            const int64_t place = x.sh * c.W + n;  // of the token in the window; k and log a are put there once a head
+            if (x.live) {
+                for (int r = t; r < K; r += kWinThreads) {
+                    const float la = !gate_rows ? gate_log_alpha(ga, x.bh, 0, r, 1, K)
+                                     : ga.kind == kGatePreact ? logsigmoid_f(gb[r]) * ga.inv_tau : gb[r];
+                    const float qr = ldf(qb + r);
+                    float D = la;
 #pragma unroll 4
-                for (int j = hi - 1; j >= lo; --j) {
-                    kt[j * K + r] = ldf(kw + j * K + r) * tc::exp2_ftz(D * tc::kLog2e);
-                    D += gw[j * K + r];
-                }
-                if (part == parts - 1) {
+                    for (int j = n - 1; j >= 0; --j) {
+                        kt[j * K + r] = ldf(kw + j * K + r) * tc::exp2_ftz(D * tc::kLog2e);
+                        D += gw[j * K + r];
+                    }
                     kt[n * K + r] = ldf(kb + r);
                     if (x.grp <= 0) {
                         static_cast<T*>(c.k)[place * K + r] = kb[r];
                         c.la[place * K + r] = la;
                     }
-                }
-                if (part == 0) {
-                    const float d = tc::exp2_ftz(D * tc::kLog2e), qd = ldf(qb + r) * d;
+                    const float d = tc::exp2_ftz(D * tc::kLog2e);
                     dec[r] = d;
-                    if (x.grp < 0)
-                        for (int g = 0; g < NG; ++g) wq[g * K + r] = qd * sc[r * NG + g];
+                    if (x.grp < 0) {
+                        for (int g = 0; g < NG; ++g) wq[g * K + r] = qr * d * sc[r * NG + g];
+                    } else {
+                        wq[r] = qr;
+                        wq[K + r] = sc[r * NG + x.grp];
+                    }
                 }
             }
-            const int v0 = x.grp < 0 ? 0 : x.grp * kG, v1 = x.grp < 0 || v0 + kG > V ? V : v0 + kG;
-            for (int i = v0 + tid; i < v1; i += kStreamThreads) static_cast<T*>(c.v)[place * V + i] = vb[i];
-        }
-        tc::named_sync(1, kStreamThreads);
-        if (x.live && x.grp < 0) {
-            for (int j = warp; j < used; j += kStreamWarps) {
-                float s = 0.f;
-                for (int r = lane; r < K; r += 32) s = fmaf(ldf(qb + r), kt[j * K + r], s);
+            tc::named_sync(2, kWinThreads);
+            if (x.live && x.grp < 0) {
+                for (int j = w; j <= n; j += kWinWarps) {
+                    float s = 0.f;
+#pragma unroll 4
+                    for (int r = lane; r < K; r += 32) s = fmaf(ldf(qb + r), kt[j * K + r], s);
 #pragma unroll
-                for (int d = 16; d > 0; d >>= 1) s += __shfl_xor_sync(0xffffffffu, s, d);
-                if (lane == 0) ps[j] = s;
+                    for (int d = 16; d > 0; d >>= 1) s += __shfl_xor_sync(0xffffffffu, s, d);
+                    if (lane == 0) ps[j] = s;
+                }
             }
+            if (t == 0) w_info[wt.s] = x;
+            warp_arrive(&a_empty);
+            warp_arrive(w_full + wt.s);
+            wt.next(2);
+        }
+        return;
+    }
+    // ---- readers
+    const T* vb = reinterpret_cast<const T*>(dyn + pl.off_v);
+    const T* vw = reinterpret_cast<const T*>(dyn + pl.off_vw);
+    float* red = reinterpret_cast<float*>(dyn + pl.off_red);  // [slices][V], or [warps][128]
+    const int unit = tid / pl.lanes, ugrp = unit % NG, slice = unit / NG;
+    const int ucol = ugrp * kG + (tid % pl.lanes) * 16;
+    const bool reads = slice < pl.slices;
+    Turn wt, rt;
+    uint32_t live_par = 0;
+    for (int it = 0; it < items; ++it) {
+        ok = ok && warp_wait(w_full + wt.s, wt.par, err, &abort_flag);
+        Item x{0, 0, 0, -1, 0};
+        if (ok) x = w_info[wt.s];
+        const char* win = dyn + pl.off_kt + wt.s * pl.win_bytes;
+        const float* kt = reinterpret_cast<const float*>(win);
+        const float* dec = reinterpret_cast<const float*>(win + (pl.off_dec - pl.off_kt));
+        const float* wq = reinterpret_cast<const float*>(win + (pl.off_wq - pl.off_kt));
+        const float* ps = reinterpret_cast<const float*>(win + (pl.off_p - pl.off_kt));
+        const int n = x.n, used = n + 1;
+        if (x.live && x.grp < 0) {
             float2 acc[8];
 #pragma unroll
             for (int e = 0; e < 8; ++e) acc[e] = make_float2(0.f, 0.f);
@@ -750,7 +804,7 @@ __global__ void __launch_bounds__(kStreamThreads + 32, 1)
                 const char* src = dyn + pl.off_ring + rt.s * pl.chunk_bytes + ucol + slice * V;
                 const float* w = wq + ugrp * K + r0 + slice;
                 if (reads && ok) {
-#pragma unroll 2
+#pragma unroll 1
                     for (int r = slice; r < rn; r += pl.slices, src += pl.slices * V, w += pl.slices) {
                         const uint4 z = *reinterpret_cast<const uint4*>(src);
                         const float2 w2 = make_float2(*w, *w);
@@ -763,29 +817,28 @@ __global__ void __launch_bounds__(kStreamThreads + 32, 1)
                         for (int e = 0; e < 8; ++e) acc[e] = fma2(w2, y[e], acc[e]);
                     }
                 }
-                __syncwarp();
-                if (lane == 0) tc::mbar_arrive(ring_empty + rt.s);
+                warp_arrive(ring_empty + rt.s);
                 rt.next(pl.ring);
             }
+            tc::named_sync(1, kReadThreads);  // the head before has been summed
             if (reads) {
                 float4* d = reinterpret_cast<float4*>(red + slice * V + ucol);
 #pragma unroll
                 for (int e = 0; e < 4; ++e) d[e] = make_float4(acc[2 * e].x, acc[2 * e].y, acc[2 * e + 1].x, acc[2 * e + 1].y);
             }
+            ok = ok && warp_wait(&b_full, live_par, err, &abort_flag);
         } else if (x.live) {
             // one group of a head whose window is full
+            ok = ok && warp_wait(&b_full, live_par, err, &abort_flag);
             uint8_t* codes = c.codes + x.sh * K * V;
             float* scale = c.scale + x.sh * K * NG + x.grp;
             const Cols<true> cols(x.grp, V);
             float acc[4] = {0.f, 0.f, 0.f, 0.f};
-            for (int r = warp * kBatch; r < K; r += kStreamWarps * kBatch) {
+            for (int r = warp * kBatch; r < K && ok; r += kReadWarps * kBatch) {
                 uint32_t z[kBatch];
-                float f[kBatch], y[kBatch][4];
+                float y[kBatch][4];
 #pragma unroll
-                for (int i = 0; i < kBatch; ++i) {
-                    z[i] = cols.codes(codes + int64_t(r + i) * V);
-                    f[i] = sc[(r + i) * NG + x.grp];
-                }
+                for (int i = 0; i < kBatch; ++i) z[i] = cols.codes(codes + int64_t(r + i) * V);
                 const auto value = [&](int j, float2* t) {
                     const T* vr = (j < n ? vw + j * V : vb) + cols.col[0];
                     t[0] = t[1] = make_float2(0.f, 0.f);
@@ -800,42 +853,47 @@ __global__ void __launch_bounds__(kStreamThreads + 32, 1)
                         t[1] = make_float2(w.z, w.w);
                     }
                 };
-                form_rows<INT8>(z, f, dec + r, kt + r, K, used, value, y);
+                form_rows<INT8>(z, wq + K + r, dec + r, kt + r, K, used, value, y);
 #pragma unroll
                 for (int i = 0; i < kBatch; ++i) {
-                    const float qr = ldf(qb + r + i);
+                    const float qr = wq[r + i];
 #pragma unroll
                     for (int e = 0; e < 4; ++e) acc[e] = fmaf(qr, y[i][e], acc[e]);
                 }
                 put_rows<INT8, true>(cols, y, kBatch, codes + int64_t(r) * V, V, scale + int64_t(r) * NG, NG);
             }
+            tc::named_sync(1, kReadThreads);
             *reinterpret_cast<float4*>(red + warp * kG + 4 * lane) = make_float4(acc[0], acc[1], acc[2], acc[3]);
-        }
-        tc::named_sync(1, kStreamThreads);
-        if (ok && x.grp < 0) {
-            for (int i = tid; i < V; i += kStreamThreads) {
+        } else tc::named_sync(1, kReadThreads);
+        tc::named_sync(1, kReadThreads);
+        if (ok) {
+            const int64_t place = x.sh * c.W + n;
+            const int v0 = x.grp < 0 ? 0 : x.grp * kG, v1 = x.grp < 0 || v0 + kG > V ? V : v0 + kG;
+            for (int i = v0 + tid; i < v1; i += kReadThreads) {
                 float s = 0.f;
                 if (x.live) {
-#pragma unroll 8
-                    for (int r = 0; r < pl.slices; ++r) s += red[r * V + i];
-                    for (int j = 0; j < n; ++j) s = fmaf(ps[j], ldf(vw + j * V + i), s);
-                    s = fmaf(ps[n], ldf(vb + i), s);
+                    const T vi = vb[i];
+                    static_cast<T*>(c.v)[place * V + i] = vi;
+                    if (x.grp < 0) {
+#pragma unroll 4
+                        for (int r = 0; r < pl.slices; ++r) s += red[r * V + i];
+#pragma unroll 4
+                        for (int j = 0; j < n; ++j) s = fmaf(ps[j], ldf(vw + j * V + i), s);
+                        s = fmaf(ps[n], ldf(&vi), s);
+                    } else {
+#pragma unroll
+                        for (int w = 0; w < kReadWarps; ++w) s += red[w * kG + i - v0];
+                    }
                 }
                 stf(o + x.bh * V + i, s);
             }
-        } else if (ok && tid < kG && x.grp * kG + tid < V) {
-            float s = 0.f;
-            if (x.live) {
-#pragma unroll
-                for (int w = 0; w < kStreamWarps; ++w) s += red[w * kG + tid];
-            }
-            stf(o + x.bh * V + x.grp * kG + tid, s);
         }
-        // red is written again only behind the next head's first barrier, kt and dec were last read in front of this
-        // head's second one
-        __syncwarp();
-        if (lane == 0) tc::mbar_arrive(head_empty + hs);
-        ht.next(pl.heads);
+        if (x.live) {
+            warp_arrive(&b_empty);
+            live_par ^= 1u;
+        }
+        warp_arrive(w_empty + wt.s);
+        wt.next(2);
     }
 }
 
@@ -892,51 +950,48 @@ gla_status step_typed(const CacheProblem& p, const void* q, const void* k, const
     return GLA_OK;
 }
 
-// Shared memory and tiling of the streamed step, or heads = 0 where it does not apply: bulk copies want every stretch
-// (a token's k, v and log a, a window, a row of scales) to be a multiple of 16 bytes, groups want whole rows of lanes,
-// and a window must fit beside a ring of at least three chunks. Other shapes take k_cache_step.
+// Shared memory and tiling of the streamed step, or smem = 0 where it does not apply: bulk copies want every stretch (a
+// token's k, v and log a, a window, a row of scales) to be a multiple of 16 bytes, groups want whole rows of lanes, and a
+// window must fit beside a ring of at least four chunks. It starts later than k_cache_step (the rows' order, the first
+// copies: 6 us against 4 for one head), which therefore keeps the calls that leave SMs without a head.
 StreamPlan stream_plan(const CacheProblem& p) {
     StreamPlan pl{};
     const int K = int(p.K), V = int(p.V), W = p.c.window, e = p.bf16 ? 2 : 4;
+    if (p.B * p.H < kSms || p.H * cdiv(p.V, kG) > (1 << 20)) return pl;
     if (K % 8 != 0 || K > 4096 || !(V % kG == 0 ? V <= 2048 : V < kG && V % 16 == 0)) return pl;
     const int NG = int(cdiv(V, kG));
     pl.lanes = V < kG ? V / 16 : kG / 16;
-    pl.slices = kStreamThreads / pl.lanes / NG;
+    pl.slices = kReadThreads / pl.lanes / NG;
     int at = 0;
     const auto take = [&](int bytes) {
         const int here = at;
         at += round_up(bytes, 128);
         return here;
     };
-    take(K * e);
+    pl.off_q = take(K * e);
     pl.off_k = take(K * e);
-    pl.off_v = take(V * e);
     pl.off_g = take(K * 4);
     pl.off_kw = take((W - 1) * K * e);
     pl.off_gw = take((W - 1) * K * 4);
-    pl.off_vw = take((W - 1) * V * e);
     pl.off_sc = take(K * NG * 4);
-    pl.head_bytes = at;
+    pl.off_v = take(V * e);
+    pl.off_vw = take((W - 1) * V * e);
+    pl.off_kt = take(W * K * 4);
+    pl.off_dec = take(K * 4);
+    pl.off_wq = take(K * (NG > 2 ? NG : 2) * 4);
+    pl.off_p = take(64 * 4);
+    pl.win_bytes = at - pl.off_kt;
+    at += pl.win_bytes;
+    const int sums = pl.slices * V > kReadWarps * kG ? pl.slices * V : kReadWarps * kG;
+    pl.off_red = take(sums * 4);
+    pl.off_ring = at;
     const int pass = pl.slices * V;
     pl.chunk_rows = (pass >= 16384 ? 1 : 16384 / pass) * pl.slices;
     pl.chunk_bytes = round_up(pl.chunk_rows * V, 128);
-    for (int heads = 2; heads >= 1; --heads) {
-        at = heads * pl.head_bytes;
-        pl.off_kt = take(W * K * 4);
-        pl.off_dec = take(K * 4);
-        pl.off_wq = take(K * NG * 4);
-        pl.off_p = take(64 * 4);
-        pl.off_red = take((pl.slices * V > kStreamWarps * kG ? pl.slices * V : kStreamWarps * kG) * 4);
-        pl.off_ring = at;
-        const int64_t room = int64_t(kStreamSmem) - 4096 - at;
-        const int64_t ring = room > 0 ? room / pl.chunk_bytes : 0;
-        if (ring >= 3) {
-            pl.heads = heads;
-            pl.ring = int(ring < kMaxRing ? ring : kMaxRing);
-            pl.smem = size_t(at) + size_t(pl.ring) * pl.chunk_bytes;
-            return pl;
-        }
-    }
+    const int64_t room = int64_t(kStreamSmem) - at, ring = room > 0 ? room / pl.chunk_bytes : 0;
+    if (ring < 4) return pl;
+    pl.ring = int(ring < kMaxRing ? ring : kMaxRing);
+    pl.smem = size_t(at) + size_t(pl.ring) * pl.chunk_bytes;
     return pl;
 }
 
@@ -946,12 +1001,12 @@ gla_status stream_typed(const CacheProblem& p, const StreamPlan& pl, const void*
     const Pool c = pool_of(p);
     const GateArgs ga{la, p.gate, p.inv_tau, p.H};
     if (!allow_smem(k_cache_stream<T, INT8>, pl.smem)) return GLA_ERR_CUDA;
-    for (int64_t b0 = 0; b0 < p.B; b0 += kMaxRows) {
-        const int n = int(p.B - b0 < kMaxRows ? p.B - b0 : kMaxRows);
-        const int64_t most = n * p.H * c.NG;  // a block for every group, were they all to fold
-        GLA_LAUNCH("cache_step", (k_cache_stream<T, INT8>), unsigned(most < 148 ? most : 148), kStreamThreads + 32, pl.smem,
-                   s, c, pl, n, b0, static_cast<const T*>(q), static_cast<const T*>(k), static_cast<const T*>(v), ga, slots,
-                   lengths, static_cast<T*>(o), device_error_word());
+    const int64_t fit = (int64_t(1) << 24) / (p.H * c.NG), step = fit < kMaxRows ? fit : kMaxRows;  // rows a launch
+    for (int64_t b0 = 0; b0 < p.B; b0 += step) {
+        const int n = int(p.B - b0 < step ? p.B - b0 : step);
+        GLA_LAUNCH("cache_step", (k_cache_stream<T, INT8>), unsigned(kSms), kStreamThreads, pl.smem, s, c, pl, n, b0,
+                   static_cast<const T*>(q), static_cast<const T*>(k), static_cast<const T*>(v), ga, slots, lengths,
+                   static_cast<T*>(o), device_error_word());
     }
     return GLA_OK;
 }
@@ -982,7 +1037,7 @@ gla_status cache_load(const CacheProblem& p, const int32_t* slots, const int32_t
 gla_status cache_step(const CacheProblem& p, const void* q, const void* k, const void* v, const float* la,
                       const int32_t* slots, const int32_t* lengths, void* o, cudaStream_t s) {
     const StreamPlan pl = stream_plan(p);
-    if (pl.heads > 0) {
+    if (pl.smem > 0) {
         const bool i8 = p.c.format == GLA_CACHE_INT8;
         if (p.bf16)
             return i8 ? stream_typed<__nv_bfloat16, true>(p, pl, q, k, v, la, slots, lengths, o, s)

@@ -100,6 +100,23 @@ __device__ __forceinline__ bool mbar_wait(uint64_t* bar, uint32_t parity, int* e
     }
 }
 
+// The same wait for short ones on the critical path (a neighbour's message, the next chunk of a stream): it polls, since
+// a suspended thread is woken late.
+__device__ __forceinline__ bool mbar_wait_poll(uint64_t* bar, uint32_t parity, int* err, volatile int* abort,
+                                               long long limit_cycles = 2000000000LL) {
+    if (mbar_try_wait(bar, parity)) return true;
+    const long long t0 = clock64();
+    while (true) {
+        if (mbar_try_wait(bar, parity)) return true;
+        if (*abort) return false;
+        if (clock64() - t0 > limit_cycles) {
+            if (err) atomicOr(err, kErrWaitTimeout);
+            *abort = 1;
+            return false;
+        }
+    }
+}
+
 // Bounded wait that ignores the abort flag: lets copies and MMAs that were
 // already issued land before a block that gave up exits.
 __device__ __forceinline__ void mbar_drain(uint64_t* bar, uint32_t parity, long long limit_cycles = 2000000000LL) {

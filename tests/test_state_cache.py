@@ -265,6 +265,77 @@ def test_step_wide(lib, H, K, V, W):
     check_step(c, [2, 0, 3], [W - 1, 3, 2 * W + 1], "channel", g)
 
 
+def many_rows(B, P, W, g, folds):
+    """Slots and lengths of a serving batch: every place of the window, some padding rows, `folds` of the rows full."""
+    sl = torch.randperm(P, generator=g)[:B].tolist()
+    ln = torch.randint(0, 3 * W, (B,), generator=g).tolist()
+    for i in range(B):
+        if i % 11 == 5:
+            sl[i] = -1 - i
+        if folds == "none" and ln[i] % W == W - 1 and W > 1:
+            ln[i] += 1
+        if folds == "all":
+            ln[i] = ln[i] // W * W + W - 1
+    return sl, ln
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("folds", ["some", "none", "all"])
+@pytest.mark.parametrize("dtype,fmt,W", [(torch.bfloat16, "int8", 16), (torch.float32, "e4m3", 5)])
+@pytest.mark.parametrize("B,H,K,V", [(80, 2, 64, 128), (40, 4, 24, 384), (151, 1, 40, 64), (300, 1, 8, 112),
+                                     (38, 4, 128, 256), (75, 2, 520, 16)])
+def test_step_many_heads(lib, B, H, K, V, dtype, fmt, W, folds):
+    c, _, g = fill_pool(B + 3, H, K, V, W, fmt, dtype, seed=B)
+    check_step(c, *many_rows(B, B + 3, W, g, folds), "channel", g)
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("gate,W", [("scalar", 8), ("head", 1), ("preact", 2)])
+def test_step_many_heads_gate_kinds(lib, gate, W):
+    c, _, g = fill_pool(90, 2, 48, 128, W, "int8", torch.bfloat16)
+    check_step(c, *many_rows(85, 90, W, g, "some"), gate, g)
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("K,V,W", [(256, 512, 16), (256, 512, 32), (128, 1024, 16)])
+def test_step_many_heads_wide(lib, K, V, W):
+    c, _, g = fill_pool(50, 4, K, V, W, "e4m3", torch.bfloat16, seed=1)
+    check_step(c, *many_rows(40, 50, W, g, "some"), "channel", g)
+
+
+@pytest.mark.gpu
+def test_step_more_rows_than_a_launch_takes(lib):
+    """Over 1024 rows: a slot that a row of an earlier launch names is refused like any other."""
+    B, H, K, V = 1100, 1, 8, 16
+    c, _, g = fill_pool(B, H, K, V, 4, "int8", torch.float32)
+    ref, _, _ = fill_pool(B, H, K, V, 4, "int8", torch.float32)
+    sl = torch.randperm(B, generator=g).to(torch.int32)
+    ln = torch.randint(0, 40, (B,), generator=g).to(torch.int32)
+    good = torch.ones(B, dtype=torch.bool)
+    for i, j in ((1090, 3), (1024, 1023), (700, 699)):
+        sl[i] = sl[j]
+        good[i] = False
+    sl[1050], good[1050] = B, False
+    ln[77], good[77] = -1, False
+    t = {n: x.cuda() for n, x in token(c, B, g).items()}
+    o = gc.cache_step(c, t["q"], t["k"], t["v"], t["log_a"], sl.cuda(), ln.cuda())
+    assert gla.gla_check_device_error() == _lib.GLA_ERR_INVALID_ARG
+    idx = good.nonzero()[:, 0]
+    want = []
+    for part in idx.split(100):  # few rows a call: the other kernel
+        p = part.cuda()
+        want.append(gc.cache_step(ref, *[t[n][p].contiguous() for n in ("q", "k", "v", "log_a")], sl[part].cuda(),
+                                  ln[part].cuda()))
+    assert gla.gla_check_device_error() == _lib.GLA_OK
+    assert bool((o[~good.cuda()] == 0).all())
+    # the two kernels sum in different orders: (Dk + 2 W + 16) u of the magnitudes, which here stay below 2^7
+    assert float((o[idx.cuda()] - torch.cat(want)).abs().max()) <= 2 * (K + 8 + 16) * U * 128
+    for n in ("k", "v", "log_a"):
+        assert torch.equal(getattr(c, n), getattr(ref, n)), n
+    assert float((c.scale / ref.scale.clamp(min=1e-30) - 1).abs().max()) <= 64 * U
+    assert int((c.codes.int() - ref.codes.int()).abs().max()) <= 1
+
+
 @pytest.mark.gpu
 def test_step_zero_gates(lib):
     """A zero gate in the window, and one in the call, hide everything before them and nothing after."""
