@@ -166,15 +166,15 @@ __device__ __forceinline__ bool named_before(const int32_t* slots, int64_t b, in
     return __syncthreads_or(dup) != 0;
 }
 
-// Round `rows` <= 8 rows of a group (four columns a lane) into their codes and scales. Lane i works out row i's scale
+// Round `rows` <= ROWS rows of a group (four columns a lane) into their codes and scales. Lane i works out row i's scale
 // and reciprocal for the whole warp.
-template <bool INT8, bool VEC>
+template <bool INT8, int ROWS = kBatch, bool VEC>
 __device__ __forceinline__ void put_rows(const Cols<VEC>& cols, const float (*y)[4], int rows, uint8_t* codes, int64_t V,
                                          float* scale, int64_t NG) {
     const int lane = threadIdx.x & 31;
     uint32_t mine = 0;
 #pragma unroll
-    for (int i = 0; i < kBatch; ++i) {
+    for (int i = 0; i < ROWS; ++i) {
         uint32_t m = 0;
 #pragma unroll
         for (int e = 0; e < 4; ++e) m = max(m, __float_as_uint(y[i][e]) & 0x7fffffffu);
@@ -183,7 +183,7 @@ __device__ __forceinline__ void put_rows(const Cols<VEC>& cols, const float (*y)
     }
     const float sc = scale_of<INT8>(mine), inv = sc > 0.f ? __frcp_rn(sc) : 0.f;
 #pragma unroll
-    for (int i = 0; i < kBatch; ++i) {
+    for (int i = 0; i < ROWS; ++i) {
         const float r = __shfl_sync(0xffffffffu, inv, i);
         if (i < rows) cols.put_codes(codes + i * V, encode4<INT8>(y[i], r));
     }
@@ -211,7 +211,7 @@ __global__ void __launch_bounds__(kThreads) k_cache_store(Pool c, int parts, con
     const int64_t sh = slot * c.H + head;
     const int rows = c.K - r0 < kBatch ? c.K - r0 : kBatch;
     if (rows <= 0) return;
-    put_rows<INT8, VEC>(cols, y, rows, c.codes + (sh * c.K + r0) * c.V, c.V, c.scale + (sh * c.K + r0) * c.NG + grp, c.NG);
+    put_rows<INT8>(cols, y, rows, c.codes + (sh * c.K + r0) * c.V, c.V, c.scale + (sh * c.K + r0) * c.NG + grp, c.NG);
 }
 
 // ---- the window -----------------------------------------------------------------------------
@@ -264,14 +264,14 @@ __device__ __forceinline__ void window_values(const Pool& c, int64_t sh, int64_t
     }
 }
 
-// Eight rows of the state: code x scale x decay + the window's outer products. value(j) gives the lane's four columns of
-// token j's v, kt + j ld its eight keys.
-template <bool INT8, typename F>
+// ROWS rows (4 or 8) of the state: code x scale x decay + the window's outer products. value(j) gives the lane's four columns of
+// token j's v, kt + j ld its keys.
+template <bool INT8, int ROWS = kBatch, typename F>
 __device__ __forceinline__ void form_rows(const uint32_t* codes, const float* scale, const float* decay, const float* kt,
                                           int ld, int used, F value, float (*out)[4]) {
-    float2 y[kBatch][2];
+    float2 y[ROWS][2];
 #pragma unroll
-    for (int i = 0; i < kBatch; ++i) {
+    for (int i = 0; i < ROWS; ++i) {
         decode4<INT8>(codes[i], y[i]);
         const float2 f = make_float2(decay[i], decay[i]), g = make_float2(scale[i], scale[i]);
         y[i][0] = mul2(f, mul2(g, y[i][0]));
@@ -280,17 +280,21 @@ __device__ __forceinline__ void form_rows(const uint32_t* codes, const float* sc
     for (int j = 0; j < used; ++j) {
         float2 v[2];
         value(j, v);
-        const float4 ka = *reinterpret_cast<const float4*>(kt + j * ld), kb = *reinterpret_cast<const float4*>(kt + j * ld + 4);
-        const float k[kBatch] = {ka.x, ka.y, ka.z, ka.w, kb.x, kb.y, kb.z, kb.w};
+        float k[ROWS];
 #pragma unroll
-        for (int i = 0; i < kBatch; ++i) {
+        for (int i = 0; i < ROWS; i += 4) {
+            const float4 x = *reinterpret_cast<const float4*>(kt + j * ld + i);
+            k[i] = x.x, k[i + 1] = x.y, k[i + 2] = x.z, k[i + 3] = x.w;
+        }
+#pragma unroll
+        for (int i = 0; i < ROWS; ++i) {
             const float2 k2 = make_float2(k[i], k[i]);
             y[i][0] = fma2(k2, v[0], y[i][0]);
             y[i][1] = fma2(k2, v[1], y[i][1]);
         }
     }
 #pragma unroll
-    for (int i = 0; i < kBatch; ++i) out[i][0] = y[i][0].x, out[i][1] = y[i][0].y, out[i][2] = y[i][1].x, out[i][3] = y[i][1].y;
+    for (int i = 0; i < ROWS; ++i) out[i][0] = y[i][0].x, out[i][1] = y[i][0].y, out[i][2] = y[i][1].x, out[i][3] = y[i][1].y;
 }
 
 // ---- load -----------------------------------------------------------------------------------
@@ -450,7 +454,7 @@ __global__ void __launch_bounds__(kThreads, 4) k_cache_step(Pool c, const T* __r
             sc[i] = scale[int64_t(ri) * c.NG];
         }
         form_rows<INT8>(z, sc, decay + r, kt + r, ld, used, [&](int j, float2* t) { cols.pairs(vs + j * kG, t); }, y);
-        put_rows<INT8, VEC>(cols, y, c.K - r < kBatch ? c.K - r : kBatch, c.codes + (sh * c.K + r) * c.V, c.V,
+        put_rows<INT8>(cols, y, c.K - r < kBatch ? c.K - r : kBatch, c.codes + (sh * c.K + r) * c.V, c.V,
                             scale + int64_t(r) * c.NG, c.NG);
     }
 }
@@ -460,8 +464,8 @@ __global__ void __launch_bounds__(kThreads, 4) k_cache_step(Pool c, const T* __r
 // persistent block per SM takes its share of the heads; its warps have three parts, a head apart in time:
 //   1 producer   one thread keeps copies in flight across heads: a head's codes are one contiguous stretch, fetched in
 //                chunks through a ring, and its token, window and scales travel ahead of them;
-//   4 windows    form the keys k_j e^{D_j}, the scores p_j and the row weights q e^G scale of the next head;
-//  12 readers    multiply the chunks (16 codes a lane) with the row weights and add the window's part.
+//   8 windows    form the keys k_j e^{D_j}, the scores p_j and the row weights q e^G scale of the next head;
+//  16 readers    multiply the chunks (two rows of 16 codes a lane) with the row weights and add the window's part.
 // So memory does not wait for the window's exponentials, and the ring (about 100 KB in flight an SM) covers the latency
 // of DRAM and the readers' reductions. As one sequence of phases in one block the same work took twice the time.
 //
@@ -469,10 +473,11 @@ __global__ void __launch_bounds__(kThreads, 4) k_cache_step(Pool c, const T* __r
 // so it is split into its groups of 128 columns, which share nothing but the window: each is an item of its own that
 // forms its columns of S_t, reads o from them and rounds them back. The blocks' shares are cut by cost, from the lengths
 // that every block reads.
-constexpr int kReadWarps = 12, kWinWarps = 4;
+constexpr int kReadWarps = 16, kWinWarps = 8;
 constexpr int kReadThreads = kReadWarps * 32, kWinThreads = kWinWarps * 32;
 constexpr int kStreamThreads = kReadThreads + kWinThreads + 32;
 constexpr int kMaxRing = 12;
+constexpr int kFoldRows = 4;                  // state rows a warp forms at a time (registers: 25 warps share the SM's)
 constexpr int kMaxRows = 1024;                // rows of a call in one launch
 constexpr int kDead = 255;
 constexpr int kFoldCost = 6;                  // of a folding group, where an ordinary head costs its number of groups
@@ -512,6 +517,20 @@ __device__ __forceinline__ bool warp_wait(uint64_t* bar, uint32_t parity, int* e
 __device__ __forceinline__ void warp_arrive(uint64_t* bar) {
     __syncwarp();
     if ((threadIdx.x & 31) == 0) tc::mbar_arrive(bar);
+}
+
+// acc += weight x 16 codes
+template <bool INT8>
+__device__ __forceinline__ void add_row(uint4 z, float weight, float2* acc) {
+    const uint32_t x[4] = {z.x, z.y, z.z, z.w};
+    const float2 w = make_float2(weight, weight);
+#pragma unroll
+    for (int e = 0; e < 4; ++e) {
+        float2 y[2];
+        decode4<INT8>(x[e], y);
+        acc[2 * e] = fma2(w, y[0], acc[2 * e]);
+        acc[2 * e + 1] = fma2(w, y[1], acc[2 * e + 1]);
+    }
 }
 
 // A ring position: stage and the parity of its turn.
@@ -562,7 +581,7 @@ __global__ void __launch_bounds__(kStreamThreads, 1)
     // take the rows: those that fold first.
     int folds = 0;
     {
-        static_assert(kMaxRows == 2 * 16 * 32 && kReadWarps + kWinWarps == 16, "two rows a thread");
+        static_assert(kMaxRows == 2 * 16 * 32 && kReadWarps == 16, "two rows a reader");
         int fold[2] = {0, 0}, before[2] = {0, 0};
         if (warp < 16) {
             int count = 0;
@@ -583,7 +602,7 @@ __global__ void __launch_bounds__(kStreamThreads, 1)
                 count += __popc(m);
             }
             if (lane == 0) warp_folds[warp] = count;
-        } else if (lane == 0) {
+        } else if (tid == kReadThreads) {
             abort_flag = 0;
             tc::mbar_init(&a_full, 1), tc::mbar_init(&a_empty, kWinWarps);
             tc::mbar_init(&b_full, 1), tc::mbar_init(&b_empty, kReadWarps);
@@ -604,19 +623,6 @@ __global__ void __launch_bounds__(kStreamThreads, 1)
                 if (b < B) {
                     const int f = first + before[u];  // folding rows in front of b
                     rows[fold[u] ? f : folds + b - f] = uint16_t(b);
-                    // a slot that an earlier row names too
-                    const int32_t slot = row_slot[b];
-                    bool twice = false;
-                    for (int i = 0; i < 64 * warp + 32 * u + 32; i += 4) {
-                        const int4 t = *reinterpret_cast<const int4*>(row_slot + i);
-                        twice |= (t.x == slot && i < b) | (t.y == slot && i + 1 < b) | (t.z == slot && i + 2 < b) |
-                                 (t.w == slot && i + 3 < b);
-                    }
-                    for (int64_t i = 0; i < b0; ++i) twice |= slots[i] == slot;
-                    if (twice && slot >= 0) {
-                        row_n[b] = kDead;
-                        if (blockIdx.x == 0) atomicOr(err, kErrBadRow);
-                    }
                 }
             }
         }
@@ -629,8 +635,10 @@ __global__ void __launch_bounds__(kStreamThreads, 1)
     bool ok = true;
     if (warp == kReadWarps + kWinWarps) {
         // ---- producer
-        if (lane != 0) return;
+        // (all lanes look for rows that name a slot twice, lane 0 does the rest)
         Turn rt;
+        int checked = -1;       // the row looked at last, and whether it stands
+        bool stands = false;
         uint32_t live_par = 0;  // of the values' stage, which only live items use
         int lives = 0;
         int64_t nch = 0;
@@ -649,17 +657,32 @@ __global__ void __launch_bounds__(kStreamThreads, 1)
                 b = rows[folds + h / int(c.H)];
                 head = h % int(c.H);
             }
-            x.live = row_n[b] != kDead;
+            if (b != checked) {
+                checked = b;
+                stands = row_n[b] != kDead;
+                if (stands) {
+                    const int32_t slot = row_slot[b];
+                    bool twice = false;
+#pragma unroll 4
+                    for (int i = lane; i < b; i += 32) twice |= row_slot[i] == slot;
+#pragma unroll 4
+                    for (int64_t i = lane; i < b0; i += 32) twice |= slots[i] == slot;
+                    stands = !__any_sync(0xffffffffu, twice);
+                    if (!stands && lane == 0) atomicOr(err, kErrBadRow);
+                }
+            }
+            x.live = stands;
             x.bh = (b0 + b) * c.H + head;
             x.sh = x.live ? row_slot[b] * c.H + head : 0;
             x.n = x.live ? row_n[b] : 0;
             const uint32_t n = uint32_t(x.n), kb = uint32_t(K) * sizeof(T), vb = uint32_t(V) * sizeof(T), gb = uint32_t(K) * 4u;
+            const auto issue = [&] {
             if (it > 0) ok = tc::mbar_wait_poll(&a_empty, uint32_t(it - 1) & 1u, err, &abort_flag);
-            if (!ok) break;
+            if (!ok) return;
             a_info = x;
             if (!x.live) {
                 tc::mbar_arrive(&a_full);
-                continue;
+                return;
             }
             const uint32_t sb = uint32_t(K) * NG * 4u;
             tc::mbar_arrive_expect_tx(&a_full, 2 * kb + (gate_rows ? gb : 0u) + sb + n * (kb + gb));
@@ -697,8 +720,11 @@ __global__ void __launch_bounds__(kStreamThreads, 1)
             if (!fold) codes(chunks < pl.ring ? chunks : pl.ring);
             if (ok) values();
             if (!fold && ok) codes(chunks);
+            };
+            if (lane == 0) issue();
+            ok = __shfl_sync(0xffffffffu, int(ok), 0) != 0;
         }
-        if (!ok) {
+        if (!ok && lane == 0) {
             // a wait ran out: let the copies that were issued land (each wait with its limit) before the block ends
             constexpr long long limit = 100000000LL;
             for (uint32_t par = 0; par < 2; ++par) {
@@ -718,6 +744,7 @@ __global__ void __launch_bounds__(kStreamThreads, 1)
         const T* kw = reinterpret_cast<const T*>(dyn + pl.off_kw);
         const float* gw = reinterpret_cast<const float*>(dyn + pl.off_gw);
         const float* sc = reinterpret_cast<const float*>(dyn + pl.off_sc);
+        const int parts = K >= kWinThreads ? 1 : kWinThreads / K, part = K >= kWinThreads ? 0 : t / K;
         Turn wt;
         for (int it = 0; it < items; ++it) {
             ok = ok && warp_wait(&a_full, uint32_t(it) & 1u, err, &abort_flag);
@@ -732,28 +759,35 @@ __global__ void __launch_bounds__(kStreamThreads, 1)
             const int n = x.n;
             const int64_t place = x.sh * c.W + n;  // of the token in the window; k and log a are put there once a head
             if (x.live) {
-                for (int r = t; r < K; r += kWinThreads) {
+                // all channels at a time, or as many parts of the window for each as there are threads
+                for (int r = K >= kWinThreads ? t : t - part * K; r < K && part < parts; r += kWinThreads) {
+                    const int lo = n * part / parts, hi = n * (part + 1) / parts;  // this part's tokens
                     const float la = !gate_rows ? gate_log_alpha(ga, x.bh, 0, r, 1, K)
                                      : ga.kind == kGatePreact ? logsigmoid_f(gb[r]) * ga.inv_tau : gb[r];
-                    const float qr = ldf(qb + r);
                     float D = la;
 #pragma unroll 4
-                    for (int j = n - 1; j >= 0; --j) {
+                    for (int j = n - 1; j >= hi; --j) D += gw[j * K + r];
+#pragma unroll 4
+                    for (int j = hi - 1; j >= lo; --j) {
                         kt[j * K + r] = ldf(kw + j * K + r) * tc::exp2_ftz(D * tc::kLog2e);
                         D += gw[j * K + r];
                     }
-                    kt[n * K + r] = ldf(kb + r);
-                    if (x.grp <= 0) {
-                        static_cast<T*>(c.k)[place * K + r] = kb[r];
-                        c.la[place * K + r] = la;
+                    if (part == parts - 1) {
+                        kt[n * K + r] = ldf(kb + r);
+                        if (x.grp <= 0) {
+                            static_cast<T*>(c.k)[place * K + r] = kb[r];
+                            c.la[place * K + r] = la;
+                        }
                     }
-                    const float d = tc::exp2_ftz(D * tc::kLog2e);
-                    dec[r] = d;
-                    if (x.grp < 0) {
-                        for (int g = 0; g < NG; ++g) wq[g * K + r] = qr * d * sc[r * NG + g];
-                    } else {
-                        wq[r] = qr;
-                        wq[K + r] = sc[r * NG + x.grp];
+                    if (part == 0) {
+                        const float qr = ldf(qb + r), d = tc::exp2_ftz(D * tc::kLog2e);
+                        dec[r] = d;
+                        if (x.grp < 0) {
+                            for (int g = 0; g < NG; ++g) wq[g * K + r] = qr * d * sc[r * NG + g];
+                        } else {
+                            wq[r] = qr;
+                            wq[K + r] = sc[r * NG + x.grp];
+                        }
                     }
                 }
             }
@@ -804,27 +838,26 @@ __global__ void __launch_bounds__(kStreamThreads, 1)
                 const char* src = dyn + pl.off_ring + rt.s * pl.chunk_bytes + ucol + slice * V;
                 const float* w = wq + ugrp * K + r0 + slice;
                 if (reads && ok) {
-#pragma unroll 1
-                    for (int r = slice; r < rn; r += pl.slices, src += pl.slices * V, w += pl.slices) {
-                        const uint4 z = *reinterpret_cast<const uint4*>(src);
-                        const float2 w2 = make_float2(*w, *w);
-                        float2 y[8];
-                        decode4<INT8>(z.x, y);
-                        decode4<INT8>(z.y, y + 2);
-                        decode4<INT8>(z.z, y + 4);
-                        decode4<INT8>(z.w, y + 6);
-#pragma unroll
-                        for (int e = 0; e < 8; ++e) acc[e] = fma2(w2, y[e], acc[e]);
-                    }
+                    // a chunk is two passes; the rows behind the state's last one are read as that one with weight 0
+                    const int step = slice + pl.slices < rn ? pl.slices : 0;
+                    const bool one = slice < rn;
+                    const uint4 z0 = *reinterpret_cast<const uint4*>(one ? src : src - slice * V);
+                    const uint4 z1 = *reinterpret_cast<const uint4*>(one ? src + step * V : src - slice * V);
+                    const float u0 = one ? w[0] : 0.f, u1 = step ? w[step] : 0.f;
+                    add_row<INT8>(z0, u0, acc);
+                    add_row<INT8>(z1, u1, acc);
                 }
                 warp_arrive(ring_empty + rt.s);
                 rt.next(pl.ring);
             }
             tc::named_sync(1, kReadThreads);  // the head before has been summed
             if (reads) {
-                float4* d = reinterpret_cast<float4*>(red + slice * V + ucol);
+                // the e-th four columns of all lanes stand together: neighbouring lanes write neighbouring words
+                float* d = red + slice * V + ucol / 4;
 #pragma unroll
-                for (int e = 0; e < 4; ++e) d[e] = make_float4(acc[2 * e].x, acc[2 * e].y, acc[2 * e + 1].x, acc[2 * e + 1].y);
+                for (int e = 0; e < 4; ++e)
+                    *reinterpret_cast<float4*>(d + e * (V / 4)) =
+                        make_float4(acc[2 * e].x, acc[2 * e].y, acc[2 * e + 1].x, acc[2 * e + 1].y);
             }
             ok = ok && warp_wait(&b_full, live_par, err, &abort_flag);
         } else if (x.live) {
@@ -834,11 +867,11 @@ __global__ void __launch_bounds__(kStreamThreads, 1)
             float* scale = c.scale + x.sh * K * NG + x.grp;
             const Cols<true> cols(x.grp, V);
             float acc[4] = {0.f, 0.f, 0.f, 0.f};
-            for (int r = warp * kBatch; r < K && ok; r += kReadWarps * kBatch) {
-                uint32_t z[kBatch];
-                float y[kBatch][4];
+            for (int r = warp * kFoldRows; r < K && ok; r += kReadWarps * kFoldRows) {
+                uint32_t z[kFoldRows];
+                float y[kFoldRows][4];
 #pragma unroll
-                for (int i = 0; i < kBatch; ++i) z[i] = cols.codes(codes + int64_t(r + i) * V);
+                for (int i = 0; i < kFoldRows; ++i) z[i] = cols.codes(codes + int64_t(r + i) * V);
                 const auto value = [&](int j, float2* t) {
                     const T* vr = (j < n ? vw + j * V : vb) + cols.col[0];
                     t[0] = t[1] = make_float2(0.f, 0.f);
@@ -853,14 +886,14 @@ __global__ void __launch_bounds__(kStreamThreads, 1)
                         t[1] = make_float2(w.z, w.w);
                     }
                 };
-                form_rows<INT8>(z, wq + K + r, dec + r, kt + r, K, used, value, y);
+                form_rows<INT8, kFoldRows>(z, wq + K + r, dec + r, kt + r, K, used, value, y);
 #pragma unroll
-                for (int i = 0; i < kBatch; ++i) {
+                for (int i = 0; i < kFoldRows; ++i) {
                     const float qr = wq[r + i];
 #pragma unroll
                     for (int e = 0; e < 4; ++e) acc[e] = fmaf(qr, y[i][e], acc[e]);
                 }
-                put_rows<INT8, true>(cols, y, kBatch, codes + int64_t(r) * V, V, scale + int64_t(r) * NG, NG);
+                put_rows<INT8, kFoldRows>(cols, y, kFoldRows, codes + int64_t(r) * V, V, scale + int64_t(r) * NG, NG);
             }
             tc::named_sync(1, kReadThreads);
             *reinterpret_cast<float4*>(red + warp * kG + 4 * lane) = make_float4(acc[0], acc[1], acc[2], acc[3]);
@@ -868,24 +901,26 @@ __global__ void __launch_bounds__(kStreamThreads, 1)
         tc::named_sync(1, kReadThreads);
         if (ok) {
             const int64_t place = x.sh * c.W + n;
-            const int v0 = x.grp < 0 ? 0 : x.grp * kG, v1 = x.grp < 0 || v0 + kG > V ? V : v0 + kG;
-            for (int i = v0 + tid; i < v1; i += kReadThreads) {
+            const int v0 = x.grp < 0 ? 0 : x.grp * kG, width = x.grp < 0 || v0 + kG > V ? V - v0 : kG;
+            for (int i = tid; i < width; i += kReadThreads) {
+                // column of the i-th sum (see above)
+                const int at = x.grp < 0 ? (i % (V / 4)) / 4 * 16 + i / (V / 4) * 4 + i % 4 : v0 + i;
                 float s = 0.f;
                 if (x.live) {
-                    const T vi = vb[i];
-                    static_cast<T*>(c.v)[place * V + i] = vi;
+                    const T vi = vb[at];
+                    static_cast<T*>(c.v)[place * V + at] = vi;
                     if (x.grp < 0) {
 #pragma unroll 4
                         for (int r = 0; r < pl.slices; ++r) s += red[r * V + i];
 #pragma unroll 4
-                        for (int j = 0; j < n; ++j) s = fmaf(ps[j], ldf(vw + j * V + i), s);
+                        for (int j = 0; j < n; ++j) s = fmaf(ps[j], ldf(vw + j * V + at), s);
                         s = fmaf(ps[n], ldf(&vi), s);
                     } else {
 #pragma unroll
-                        for (int w = 0; w < kReadWarps; ++w) s += red[w * kG + i - v0];
+                        for (int w = 0; w < kReadWarps; ++w) s += red[w * kG + i];
                     }
                 }
-                stf(o + x.bh * V + i, s);
+                stf(o + x.bh * V + at, s);
             }
         }
         if (x.live) {
@@ -985,8 +1020,7 @@ StreamPlan stream_plan(const CacheProblem& p) {
     const int sums = pl.slices * V > kReadWarps * kG ? pl.slices * V : kReadWarps * kG;
     pl.off_red = take(sums * 4);
     pl.off_ring = at;
-    const int pass = pl.slices * V;
-    pl.chunk_rows = (pass >= 16384 ? 1 : 16384 / pass) * pl.slices;
+    pl.chunk_rows = 2 * pl.slices;
     pl.chunk_bytes = round_up(pl.chunk_rows * V, 128);
     const int64_t room = int64_t(kStreamSmem) - at, ring = room > 0 ? room / pl.chunk_bytes : 0;
     if (ring < 4) return pl;
