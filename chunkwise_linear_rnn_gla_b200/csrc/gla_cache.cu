@@ -462,12 +462,13 @@ __global__ void __launch_bounds__(kThreads, 4) k_cache_step(Pool c, const T* __r
 // ---- step, streamed ---------------------------------------------------------------------------
 // For calls with heads enough to give every SM some, of shapes that bulk copies can move (stream_plan below). One
 // persistent block per SM takes its share of the heads; its warps have three parts, a head apart in time:
-//   1 producer   one thread keeps copies in flight across heads: a head's codes are one contiguous stretch, fetched in
-//                chunks through a ring, and its token, window and scales travel ahead of them;
-//   8 windows    form the keys k_j e^{D_j}, the scores p_j and the row weights q e^G scale of the next head;
-//  16 readers    multiply the chunks (two rows of 16 codes a lane) with the row weights and add the window's part.
-// So memory does not wait for the window's exponentials, and the ring (about 100 KB in flight an SM) covers the latency
-// of DRAM and the readers' reductions. As one sequence of phases in one block the same work took twice the time.
+//   3 producers  one thread of the first keeps a head's codes coming, one contiguous stretch fetched in chunks through a
+//                ring; the second's fetches its token, keys, log decays and scales ahead of them, the third's its values;
+//   8 windows    form the keys k_j e^{D_j}, the scores p_j and the row weights q e^G scale of the next head, then write
+//                out the head before: the readers' sums and the window's part;
+//  16 readers    multiply the chunks (16 codes a lane) with the row weights.
+// So memory does not wait for the window's exponentials or the reductions, and the ring (about 100 KB in flight an SM)
+// covers the latency of DRAM. As one sequence of phases in one block the same work took twice the time.
 //
 // A head whose window is full costs several times the others (every entry takes `window` multiply-adds and is rounded),
 // so it is split into its groups of 128 columns, which share nothing but the window: each is an item of its own that
@@ -475,7 +476,8 @@ __global__ void __launch_bounds__(kThreads, 4) k_cache_step(Pool c, const T* __r
 // that every block reads.
 constexpr int kReadWarps = 16, kWinWarps = 8;
 constexpr int kReadThreads = kReadWarps * 32, kWinThreads = kWinWarps * 32;
-constexpr int kStreamThreads = kReadThreads + kWinThreads + 32;
+constexpr int kStreamThreads = kReadThreads + kWinThreads + 96;
+constexpr int kPasses = 2;                    // rows of a chunk that one lane reads
 constexpr int kMaxRing = 12;
 constexpr int kFoldRows = 4;                  // state rows a warp forms at a time (registers: 25 warps share the SM's)
 constexpr int kMaxRows = 1024;                // rows of a call in one launch
@@ -512,6 +514,11 @@ __device__ __forceinline__ void bulk_copy(void* dst, const void* src, uint32_t b
 // A wait of a whole warp, which then agrees on its outcome.
 __device__ __forceinline__ bool warp_wait(uint64_t* bar, uint32_t parity, int* err, int* abort) {
     const bool ok = tc::mbar_wait_poll(bar, parity, err, abort);
+    return __all_sync(0xffffffffu, ok) != 0;
+}
+// for waits that are long by design: the warp leaves the issue slots to the others
+__device__ __forceinline__ bool warp_sleep(uint64_t* bar, uint32_t parity, int* err, int* abort) {
+    const bool ok = tc::mbar_wait(bar, parity, err, abort);
     return __all_sync(0xffffffffu, ok) != 0;
 }
 __device__ __forceinline__ void warp_arrive(uint64_t* bar) {
@@ -568,7 +575,9 @@ __global__ void __launch_bounds__(kStreamThreads, 1)
                    const int32_t* __restrict__ lengths, T* __restrict__ o, int* err) {
     extern __shared__ __align__(128) char dyn[];
     // a: the window warps' inputs; b: the readers' values; w: the window warps' results
-    __shared__ uint64_t a_full, a_empty, b_full, b_empty, w_full[2], w_empty[2], ring_full[kMaxRing], ring_empty[kMaxRing];
+    // red: the readers' sums
+    __shared__ uint64_t a_full, a_empty, b_full, b_empty, w_full[2], w_empty[2], red_full, red_empty;
+    __shared__ uint64_t ring_full[kMaxRing], ring_empty[kMaxRing];
     __shared__ Item a_info, w_info[2];
     __shared__ __align__(16) int32_t row_slot[kMaxRows];
     __shared__ uint16_t rows[kMaxRows];
@@ -605,7 +614,8 @@ __global__ void __launch_bounds__(kStreamThreads, 1)
         } else if (tid == kReadThreads) {
             abort_flag = 0;
             tc::mbar_init(&a_full, 1), tc::mbar_init(&a_empty, kWinWarps);
-            tc::mbar_init(&b_full, 1), tc::mbar_init(&b_empty, kReadWarps);
+            tc::mbar_init(&b_full, 1), tc::mbar_init(&b_empty, kWinWarps);
+            tc::mbar_init(&red_full, kReadWarps), tc::mbar_init(&red_empty, kWinWarps);
             for (int i = 0; i < 2; ++i) tc::mbar_init(w_full + i, kWinWarps), tc::mbar_init(w_empty + i, kReadWarps);
             for (int i = 0; i < pl.ring; ++i) tc::mbar_init(ring_full + i, 1), tc::mbar_init(ring_empty + i, kReadWarps);
             tc::fence_barrier_init();
@@ -633,15 +643,14 @@ __global__ void __launch_bounds__(kStreamThreads, 1)
     const int chunks = (K + pl.chunk_rows - 1) / pl.chunk_rows;
     // A wait that ran out leaves a thread's `ok` false: it then writes nothing, but keeps step with the block's barriers.
     bool ok = true;
-    if (warp == kReadWarps + kWinWarps) {
-        // ---- producer
-        // (all lanes look for rows that name a slot twice, lane 0 does the rest)
+    if (warp >= kReadWarps + kWinWarps) {
+        // ---- producers (all lanes look for rows that name a slot twice, lane 0 does the rest)
+        const int part = warp - (kReadWarps + kWinWarps);  // 0: codes, 1: keys, 2: values
         Turn rt;
         int checked = -1;       // the row looked at last, and whether it stands
         bool stands = false;
-        uint32_t live_par = 0;  // of the values' stage, which only live items use
-        int lives = 0;
-        int64_t nch = 0;
+        int lives = 0;          // items so far that are not padding
+        int64_t nch = 0;        // chunks so far
         for (int it = 0; it < items && ok; ++it) {
             Item x;
             int b, head;
@@ -673,68 +682,68 @@ __global__ void __launch_bounds__(kStreamThreads, 1)
             }
             x.live = stands;
             x.bh = (b0 + b) * c.H + head;
-            x.sh = x.live ? row_slot[b] * c.H + head : 0;
-            x.n = x.live ? row_n[b] : 0;
-            const uint32_t n = uint32_t(x.n), kb = uint32_t(K) * sizeof(T), vb = uint32_t(V) * sizeof(T), gb = uint32_t(K) * 4u;
-            const auto issue = [&] {
-            if (it > 0) ok = tc::mbar_wait_poll(&a_empty, uint32_t(it - 1) & 1u, err, &abort_flag);
-            if (!ok) return;
-            a_info = x;
-            if (!x.live) {
-                tc::mbar_arrive(&a_full);
-                return;
-            }
-            const uint32_t sb = uint32_t(K) * NG * 4u;
-            tc::mbar_arrive_expect_tx(&a_full, 2 * kb + (gate_rows ? gb : 0u) + sb + n * (kb + gb));
-            if (n > 0) {
-                bulk_copy(dyn + pl.off_gw, c.la + x.sh * c.W * K, n * gb, &a_full);
-                bulk_copy(dyn + pl.off_kw, static_cast<T*>(c.k) + x.sh * c.W * K, n * kb, &a_full);
-            }
-            bulk_copy(dyn + pl.off_q, q + x.bh * K, kb, &a_full);
-            bulk_copy(dyn + pl.off_k, k + x.bh * K, kb, &a_full);
-            if (gate_rows) bulk_copy(dyn + pl.off_g, ga.g + x.bh * K, gb, &a_full);
-            bulk_copy(dyn + pl.off_sc, c.scale + x.sh * K * NG, sb, &a_full);
-            const auto values = [&] {  // the values' stage is free once the head before has been written out
-                if (lives > 0) ok = tc::mbar_wait_poll(&b_empty, live_par ^ 1u, err, &abort_flag);
-                if (!ok) return;
-                tc::mbar_arrive_expect_tx(&b_full, (n + 1) * vb);
-                bulk_copy(dyn + pl.off_v, v + x.bh * V, vb, &b_full);
-                if (n > 0) bulk_copy(dyn + pl.off_vw, static_cast<T*>(c.v) + x.sh * c.W * V, n * vb, &b_full);
-                ++lives;
-                live_par ^= 1u;
-            };
-            // the readers free the values' stage behind the chunks of the head before: what of the ring is free goes first
-            int ch = 0;
-            const auto codes = [&](int upto) {
-                for (; ch < upto && ok; ++ch) {
-                    if (nch >= pl.ring) ok = tc::mbar_wait_poll(ring_empty + rt.s, rt.par ^ 1u, err, &abort_flag);
-                    if (!ok) return;
-                    const int r0 = ch * pl.chunk_rows, m = K - r0 < pl.chunk_rows ? K - r0 : pl.chunk_rows;
-                    tc::mbar_arrive_expect_tx(ring_full + rt.s, uint32_t(m) * V);
-                    bulk_copy(dyn + pl.off_ring + rt.s * pl.chunk_bytes, c.codes + (x.sh * K + r0) * V, uint32_t(m) * V,
-                              ring_full + rt.s);
-                    rt.next(pl.ring);
-                    ++nch;
+            x.sh = stands ? row_slot[b] * c.H + head : 0;
+            x.n = stands ? row_n[b] : 0;
+            const uint32_t n = uint32_t(x.n), kb = uint32_t(K) * sizeof(T), vb = uint32_t(V) * sizeof(T);
+            const uint32_t gb = uint32_t(K) * 4u, sb = uint32_t(K) * NG * 4u;
+            if (part == 0) {
+                if (lane == 0 && stands && !fold) {
+                    for (int ch = 0; ch < chunks && ok; ++ch) {
+                        if (nch >= pl.ring) ok = tc::mbar_wait_poll(ring_empty + rt.s, rt.par ^ 1u, err, &abort_flag);
+                        if (!ok) break;
+                        const int r0 = ch * pl.chunk_rows, m = K - r0 < pl.chunk_rows ? K - r0 : pl.chunk_rows;
+                        tc::mbar_arrive_expect_tx(ring_full + rt.s, uint32_t(m) * V);
+                        bulk_copy(dyn + pl.off_ring + rt.s * pl.chunk_bytes, c.codes + (x.sh * K + r0) * V, uint32_t(m) * V,
+                                  ring_full + rt.s);
+                        rt.next(pl.ring);
+                        ++nch;
+                    }
                 }
-            };
-            if (!fold) codes(chunks < pl.ring ? chunks : pl.ring);
-            if (ok) values();
-            if (!fold && ok) codes(chunks);
-            };
-            if (lane == 0) issue();
+            } else if (part == 1) {
+                if (lane == 0) {
+                    if (it > 0) ok = tc::mbar_wait_poll(&a_empty, uint32_t(it - 1) & 1u, err, &abort_flag);
+                    if (ok) {
+                        a_info = x;
+                        if (!stands) tc::mbar_arrive(&a_full);
+                        else {
+                            tc::mbar_arrive_expect_tx(&a_full, 2 * kb + (gate_rows ? gb : 0u) + sb + n * (kb + gb));
+                            if (n > 0) {
+                                bulk_copy(dyn + pl.off_gw, c.la + x.sh * c.W * K, n * gb, &a_full);
+                                bulk_copy(dyn + pl.off_kw, static_cast<T*>(c.k) + x.sh * c.W * K, n * kb, &a_full);
+                            }
+                            bulk_copy(dyn + pl.off_q, q + x.bh * K, kb, &a_full);
+                            bulk_copy(dyn + pl.off_k, k + x.bh * K, kb, &a_full);
+                            if (gate_rows) bulk_copy(dyn + pl.off_g, ga.g + x.bh * K, gb, &a_full);
+                            bulk_copy(dyn + pl.off_sc, c.scale + x.sh * K * NG, sb, &a_full);
+                        }
+                    }
+                }
+            } else if (lane == 0 && stands) {
+                // the values' stage is free once the head before has been written out
+                if (lives > 0) ok = tc::mbar_wait(&b_empty, uint32_t(lives - 1) & 1u, err, &abort_flag);
+                if (ok) {
+                    tc::mbar_arrive_expect_tx(&b_full, (n + 1) * vb);
+                    bulk_copy(dyn + pl.off_v, v + x.bh * V, vb, &b_full);
+                    if (n > 0) bulk_copy(dyn + pl.off_vw, static_cast<T*>(c.v) + x.sh * c.W * V, n * vb, &b_full);
+                }
+                ++lives;
+            }
             ok = __shfl_sync(0xffffffffu, int(ok), 0) != 0;
         }
         if (!ok && lane == 0) {
             // a wait ran out: let the copies that were issued land (each wait with its limit) before the block ends
             constexpr long long limit = 100000000LL;
             for (uint32_t par = 0; par < 2; ++par) {
-                tc::mbar_drain(&a_full, par, limit);
-                tc::mbar_drain(&b_full, par, limit);
-                for (int i = 0; i < pl.ring; ++i) tc::mbar_drain(ring_full + i, par, limit);
+                for (int i = 0; i < pl.ring && part == 0; ++i) tc::mbar_drain(ring_full + i, par, limit);
+                if (part == 1) tc::mbar_drain(&a_full, par, limit);
+                if (part == 2) tc::mbar_drain(&b_full, par, limit);
             }
         }
         return;
     }
+    const T* vb = reinterpret_cast<const T*>(dyn + pl.off_v);
+    const T* vw = reinterpret_cast<const T*>(dyn + pl.off_vw);
+    float* red = reinterpret_cast<float*>(dyn + pl.off_red);  // [slices][V], or [warps][128]
     if (warp >= kReadWarps) {
         // ---- window warps
         const int t = tid - kReadThreads, w = warp - kReadWarps;
@@ -746,9 +755,44 @@ __global__ void __launch_bounds__(kStreamThreads, 1)
         const float* sc = reinterpret_cast<const float*>(dyn + pl.off_sc);
         const int parts = K >= kWinThreads ? 1 : kWinThreads / K, part = K >= kWinThreads ? 0 : t / K;
         Turn wt;
+        Item last{0, 0, 0, -1, 0};
+        bool have = false;
+        int lives = 0;
+        // the head `last`: what the readers summed and, of an ordinary head, the window's part
+        const auto finish = [&](const float* ps, int it) {
+            ok = ok && warp_sleep(&red_full, uint32_t(it) & 1u, err, &abort_flag);
+            if (last.live) ok = ok && warp_sleep(&b_full, uint32_t(lives++) & 1u, err, &abort_flag);
+            if (have && ok) {
+                const int n = last.n;
+                const int64_t place = last.sh * c.W + n;
+                const int v0 = last.grp < 0 ? 0 : last.grp * kG, width = last.grp < 0 || v0 + kG > V ? V - v0 : kG;
+                for (int i = t; i < width; i += kWinThreads) {
+                    // column of the i-th sum (the readers' layout)
+                    const int at = last.grp < 0 ? (i % (V / 4)) / 4 * 16 + i / (V / 4) * 4 + i % 4 : v0 + i;
+                    float s = 0.f;
+                    if (last.live) {
+                        const T vi = vb[at];
+                        static_cast<T*>(c.v)[place * V + at] = vi;
+                        if (last.grp < 0) {
+#pragma unroll 8
+                            for (int r = 0; r < pl.slices; ++r) s += red[r * V + i];
+#pragma unroll 8
+                            for (int j = 0; j < n; ++j) s = fmaf(ps[j], ldf(vw + j * V + at), s);
+                            s = fmaf(ps[n], ldf(&vi), s);
+                        } else {
+#pragma unroll
+                            for (int r = 0; r < kReadWarps; ++r) s += red[r * kG + i];
+                        }
+                    }
+                    stf(o + last.bh * V + at, s);
+                }
+            }
+            warp_arrive(&red_empty);
+            if (last.live) warp_arrive(&b_empty);
+        };
         for (int it = 0; it < items; ++it) {
-            ok = ok && warp_wait(&a_full, uint32_t(it) & 1u, err, &abort_flag);
-            if (it >= 2) ok = ok && warp_wait(w_empty + wt.s, wt.par ^ 1u, err, &abort_flag);
+            ok = ok && warp_sleep(&a_full, uint32_t(it) & 1u, err, &abort_flag);
+            if (it >= 2) ok = ok && warp_sleep(w_empty + wt.s, wt.par ^ 1u, err, &abort_flag);
             Item x{0, 0, 0, -1, 0};
             if (ok) x = a_info;
             char* win = dyn + pl.off_kt + wt.s * pl.win_bytes;
@@ -803,21 +847,27 @@ __global__ void __launch_bounds__(kStreamThreads, 1)
                 }
             }
             if (t == 0) w_info[wt.s] = x;
-            warp_arrive(&a_empty);
             warp_arrive(w_full + wt.s);
+            warp_arrive(&a_empty);
+            if (it > 0) finish(reinterpret_cast<const float*>(dyn + pl.off_p + (wt.s ^ 1) * pl.win_bytes), it - 1);
+            last = x;
+            have = ok;
             wt.next(2);
         }
+        tc::named_sync(2, kWinThreads);
+        if (items > 0) finish(reinterpret_cast<const float*>(dyn + pl.off_p + (wt.s ^ 1) * pl.win_bytes), items - 1);
         return;
     }
     // ---- readers
-    const T* vb = reinterpret_cast<const T*>(dyn + pl.off_v);
-    const T* vw = reinterpret_cast<const T*>(dyn + pl.off_vw);
-    float* red = reinterpret_cast<float*>(dyn + pl.off_red);  // [slices][V], or [warps][128]
     const int unit = tid / pl.lanes, ugrp = unit % NG, slice = unit / NG;
     const int ucol = ugrp * kG + (tid % pl.lanes) * 16;
     const bool reads = slice < pl.slices;
     Turn wt, rt;
-    uint32_t live_par = 0;
+    int lives = 0;
+    // the sums of the head before have been taken (waited for by padding rows too: no part gets two heads ahead)
+    const auto last_written = [&](int it) {
+        if (it > 0) ok = ok && warp_wait(&red_empty, uint32_t(it - 1) & 1u, err, &abort_flag);
+    };
     for (int it = 0; it < items; ++it) {
         ok = ok && warp_wait(w_full + wt.s, wt.par, err, &abort_flag);
         Item x{0, 0, 0, -1, 0};
@@ -826,32 +876,33 @@ __global__ void __launch_bounds__(kStreamThreads, 1)
         const float* kt = reinterpret_cast<const float*>(win);
         const float* dec = reinterpret_cast<const float*>(win + (pl.off_dec - pl.off_kt));
         const float* wq = reinterpret_cast<const float*>(win + (pl.off_wq - pl.off_kt));
-        const float* ps = reinterpret_cast<const float*>(win + (pl.off_p - pl.off_kt));
-        const int n = x.n, used = n + 1;
         if (x.live && x.grp < 0) {
             float2 acc[8];
 #pragma unroll
             for (int e = 0; e < 8; ++e) acc[e] = make_float2(0.f, 0.f);
-            for (int ch = 0; ch < chunks; ++ch) {
+            const float* w = wq + ugrp * K + slice;
+            for (int ch = 0; ch < chunks; ++ch, w += pl.chunk_rows) {
                 ok = ok && warp_wait(ring_full + rt.s, rt.par, err, &abort_flag);
-                const int r0 = ch * pl.chunk_rows, rn = K - r0 < pl.chunk_rows ? K - r0 : pl.chunk_rows;
-                const char* src = dyn + pl.off_ring + rt.s * pl.chunk_bytes + ucol + slice * V;
-                const float* w = wq + ugrp * K + r0 + slice;
+                const int rn = K - ch * pl.chunk_rows;  // rows from the chunk's first
+                const char* src = dyn + pl.off_ring + rt.s * pl.chunk_bytes + ucol;
                 if (reads && ok) {
-                    // a chunk is two passes; the rows behind the state's last one are read as that one with weight 0
-                    const int step = slice + pl.slices < rn ? pl.slices : 0;
-                    const bool one = slice < rn;
-                    const uint4 z0 = *reinterpret_cast<const uint4*>(one ? src : src - slice * V);
-                    const uint4 z1 = *reinterpret_cast<const uint4*>(one ? src + step * V : src - slice * V);
-                    const float u0 = one ? w[0] : 0.f, u1 = step ? w[step] : 0.f;
-                    add_row<INT8>(z0, u0, acc);
-                    add_row<INT8>(z1, u1, acc);
+                    // rows behind the state's last one are read as the chunk's first with weight 0
+                    uint4 z[kPasses];
+                    float u[kPasses];
+#pragma unroll
+                    for (int i = 0; i < kPasses; ++i) {
+                        const int r = slice + i * pl.slices;
+                        z[i] = *reinterpret_cast<const uint4*>(src + (r < rn ? r * V : 0));
+                        u[i] = r < rn ? w[i * pl.slices] : 0.f;
+                    }
+#pragma unroll
+                    for (int i = 0; i < kPasses; ++i) add_row<INT8>(z[i], u[i], acc);
                 }
                 warp_arrive(ring_empty + rt.s);
                 rt.next(pl.ring);
             }
-            tc::named_sync(1, kReadThreads);  // the head before has been summed
-            if (reads) {
+            last_written(it);
+            if (reads && ok) {
                 // the e-th four columns of all lanes stand together: neighbouring lanes write neighbouring words
                 float* d = red + slice * V + ucol / 4;
 #pragma unroll
@@ -859,10 +910,10 @@ __global__ void __launch_bounds__(kStreamThreads, 1)
                     *reinterpret_cast<float4*>(d + e * (V / 4)) =
                         make_float4(acc[2 * e].x, acc[2 * e].y, acc[2 * e + 1].x, acc[2 * e + 1].y);
             }
-            ok = ok && warp_wait(&b_full, live_par, err, &abort_flag);
         } else if (x.live) {
             // one group of a head whose window is full
-            ok = ok && warp_wait(&b_full, live_par, err, &abort_flag);
+            ok = ok && warp_wait(&b_full, uint32_t(lives) & 1u, err, &abort_flag);
+            const int n = x.n, used = n + 1;
             uint8_t* codes = c.codes + x.sh * K * V;
             float* scale = c.scale + x.sh * K * NG + x.grp;
             const Cols<true> cols(x.grp, V);
@@ -895,38 +946,11 @@ __global__ void __launch_bounds__(kStreamThreads, 1)
                 }
                 put_rows<INT8, kFoldRows>(cols, y, kFoldRows, codes + int64_t(r) * V, V, scale + int64_t(r) * NG, NG);
             }
-            tc::named_sync(1, kReadThreads);
-            *reinterpret_cast<float4*>(red + warp * kG + 4 * lane) = make_float4(acc[0], acc[1], acc[2], acc[3]);
-        } else tc::named_sync(1, kReadThreads);
-        tc::named_sync(1, kReadThreads);
-        if (ok) {
-            const int64_t place = x.sh * c.W + n;
-            const int v0 = x.grp < 0 ? 0 : x.grp * kG, width = x.grp < 0 || v0 + kG > V ? V - v0 : kG;
-            for (int i = tid; i < width; i += kReadThreads) {
-                // column of the i-th sum (see above)
-                const int at = x.grp < 0 ? (i % (V / 4)) / 4 * 16 + i / (V / 4) * 4 + i % 4 : v0 + i;
-                float s = 0.f;
-                if (x.live) {
-                    const T vi = vb[at];
-                    static_cast<T*>(c.v)[place * V + at] = vi;
-                    if (x.grp < 0) {
-#pragma unroll 4
-                        for (int r = 0; r < pl.slices; ++r) s += red[r * V + i];
-#pragma unroll 4
-                        for (int j = 0; j < n; ++j) s = fmaf(ps[j], ldf(vw + j * V + at), s);
-                        s = fmaf(ps[n], ldf(&vi), s);
-                    } else {
-#pragma unroll
-                        for (int w = 0; w < kReadWarps; ++w) s += red[w * kG + i];
-                    }
-                }
-                stf(o + x.bh * V + at, s);
-            }
-        }
-        if (x.live) {
-            warp_arrive(&b_empty);
-            live_par ^= 1u;
-        }
+            last_written(it);
+            if (ok) *reinterpret_cast<float4*>(red + warp * kG + 4 * lane) = make_float4(acc[0], acc[1], acc[2], acc[3]);
+        } else last_written(it);
+        lives += x.live;
+        warp_arrive(&red_full);
         warp_arrive(w_empty + wt.s);
         wt.next(2);
     }
@@ -1020,7 +1044,7 @@ StreamPlan stream_plan(const CacheProblem& p) {
     const int sums = pl.slices * V > kReadWarps * kG ? pl.slices * V : kReadWarps * kG;
     pl.off_red = take(sums * 4);
     pl.off_ring = at;
-    pl.chunk_rows = 2 * pl.slices;
+    pl.chunk_rows = kPasses * pl.slices;
     pl.chunk_bytes = round_up(pl.chunk_rows * V, 128);
     const int64_t room = int64_t(kStreamSmem) - at, ring = room > 0 ? room / pl.chunk_bytes : 0;
     if (ring < 4) return pl;
