@@ -511,6 +511,28 @@ __device__ __forceinline__ void bulk_copy(void* dst, const void* src, uint32_t b
                  : "memory");
 }
 
+// Two or four adjacent elements as fp32, and four back.
+__device__ __forceinline__ float2 ld2(const float* p) { return *reinterpret_cast<const float2*>(p); }
+__device__ __forceinline__ float2 ld2(const __nv_bfloat16* p) {
+    return __bfloat1622float2(*reinterpret_cast<const __nv_bfloat162*>(p));
+}
+__device__ __forceinline__ void ld4(const float* p, float2* y) {
+    const float4 x = *reinterpret_cast<const float4*>(p);
+    y[0] = make_float2(x.x, x.y);
+    y[1] = make_float2(x.z, x.w);
+}
+__device__ __forceinline__ void ld4(const __nv_bfloat16* p, float2* y) {
+    const uint2 x = *reinterpret_cast<const uint2*>(p);
+    y[0] = __bfloat1622float2(*reinterpret_cast<const __nv_bfloat162*>(&x.x));
+    y[1] = __bfloat1622float2(*reinterpret_cast<const __nv_bfloat162*>(&x.y));
+}
+__device__ __forceinline__ void st4(float* p, const float2* y) {
+    *reinterpret_cast<float4*>(p) = make_float4(y[0].x, y[0].y, y[1].x, y[1].y);
+}
+__device__ __forceinline__ void st4(__nv_bfloat16* p, const float2* y) {
+    *reinterpret_cast<uint2*>(p) = make_uint2(tc::pack_bf16x2(y[0].x, y[0].y), tc::pack_bf16x2(y[1].x, y[1].y));
+}
+
 // A wait of a whole warp, which then agrees on its outcome.
 __device__ __forceinline__ bool warp_wait(uint64_t* bar, uint32_t parity, int* err, int* abort) {
     const bool ok = tc::mbar_wait_poll(bar, parity, err, abort);
@@ -753,7 +775,7 @@ __global__ void __launch_bounds__(kStreamThreads, 1)
         const T* kw = reinterpret_cast<const T*>(dyn + pl.off_kw);
         const float* gw = reinterpret_cast<const float*>(dyn + pl.off_gw);
         const float* sc = reinterpret_cast<const float*>(dyn + pl.off_sc);
-        const int parts = K >= kWinThreads ? 1 : kWinThreads / K, part = K >= kWinThreads ? 0 : t / K;
+        const int parts = K / 2 >= kWinThreads ? 1 : kWinThreads / (K / 2), part = parts == 1 ? 0 : t / (K / 2);
         Turn wt;
         Item last{0, 0, 0, -1, 0};
         bool have = false;
@@ -763,28 +785,48 @@ __global__ void __launch_bounds__(kStreamThreads, 1)
             ok = ok && warp_sleep(&red_full, uint32_t(it) & 1u, err, &abort_flag);
             if (last.live) ok = ok && warp_sleep(&b_full, uint32_t(lives++) & 1u, err, &abort_flag);
             if (have && ok) {
-                const int n = last.n;
-                const int64_t place = last.sh * c.W + n;
-                const int v0 = last.grp < 0 ? 0 : last.grp * kG, width = last.grp < 0 || v0 + kG > V ? V - v0 : kG;
-                for (int i = t; i < width; i += kWinThreads) {
-                    // column of the i-th sum (the readers' layout)
-                    const int at = last.grp < 0 ? (i % (V / 4)) / 4 * 16 + i / (V / 4) * 4 + i % 4 : v0 + i;
-                    float s = 0.f;
-                    if (last.live) {
-                        const T vi = vb[at];
-                        static_cast<T*>(c.v)[place * V + at] = vi;
-                        if (last.grp < 0) {
-#pragma unroll 8
-                            for (int r = 0; r < pl.slices; ++r) s += red[r * V + i];
-#pragma unroll 8
-                            for (int j = 0; j < n; ++j) s = fmaf(ps[j], ldf(vw + j * V + at), s);
-                            s = fmaf(ps[n], ldf(&vi), s);
-                        } else {
-#pragma unroll
-                            for (int r = 0; r < kReadWarps; ++r) s += red[r * kG + i];
+                const int n = last.n, half = t & 1;
+                const bool whole = last.grp < 0;
+                T* put = static_cast<T*>(c.v) + (last.sh * c.W + n) * V;
+                const int v0 = whole ? 0 : last.grp * kG, quads = (whole || v0 + kG > V ? V - v0 : kG) / 4;
+                const int rows = whole ? pl.slices : kReadWarps, ld = whole ? V : kG;
+                // four columns of two lanes, which take every other row of the sums and every other token
+                for (int i0 = 0; i0 < quads; i0 += kWinThreads / 2) {
+                    const int i = i0 + (t >> 1);
+                    const bool mine = i < quads;
+                    // first column of the i-th four (the readers' layout)
+                    const int at = whole ? i % (V / 16) * 16 + i / (V / 16) * 4 : v0 + 4 * i;
+                    float2 s[2] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f)};
+                    if (last.live && mine) {
+#pragma unroll 4
+                        for (int r = half; r < rows; r += 2) {
+                            float2 y[2];
+                            ld4(red + r * ld + 4 * i, y);
+                            s[0] = add2(s[0], y[0]);
+                            s[1] = add2(s[1], y[1]);
+                        }
+                        if (whole) {
+#pragma unroll 4
+                            for (int j = half; j <= n; j += 2) {
+                                float2 y[2];
+                                ld4(j < n ? vw + j * V + at : vb + at, y);
+                                const float2 pj = make_float2(ps[j], ps[j]);
+                                s[0] = fma2(pj, y[0], s[0]);
+                                s[1] = fma2(pj, y[1], s[1]);
+                            }
                         }
                     }
-                    stf(o + last.bh * V + at, s);
+#pragma unroll
+                    for (int e = 0; e < 2; ++e) {
+                        s[e].x += __shfl_xor_sync(0xffffffffu, s[e].x, 1);
+                        s[e].y += __shfl_xor_sync(0xffffffffu, s[e].y, 1);
+                    }
+                    if (mine && half == 0) st4(o + last.bh * V + at, s);
+                    if (mine && half == 1 && last.live) {  // the token's value goes into the window
+                        float2 y[2];
+                        ld4(vb + at, y);
+                        st4(put + at, y);
+                    }
                 }
             }
             warp_arrive(&red_empty);
@@ -803,34 +845,48 @@ __global__ void __launch_bounds__(kStreamThreads, 1)
             const int n = x.n;
             const int64_t place = x.sh * c.W + n;  // of the token in the window; k and log a are put there once a head
             if (x.live) {
-                // all channels at a time, or as many parts of the window for each as there are threads
-                for (int r = K >= kWinThreads ? t : t - part * K; r < K && part < parts; r += kWinThreads) {
+                // two channels a thread: all of them at a time, or as many parts of the window as there are threads
+                for (int r = 2 * (parts == 1 ? t : t - part * (K / 2)); r < K && part < parts; r += 2 * kWinThreads) {
                     const int lo = n * part / parts, hi = n * (part + 1) / parts;  // this part's tokens
-                    const float la = !gate_rows ? gate_log_alpha(ga, x.bh, 0, r, 1, K)
-                                     : ga.kind == kGatePreact ? logsigmoid_f(gb[r]) * ga.inv_tau : gb[r];
-                    float D = la;
+                    float2 la;
+                    if (!gate_rows) la.x = la.y = gate_log_alpha(ga, x.bh, 0, r, 1, K);
+                    else {
+                        la = ld2(gb + r);
+                        if (ga.kind == kGatePreact)
+                            la = make_float2(logsigmoid_f(la.x) * ga.inv_tau, logsigmoid_f(la.y) * ga.inv_tau);
+                    }
+                    const auto decay = [](float2 D) {
+                        const float2 e = mul2(D, make_float2(tc::kLog2e, tc::kLog2e));
+                        return make_float2(tc::exp2_ftz(e.x), tc::exp2_ftz(e.y));
+                    };
+                    float2 D = la;
 #pragma unroll 4
-                    for (int j = n - 1; j >= hi; --j) D += gw[j * K + r];
+                    for (int j = n - 1; j >= hi; --j) D = add2(D, ld2(gw + j * K + r));
 #pragma unroll 4
                     for (int j = hi - 1; j >= lo; --j) {
-                        kt[j * K + r] = ldf(kw + j * K + r) * tc::exp2_ftz(D * tc::kLog2e);
-                        D += gw[j * K + r];
+                        *reinterpret_cast<float2*>(kt + j * K + r) = mul2(ld2(kw + j * K + r), decay(D));
+                        D = add2(D, ld2(gw + j * K + r));
                     }
                     if (part == parts - 1) {
-                        kt[n * K + r] = ldf(kb + r);
+                        *reinterpret_cast<float2*>(kt + n * K + r) = ld2(kb + r);
                         if (x.grp <= 0) {
-                            static_cast<T*>(c.k)[place * K + r] = kb[r];
-                            c.la[place * K + r] = la;
+                            T* put = static_cast<T*>(c.k) + place * K + r;
+                            put[0] = kb[r];
+                            put[1] = kb[r + 1];
+                            *reinterpret_cast<float2*>(c.la + place * K + r) = la;
                         }
                     }
                     if (part == 0) {
-                        const float qr = ldf(qb + r), d = tc::exp2_ftz(D * tc::kLog2e);
-                        dec[r] = d;
+                        const float2 qr = ld2(qb + r), d = decay(D), qd = mul2(qr, d);
+                        *reinterpret_cast<float2*>(dec + r) = d;
                         if (x.grp < 0) {
-                            for (int g = 0; g < NG; ++g) wq[g * K + r] = qr * d * sc[r * NG + g];
+                            for (int g = 0; g < NG; ++g)
+                                *reinterpret_cast<float2*>(wq + g * K + r) =
+                                    mul2(qd, make_float2(sc[r * NG + g], sc[(r + 1) * NG + g]));
                         } else {
-                            wq[r] = qr;
-                            wq[K + r] = sc[r * NG + x.grp];
+                            *reinterpret_cast<float2*>(wq + r) = qr;
+                            *reinterpret_cast<float2*>(wq + K + r) =
+                                make_float2(sc[r * NG + x.grp], sc[(r + 1) * NG + x.grp]);
                         }
                     }
                 }
@@ -839,8 +895,10 @@ __global__ void __launch_bounds__(kStreamThreads, 1)
             if (x.live && x.grp < 0) {
                 for (int j = w; j <= n; j += kWinWarps) {
                     float s = 0.f;
+                    float2 s2 = make_float2(0.f, 0.f);
 #pragma unroll 4
-                    for (int r = lane; r < K; r += 32) s = fmaf(ldf(qb + r), kt[j * K + r], s);
+                    for (int r = 2 * lane; r < K; r += 64) s2 = fma2(ld2(qb + r), ld2(kt + j * K + r), s2);
+                    s = s2.x + s2.y;
 #pragma unroll
                     for (int d = 16; d > 0; d >>= 1) s += __shfl_xor_sync(0xffffffffu, s, d);
                     if (lane == 0) ps[j] = s;
