@@ -159,6 +159,28 @@ struct Cols {
     }
 };
 
+// Two or four adjacent elements as fp32, and four back.
+__device__ __forceinline__ float2 ld2(const float* p) { return *reinterpret_cast<const float2*>(p); }
+__device__ __forceinline__ float2 ld2(const __nv_bfloat16* p) {
+    return __bfloat1622float2(*reinterpret_cast<const __nv_bfloat162*>(p));
+}
+__device__ __forceinline__ void ld4(const float* p, float2* y) {
+    const float4 x = *reinterpret_cast<const float4*>(p);
+    y[0] = make_float2(x.x, x.y);
+    y[1] = make_float2(x.z, x.w);
+}
+__device__ __forceinline__ void ld4(const __nv_bfloat16* p, float2* y) {
+    const uint2 x = *reinterpret_cast<const uint2*>(p);
+    y[0] = __bfloat1622float2(*reinterpret_cast<const __nv_bfloat162*>(&x.x));
+    y[1] = __bfloat1622float2(*reinterpret_cast<const __nv_bfloat162*>(&x.y));
+}
+__device__ __forceinline__ void st4(float* p, const float2* y) {
+    *reinterpret_cast<float4*>(p) = make_float4(y[0].x, y[0].y, y[1].x, y[1].y);
+}
+__device__ __forceinline__ void st4(__nv_bfloat16* p, const float2* y) {
+    *reinterpret_cast<uint2*>(p) = make_uint2(tc::pack_bf16x2(y[0].x, y[0].y), tc::pack_bf16x2(y[1].x, y[1].y));
+}
+
 // Whether an earlier row of the call names the same slot (every thread of the block gets the answer).
 __device__ __forceinline__ bool named_before(const int32_t* slots, int64_t b, int32_t slot) {
     int dup = 0;
@@ -246,21 +268,25 @@ __device__ __forceinline__ void window_keys(const Pool& c, int64_t sh, int64_t b
 }
 
 // vs[j][0..127]: the group's columns of the window's values, fp32
-template <typename T, bool STEP>
+template <typename T, bool STEP, bool VEC>
 __device__ __forceinline__ void window_values(const Pool& c, int64_t sh, int64_t bh, int n, int grp,
                                               const T* __restrict__ vc, float* vs) {
     T* wv = static_cast<T*>(c.v) + sh * c.W * c.V;
-    for (int i = threadIdx.x; i < (n + (STEP ? 1 : 0)) * kG; i += kThreads) {
-        const int j = i / kG, col = grp * kG + i % kG;
-        float x = 0.f;
-        if (col < c.V) {
-            if (STEP && j == n) {
-                const T v = vc[bh * c.V + col];
-                wv[n * c.V + col] = v;
-                x = ldf(&v);
-            } else x = ldf(wv + j * c.V + col);
+    constexpr int E = VEC ? 4 : 1;  // columns a thread takes (a width that is a multiple of 4: they are aligned)
+    for (int i = threadIdx.x; i < (n + (STEP ? 1 : 0)) * (kG / E); i += kThreads) {
+        const int j = i / (kG / E), at = i % (kG / E) * E, col = grp * kG + at;
+        const bool in = col < c.V;
+        if constexpr (VEC) {
+            float2 x[2] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f)};
+            if (in) ld4(STEP && j == n ? vc + bh * c.V + col : wv + j * c.V + col, x);
+            if (STEP && j == n && in) st4(wv + n * c.V + col, x);
+            st4(vs + j * kG + at, x);
+        } else {
+            float x = 0.f;
+            if (in) x = ldf(STEP && j == n ? vc + bh * c.V + col : wv + j * c.V + col);
+            if (STEP && j == n && in) stf(wv + n * c.V + col, x);
+            vs[j * kG + at] = x;
         }
-        vs[i] = x;
     }
 }
 
@@ -298,17 +324,21 @@ __device__ __forceinline__ void form_rows(const uint32_t* codes, const float* sc
 }
 
 // ---- load -----------------------------------------------------------------------------------
-// One block per (row of the call, head, group, 64 state rows).
+// One block per (row of the call, head, group, kLoadRows state rows); 5 bytes an entry, 4 of them written. The window is
+// read once a block, and a warp's codes are on their way before the window is worked out.
+constexpr int kLoadRows = 128;
+
 template <typename T, bool INT8, bool VEC>
-__global__ void __launch_bounds__(kThreads) k_cache_load(Pool c, int parts, const int32_t* __restrict__ slots,
-                                                         const int32_t* __restrict__ lengths, float* __restrict__ S,
-                                                         int* err) {
-    constexpr int ROWS = kWarps * kBatch;
+__global__ void __launch_bounds__(kThreads, 4) k_cache_load(Pool c, int parts, const int32_t* __restrict__ slots,
+                                                            const int32_t* __restrict__ lengths, float* __restrict__ S,
+                                                            int* err) {
+    constexpr int BATCHES = kLoadRows / (kWarps * kBatch);
     extern __shared__ __align__(16) float sm[];
     const int64_t bhg = blockIdx.x / parts, bh = bhg / c.NG, b = bh / c.H, head = bh % c.H;
     const int part = int(blockIdx.x % parts), grp = int(bhg % c.NG);
     const Cols<VEC> cols(grp, c.V);
-    const int w0 = int(threadIdx.x >> 5) * kBatch, r0 = part * ROWS + w0;
+    const int first = part * kLoadRows, last = first + kLoadRows < c.K ? first + kLoadRows : c.K;
+    const int w0 = int(threadIdx.x >> 5) * kBatch;  // this warp's first row of each batch of 64
     const int32_t slot = slots[b];
     const int32_t len = lengths ? lengths[b] : 0;
     bool live = slot >= 0;
@@ -316,35 +346,41 @@ __global__ void __launch_bounds__(kThreads) k_cache_load(Pool c, int parts, cons
         live = false;
         if (threadIdx.x == 0) atomicOr(err, kErrBadRow);
     }
-    float y[kBatch][4];
-    if (live) {
-        const int64_t sh = slot * c.H + head;
-        const int n = len % c.W;
-        uint32_t x[kBatch];
-        float sc[kBatch];
+    if (!live) {
+        const float zero[4] = {0.f, 0.f, 0.f, 0.f};
+        for (int r = first + int(threadIdx.x >> 5); r < last; r += kWarps) cols.store(S + (bh * c.K + r) * c.V, zero);
+        return;
+    }
+    const int64_t sh = slot * c.H + head;
+    const int n = len % c.W;
+    uint32_t x[BATCHES][kBatch];
+#pragma unroll
+    for (int u = 0; u < BATCHES; ++u)
 #pragma unroll
         for (int i = 0; i < kBatch; ++i) {
-            const int r = r0 + i < c.K ? r0 + i : c.K - 1;
-            x[i] = cols.codes(c.codes + (sh * c.K + r) * c.V);
-            sc[i] = c.scale[(sh * c.K + r) * c.NG + grp];
+            const int r = first + u * kWarps * kBatch + w0 + i;
+            x[u][i] = cols.codes(c.codes + (sh * c.K + (r < c.K ? r : c.K - 1)) * c.V);
         }
-        float* kt = sm;                   // [W][ROWS]
-        float* decay = kt + c.W * ROWS;   // [ROWS]
-        float* vs = decay + ROWS;         // [W][128]
-        const int first = part * ROWS, last = first + ROWS < c.K ? first + ROWS : c.K;
-        window_keys<T, false>(c, sh, bh, n, first, last, ROWS, nullptr, GateArgs{}, false, kt, decay);
-        window_values<T, false>(c, sh, bh, n, grp, nullptr, vs);
-        __syncthreads();
-        form_rows<INT8>(x, sc, decay + w0, kt + w0, ROWS, n, [&](int j, float2* t) { cols.pairs(vs + j * kG, t); }, y);
-    } else {
+    float* kt = sm;                        // [W][kLoadRows]
+    float* decay = kt + c.W * kLoadRows;   // [kLoadRows]
+    float* scale = decay + kLoadRows;      // [kLoadRows]
+    float* vs = scale + kLoadRows;         // [W][128]
+    for (int r = threadIdx.x; r < kLoadRows; r += kThreads)
+        scale[r] = first + r < last ? c.scale[(sh * c.K + first + r) * c.NG + grp] : 0.f;
+    window_keys<T, false>(c, sh, bh, n, first, last, kLoadRows, nullptr, GateArgs{}, false, kt, decay);
+    window_values<T, false, VEC>(c, sh, bh, n, grp, nullptr, vs);
+    __syncthreads();
+#pragma unroll
+    for (int u = 0; u < BATCHES; ++u) {
+        const int r = u * kWarps * kBatch + w0;
+        if (first + r >= last) break;
+        float y[kBatch][4];
+        form_rows<INT8>(x[u], scale + r, decay + r, kt + r, kLoadRows, n,
+                        [&](int j, float2* t) { cols.pairs(vs + j * kG, t); }, y);
 #pragma unroll
         for (int i = 0; i < kBatch; ++i)
-#pragma unroll
-            for (int e = 0; e < 4; ++e) y[i][e] = 0.f;
+            if (first + r + i < last) cols.store(S + (bh * c.K + first + r + i) * c.V, y[i]);
     }
-#pragma unroll
-    for (int i = 0; i < kBatch; ++i)
-        if (r0 + i < c.K) cols.store(S + (bh * c.K + r0 + i) * c.V, y[i]);
 }
 
 // ---- step -----------------------------------------------------------------------------------
@@ -399,7 +435,7 @@ __global__ void __launch_bounds__(kThreads, 4) k_cache_step(Pool c, const T* __r
     };
     fetch(0);
     window_keys<T, true>(c, sh, bh, n, 0, c.K, ld, k, ga, grp == 0, kt, decay);
-    window_values<T, true>(c, sh, bh, n, grp, v, vs);
+    window_values<T, true, VEC>(c, sh, bh, n, grp, v, vs);
     for (int r = tid; r < ld; r += kThreads)
         wq[r] = r < c.K ? ldf(q + bh * c.K + r) * decay[r] * scale[int64_t(r) * c.NG] : 0.f;
     __syncthreads();
@@ -477,12 +513,12 @@ __global__ void __launch_bounds__(kThreads, 4) k_cache_step(Pool c, const T* __r
 constexpr int kReadWarps = 16, kWinWarps = 8;
 constexpr int kReadThreads = kReadWarps * 32, kWinThreads = kWinWarps * 32;
 constexpr int kStreamThreads = kReadThreads + kWinThreads + 96;
-constexpr int kPasses = 2;                    // rows of a chunk that one lane reads
+constexpr int kPasses = 4;                    // rows of a chunk that one lane reads
 constexpr int kMaxRing = 12;
 constexpr int kFoldRows = 4;                  // state rows a warp forms at a time (registers: 25 warps share the SM's)
 constexpr int kMaxRows = 1024;                // rows of a call in one launch
 constexpr int kDead = 255;
-constexpr int kFoldCost = 6;                  // of a folding group, where an ordinary head costs its number of groups
+constexpr int kFoldCost = 12;                 // of a folding group, where an ordinary head costs its number of groups
 constexpr size_t kStreamSmem = 227 * 1024 - 8192;  // less the static part
 
 struct StreamPlan {
@@ -509,28 +545,6 @@ __device__ __forceinline__ void bulk_copy(void* dst, const void* src, uint32_t b
                      tc::smem_u32(dst)),
                  "l"(src), "r"(bytes), "r"(tc::smem_u32(bar))
                  : "memory");
-}
-
-// Two or four adjacent elements as fp32, and four back.
-__device__ __forceinline__ float2 ld2(const float* p) { return *reinterpret_cast<const float2*>(p); }
-__device__ __forceinline__ float2 ld2(const __nv_bfloat16* p) {
-    return __bfloat1622float2(*reinterpret_cast<const __nv_bfloat162*>(p));
-}
-__device__ __forceinline__ void ld4(const float* p, float2* y) {
-    const float4 x = *reinterpret_cast<const float4*>(p);
-    y[0] = make_float2(x.x, x.y);
-    y[1] = make_float2(x.z, x.w);
-}
-__device__ __forceinline__ void ld4(const __nv_bfloat16* p, float2* y) {
-    const uint2 x = *reinterpret_cast<const uint2*>(p);
-    y[0] = __bfloat1622float2(*reinterpret_cast<const __nv_bfloat162*>(&x.x));
-    y[1] = __bfloat1622float2(*reinterpret_cast<const __nv_bfloat162*>(&x.y));
-}
-__device__ __forceinline__ void st4(float* p, const float2* y) {
-    *reinterpret_cast<float4*>(p) = make_float4(y[0].x, y[0].y, y[1].x, y[1].y);
-}
-__device__ __forceinline__ void st4(__nv_bfloat16* p, const float2* y) {
-    *reinterpret_cast<uint2*>(p) = make_uint2(tc::pack_bf16x2(y[0].x, y[0].y), tc::pack_bf16x2(y[1].x, y[1].y));
 }
 
 // A wait of a whole warp, which then agrees on its outcome.
@@ -1024,8 +1038,7 @@ size_t step_smem(const CacheProblem& p) {
     return sizeof(float) * (size_t(p.c.window) * (ld + kG) + 2 * ld + 64 + kWarps * kG);
 }
 size_t load_smem(const CacheProblem& p) {
-    constexpr size_t rows = kWarps * kBatch;
-    return sizeof(float) * (size_t(p.c.window) * (rows + kG) + rows);
+    return sizeof(float) * (size_t(p.c.window) * (kLoadRows + kG) + 2 * kLoadRows);
 }
 
 template <typename K>
@@ -1046,7 +1059,7 @@ gla_status store_typed(const CacheProblem& p, const float* S, const int32_t* slo
 template <typename T, bool INT8, bool VEC>
 gla_status load_typed(const CacheProblem& p, const int32_t* slots, const int32_t* lengths, float* S, cudaStream_t s) {
     const Pool c = pool_of(p);
-    const int parts = int(cdiv(p.K, kWarps * kBatch));
+    const int parts = int(cdiv(p.K, kLoadRows));
     const size_t smem = load_smem(p);
     if (!allow_smem(k_cache_load<T, INT8, VEC>, smem)) return GLA_ERR_CUDA;
     GLA_LAUNCH("cache_load", (k_cache_load<T, INT8, VEC>), unsigned(p.B * p.H * c.NG * parts), kThreads, smem, s, c,
@@ -1069,7 +1082,7 @@ gla_status step_typed(const CacheProblem& p, const void* q, const void* k, const
 
 // Shared memory and tiling of the streamed step, or smem = 0 where it does not apply: bulk copies want every stretch (a
 // token's k, v and log a, a window, a row of scales) to be a multiple of 16 bytes, groups want whole rows of lanes, and a
-// window must fit beside a ring of at least four chunks. It starts later than k_cache_step (the rows' order, the first
+// window must fit beside a ring of at least three chunks. It starts later than k_cache_step (the rows' order, the first
 // copies: 6 us against 4 for one head), which therefore keeps the calls that leave SMs without a head.
 StreamPlan stream_plan(const CacheProblem& p) {
     StreamPlan pl{};
@@ -1105,7 +1118,7 @@ StreamPlan stream_plan(const CacheProblem& p) {
     pl.chunk_rows = kPasses * pl.slices;
     pl.chunk_bytes = round_up(pl.chunk_rows * V, 128);
     const int64_t room = int64_t(kStreamSmem) - at, ring = room > 0 ? room / pl.chunk_bytes : 0;
-    if (ring < 4) return pl;
+    if (ring < 3) return pl;
     pl.ring = int(ring < kMaxRing ? ring : kMaxRing);
     pl.smem = size_t(at) + size_t(pl.ring) * pl.chunk_bytes;
     return pl;
