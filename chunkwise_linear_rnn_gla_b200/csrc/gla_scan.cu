@@ -7,9 +7,6 @@ namespace {
 // ---- forward ------------------------------------------------------------------------------
 // Grid: (sequence or head) x channel tile x cluster of `cl` blocks. Rows of round r and block q: from
 // (r cl + q) WARPS ROWS.
-//
-// The rows' maps of round r + 1 are worked out while the blocks' maps of round r travel, so a round costs its arithmetic
-// and not the exchange.
 template <typename T, int VEC, bool PACKED, bool PREACT, bool LEAK, int WARPS, int ROWS>
 __global__ void __launch_bounds__(WARPS * 32, 16 / WARPS)
     k_scan_fwd(ScanProblem p, int cl, const T* __restrict__ x, const float* __restrict__ la,
@@ -27,91 +24,71 @@ __global__ void __launch_bounds__(WARPS * 32, 16 / WARPS)
     const bool mine = at.mine;
     const int rounds = int(cdiv(p.L, int64_t(WARPS * ROWS) * cl));
     Exchange<V> ex{reinterpret_cast<Map<V>*>(dyn), bar, &abort_flag, err, cl, rank, rounds};
+    const RowOffsets<ROWS> whole(ROWS, p.D);
+    const auto offsets = [&](int64_t t) { return p.L - t >= ROWS ? whole : RowOffsets<ROWS>(p.L - t, p.D); };
+    Ahead<float, VEC, ROWS> ga;
+    Ahead<T, VEC, ROWS> xa;
     const auto stage = [&](int r) {
         const int64_t t = at.row(r), i = at.first(t);
-        const RowOffsets<ROWS> ro(p.L - t, p.D);
-        stage_rows<float, VEC, ROWS>(at.gates(r & 1), la + i, ro);
-        stage_rows<T, VEC, ROWS>(at.elems(r & 1, 0), x + i, ro);
+        const RowOffsets<ROWS> ro = offsets(t);
+        ga.fetch(at.gates(r & 1), la + i, ro);
+        xa.fetch(at.elems(r & 1, 0), x + i, ro);
     };
     stage(0);
-    copies_commit();
-    if (rounds > 1) stage(1);
     copies_commit();
     ex.begin();
     if constexpr (PACKED) copy_empty<V>(cu, p, head, c, mine, h0, hT, rank * WARPS + warp, cl * WARPS, lane);
     V carry = vset<V>(0.f);
     if (!PACKED && h0) carry = ldv<V>(h0 + lead * p.D + cc);
+    ex.ready();
     const int64_t nseg = cdiv(p.L, kSeg);
-    // the warp's rows of one round: their steps' maps, what the rows are, and the map of all of them
-    struct Rows {
-        V a[ROWS], b[ROWS];
-        RowInfo ri;
-        Map<V> own;
-    };
-    const auto work_out = [&](int r, Rows& x_) {
+    for (int r = 0; r < rounds; ++r) {
         const int par = r & 1;
         const int64_t t0 = at.row(r), first = at.first(t0);
-        const RowOffsets<ROWS> ro(p.L - t0, p.D);
+        const RowOffsets<ROWS> ro = offsets(t0);
+        xa.turn();
+        if (r + 1 < rounds) stage(r + 1);
+        copies_commit();
+        copies_wait<1>();
         RowInfo ri{0, 0, 0, 0};
         if constexpr (PACKED) ri = rows_packed<ROWS>(cu, int(p.B), t0, p.L, lane);
         else ri.valid = t0 + ROWS <= p.L ? ~0u : t0 < p.L ? (1u << (p.L - t0)) - 1 : 0u;
+        V a[ROWS], b[ROWS];
 #pragma unroll
         for (int j = 0; j < ROWS; ++j) {
             V w, dz;
-            gate_of<PREACT, LEAK>(p.inv_tau, ldv<V>(at.gates(par) + j * 32 * VEC), x_.a[j], w, dz);
-            x_.b[j] = take_row<V>(at.elems(par, 0), x + first, ro.off[j], j);
-            if constexpr (LEAK) x_.b[j] = vmul(x_.b[j], w);
+            gate_of<PREACT, LEAK>(p.inv_tau, ga.template row<V>(at.gates(par), j), a[j], w, dz);
+            b[j] = xa.template row<V>(at.elems(par, 0), j);
+            if constexpr (LEAK) b[j] = vmul(b[j], w);
         }
         constexpr uint32_t kAll = (1u << ROWS) - 1;
-        if ((ri.valid & kAll) != kAll) {
+        const bool all = (ri.valid & kAll) == kAll;
+        if (!all) {
 #pragma unroll
             for (int j = 0; j < ROWS; ++j)
-                if (!(ri.valid >> j & 1)) x_.a[j] = vset<V>(1.f), x_.b[j] = vset<V>(0.f);
+                if (!(ri.valid >> j & 1)) a[j] = vset<V>(1.f), b[j] = vset<V>(0.f);
         }
         Map<V> own{vset<V>(1.f), vset<V>(0.f)};
 #pragma unroll
         for (int j = 0; j < ROWS; ++j) {
             if (PACKED && (ri.start >> j & 1)) own.u = state_of<V>(h0, __shfl_sync(0xffffffffu, ri.n, j), p, head, cc);
-            own.a = vmul(own.a, x_.a[j]);
-            own.u = vfma(x_.a[j], own.u, x_.b[j]);
+            own.a = vmul(own.a, a[j]);
+            own.u = vfma(a[j], own.u, b[j]);
         }
         if (PACKED && ri.start) own.a = vset<V>(kForget);
         agg[par][warp][lane] = own;
-        x_.ri = ri;
-        x_.own = own;
-    };
-    // behind the block's barrier: the map of its rows in front of this warp's; the last warp sends the block's
-    const auto join_up = [&](int r, const Rows& x_) {
-        Map<V> pre{vset<V>(1.f), vset<V>(0.f)};
+        __syncthreads();
+        Map<V> pre{vset<V>(1.f), vset<V>(0.f)};  // of the block's rows in front of this warp's
 #pragma unroll
         for (int w = 0; w < WARPS - 1; ++w) {
             if (w < warp) {
-                const Map<V> m = agg[r & 1][w][lane];
+                const Map<V> m = agg[par][w][lane];
                 pre = Map<V>{join<PACKED>(m.a, pre.a), join<PACKED>(m.a, pre.u, m.u)};
             }
         }
-        if (cl > 1 && warp == WARPS - 1)
-            ex.put(r, Map<V>{join<PACKED>(x_.own.a, pre.a), join<PACKED>(x_.own.a, pre.u, x_.own.u)});
-        return pre;
-    };
-    copies_wait<1>();
-    Rows now;
-    work_out(0, now);
-    __syncthreads();
-    ex.ready();
-    Map<V> pre = join_up(0, now);
-    for (int r = 0; r < rounds; ++r) {
-        const int64_t t0 = at.row(r), first = at.first(t0);
-        const RowOffsets<ROWS> ro(p.L - t0, p.D);
-        Rows next;
-        if (r + 1 < rounds) {
-            if (r + 2 < rounds) stage(r + 2);
-            copies_commit();
-            copies_wait<1>();
-            work_out(r + 1, next);
-        }
         V in = carry;  // state entering the block's rows
         if (cl > 1) {
+            if (warp == WARPS - 1) ex.put(r, Map<V>{join<PACKED>(own.a, pre.a), join<PACKED>(own.a, pre.u, own.u)});
             const Map<V>* m = ex.get(r);
             for (int q = 0; q < cl; ++q) {
                 if (q == rank) in = carry;
@@ -120,31 +97,34 @@ __global__ void __launch_bounds__(WARPS * 32, 16 / WARPS)
         } else {
             Map<V> t = pre;
             for (int w = warp; w < WARPS; ++w) {
-                const Map<V> m = agg[r & 1][w][lane];
+                const Map<V> m = agg[par][w][lane];
                 t = Map<V>{join<PACKED>(m.a, t.a), join<PACKED>(m.a, t.u, m.u)};
             }
             carry = join<PACKED>(t.a, in, t.u);
         }
         V s = join<PACKED>(pre.a, in, pre.u);
         if (seg && mine && t0 < p.L && t0 % kSeg == 0) stv(seg + (lead * nseg + t0 / kSeg) * p.D + c, s);
+        T* out = h + first;
+        if (!PACKED && all && h) {
 #pragma unroll
-        for (int j = 0; j < ROWS; ++j) {
-            if (PACKED && (now.ri.start >> j & 1))
-                s = state_of<V>(h0, __shfl_sync(0xffffffffu, now.ri.n, j), p, head, cc);
-            s = vfma(now.a[j], s, now.b[j]);
-            if (h && mine && (now.ri.valid >> j & 1)) stv(h + first + ro.off[j], s);
-            if (PACKED && (now.ri.end >> j & 1)) {
-                const int64_t n = __shfl_sync(0xffffffffu, now.ri.n, j);
-                if (hT && mine) stv(hT + (n * p.H + head) * p.D + c, s);
+            for (int j = 0; j < ROWS; ++j) {
+                s = vfma(a[j], s, b[j]);
+                if (mine) stv(out + ro.off[j], s);
+            }
+        } else {
+#pragma unroll
+            for (int j = 0; j < ROWS; ++j) {
+                if (PACKED && (ri.start >> j & 1)) s = state_of<V>(h0, __shfl_sync(0xffffffffu, ri.n, j), p, head, cc);
+                s = vfma(a[j], s, b[j]);
+                if (h && mine && (ri.valid >> j & 1)) stv(out + ro.off[j], s);
+                if (PACKED && (ri.end >> j & 1)) {
+                    const int64_t n = __shfl_sync(0xffffffffu, ri.n, j);
+                    if (hT && mine) stv(hT + (n * p.H + head) * p.D + c, s);
+                }
             }
         }
         // rows behind the last one leave the state as it is, so the warp with the last row holds hT
         if (!PACKED && hT && mine && t0 < p.L && t0 + ROWS >= p.L) stv(hT + lead * p.D + c, s);
-        if (r + 1 < rounds) {
-            __syncthreads();
-            pre = join_up(r + 1, next);
-            now = next;
-        }
     }
     ex.end();
 }
@@ -190,19 +170,27 @@ __global__ void __launch_bounds__(kStepThreads) k_scan_step(ScanProblem p, const
     stf(h + b * n + c, y);
 }
 
-constexpr int kFwdWarps = 8, kFwdRows = 8;
+constexpr int kFwdRows = 8;
+
+template <typename T, int VEC, bool PACKED, bool PREACT, bool LEAK, int WARPS>
+gla_status fwd_launch(const ScanProblem& p, const void* x, const float* la, const int32_t* cu, const float* h0,
+                      void* h, float* hT, float* seg, cudaStream_t s) {
+    using V = typename VecOf<VEC>::type;
+    constexpr int threads = WARPS * 32, stages = WARPS * kFwdStage<T, VEC, kFwdRows>;
+    const int64_t groups = (PACKED ? p.H : p.B * p.H) * cdiv(p.D, 32 * VEC);
+    const auto kernel = k_scan_fwd<T, VEC, PACKED, PREACT, LEAK, WARPS, kFwdRows>;
+    static const ClusterFit fit = ask_fit(kernel, threads, smem_of<V>, stages);
+    const int cl = cluster_size(fit, groups, p.L, WARPS * kFwdRows);
+    return launch_clusters("scan_fwd", kernel, fit, groups, cl, threads, smem_of<V>(cl, stages), s, p, cl,
+                           static_cast<const T*>(x), la, cu, h0, static_cast<T*>(h), hT, seg, device_error_word());
+}
 
 template <typename T, int VEC, bool PACKED, bool PREACT, bool LEAK>
 gla_status fwd_typed(const ScanProblem& p, const void* x, const float* la, const int32_t* cu, const float* h0,
                      void* h, float* hT, float* seg, cudaStream_t s) {
-    using V = typename VecOf<VEC>::type;
-    constexpr int threads = kFwdWarps * 32, stages = kFwdWarps * kFwdStage<T, VEC, kFwdRows>;
     const int64_t groups = (PACKED ? p.H : p.B * p.H) * cdiv(p.D, 32 * VEC);
-    const auto kernel = k_scan_fwd<T, VEC, PACKED, PREACT, LEAK, kFwdWarps, kFwdRows>;
-    static const ClusterFit fit = ask_fit(kernel, threads, smem_of<V>, stages);
-    const int cl = cluster_size(fit, groups, p.L, kFwdWarps * kFwdRows);
-    return launch_clusters("scan_fwd", kernel, fit, groups, cl, threads, smem_of<V>(cl, stages), s, p, cl,
-                           static_cast<const T*>(x), la, cu, h0, static_cast<T*>(h), hT, seg, device_error_word());
+    if (many_groups(groups)) return fwd_launch<T, VEC, PACKED, PREACT, LEAK, 4>(p, x, la, cu, h0, h, hT, seg, s);
+    return fwd_launch<T, VEC, PACKED, PREACT, LEAK, 8>(p, x, la, cu, h0, h, hT, seg, s);
 }
 
 template <typename T>

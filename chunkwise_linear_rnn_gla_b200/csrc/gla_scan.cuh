@@ -324,8 +324,8 @@ struct RowOffsets {
 // ---- staged loads -------------------------------------------------------------------------
 // The rows of the next round travel while this one is computed: every lane copies its own channels into its own
 // places of shared memory (cp.async, 4 or 8 bytes a row), so that no thread waits for another's copies and two
-// rounds' rows cost no registers. Single bf16 channels (an odd width) are too narrow for such a copy and are loaded
-// where they are used.
+// rounds' rows cost no registers. Single bf16 channels (an odd width) are too narrow for such a copy and travel in
+// registers.
 template <int BYTES>
 __device__ __forceinline__ void copy_async(void* dst, const void* src) {
     asm volatile("cp.async.ca.shared.global [%0], [%1], %2;" ::"r"(tc::smem_u32(dst)), "l"(src), "n"(BYTES) : "memory");
@@ -337,20 +337,31 @@ __device__ __forceinline__ void copies_wait() { asm volatile("cp.async.wait_grou
 template <typename T, int VEC>
 constexpr bool kStaged = sizeof(T) * VEC >= 4;
 
-// A lane's rows of one tensor in shared memory: row j at [j][lane].
+// A lane's rows of one tensor, a round ahead: row j at [j][lane] in shared memory, or in registers where they are too
+// narrow for a copy.
 template <typename T, int VEC, int ROWS>
-__device__ __forceinline__ void stage_rows(T* st, const T* src, const RowOffsets<ROWS>& ro) {
-    if constexpr (kStaged<T, VEC>) {
+struct Ahead {
+    T kept[kStaged<T, VEC> ? 1 : ROWS], coming[kStaged<T, VEC> ? 1 : ROWS];
+    __device__ __forceinline__ void fetch(T* st, const T* src, const RowOffsets<ROWS>& ro) {
 #pragma unroll
-        for (int j = 0; j < ROWS; ++j) copy_async<sizeof(T) * VEC>(st + j * 32 * VEC, src + ro.off[j]);
+        for (int j = 0; j < ROWS; ++j) {
+            if constexpr (kStaged<T, VEC>) copy_async<sizeof(T) * VEC>(st + j * 32 * VEC, src + ro.off[j]);
+            else coming[j] = src[ro.off[j]];
+        }
     }
-}
-template <typename V, typename T>
-__device__ __forceinline__ V take_row(const T* st, const T* src, uint32_t off, int j) {
-    constexpr int VEC = int(sizeof(V) / 4);
-    if constexpr (kStaged<T, VEC>) return ldv<V>(st + j * 32 * VEC);
-    else return ldv<V>(src + off);
-}
+    // what was fetched last is this round's now
+    __device__ __forceinline__ void turn() {
+        if constexpr (!kStaged<T, VEC>) {
+#pragma unroll
+            for (int j = 0; j < ROWS; ++j) kept[j] = coming[j];
+        }
+    }
+    template <typename V>
+    __device__ __forceinline__ V row(const T* st, int j) const {
+        if constexpr (kStaged<T, VEC>) return ldv<V>(st + j * 32 * VEC);
+        else return ldv<V>(&kept[j]);
+    }
+};
 
 // bytes a warp's stage takes
 template <typename T, int VEC, int ROWS>
@@ -435,6 +446,11 @@ int cluster_size(const ClusterFit& f, int64_t groups, int64_t L, int tile) {
     }
     return best;
 }
+
+// Blocks of four warps where there are channel tiles and sequences for a quarter of the SMs: more blocks that wait at
+// different times (forward 33.3 us against 35.6 at 8 sequences of 2048 steps, width 1024). Else of eight, whose rounds
+// cover twice the rows (29 us against 43 at one sequence of 16384 steps, width 64).
+inline bool many_groups(int64_t groups) { return groups * 4 >= 148; }
 
 template <typename K, typename... Args>
 gla_status launch_clusters(const char* name, K kernel, const ClusterFit& f, int64_t groups, int cl, int threads, size_t smem,

@@ -28,12 +28,16 @@ __global__ void __launch_bounds__(WARPS * 32, 16 / WARPS)
     const bool mine = at.mine;
     const int rounds = int(cdiv(p.L, int64_t(WARPS * ROWS) * cl));
     Exchange<V> ex{reinterpret_cast<Map<V>*>(dyn), bar, &abort_flag, err, cl, rank, rounds};
+    const RowOffsets<ROWS> whole(ROWS, p.D);
+    const auto offsets = [&](int64_t t) { return p.L - t >= ROWS ? whole : RowOffsets<ROWS>(p.L - t, p.D); };
+    Ahead<float, VEC, ROWS> ga;
+    Ahead<T, VEC, ROWS> xa, da;
     const auto stage = [&](int r) {
         const int64_t t = at.row(r), i = at.first(t);
-        const RowOffsets<ROWS> ro(p.L - t, p.D);
-        stage_rows<float, VEC, ROWS>(at.gates(r & 1), la + i, ro);
-        stage_rows<T, VEC, ROWS>(at.elems(r & 1, 0), x + i, ro);
-        stage_rows<T, VEC, ROWS>(at.elems(r & 1, 1), dh + i, ro);
+        const RowOffsets<ROWS> ro = offsets(t);
+        ga.fetch(at.gates(r & 1), la + i, ro);
+        xa.fetch(at.elems(r & 1, 0), x + i, ro);
+        da.fetch(at.elems(r & 1, 1), dh + i, ro);
     };
     stage(rounds - 1);
     copies_commit();
@@ -47,8 +51,10 @@ __global__ void __launch_bounds__(WARPS * 32, 16 / WARPS)
         const int r = rounds - 1 - it, par = r & 1;
         const int64_t t0 = at.row(r), first = at.first(t0);
         const int64_t tile = (int64_t(r) * cl + rank) * (WARPS * ROWS) / kSeg;  // a block's rows begin with a segment
-        const RowOffsets<ROWS> ro(p.L - t0, p.D);
+        const RowOffsets<ROWS> ro = offsets(t0);
         V s = ldv<V>(seg + (lead * nseg + (tile < nseg ? tile : nseg - 1)) * p.D + cc);  // entering the block's rows
+        xa.turn();
+        da.turn();
         if (r > 0) stage(r - 1);
         copies_commit();
         copies_wait<1>();
@@ -58,9 +64,9 @@ __global__ void __launch_bounds__(WARPS * 32, 16 / WARPS)
         V a[ROWS], w[ROWS], xv[ROWS], d[ROWS], dz[ROWS];
 #pragma unroll
         for (int j = 0; j < ROWS; ++j) {
-            gate_of<PREACT, LEAK>(p.inv_tau, ldv<V>(at.gates(par) + j * 32 * VEC), a[j], w[j], dz[j]);
-            xv[j] = take_row<V>(at.elems(par, 0), x + first, ro.off[j], j);
-            d[j] = take_row<V>(at.elems(par, 1), dh + first, ro.off[j], j);
+            gate_of<PREACT, LEAK>(p.inv_tau, ga.template row<V>(at.gates(par), j), a[j], w[j], dz[j]);
+            xv[j] = xa.template row<V>(at.elems(par, 0), j);
+            d[j] = da.template row<V>(at.elems(par, 1), j);
         }
         constexpr uint32_t kAll = (1u << ROWS) - 1;
         if ((ri.valid & kAll) != kAll) {
@@ -167,15 +173,12 @@ gla_status bwd_launch(const ScanProblem& p, const void* x, const float* la, cons
                            dla, dh0, seg, device_error_word());
 }
 
-// Blocks of four warps where there are channel tiles and sequences for at least half a wave of them (more blocks that
-// wait at different times: 71 us against 77 at 4 sequences of 2048 steps, width 2048), else of eight, whose rounds cover
-// twice the rows (82 us against 107 at one sequence of 16384 steps, width 1024).
 template <typename T, int VEC, bool PACKED, bool PREACT, bool LEAK>
 gla_status bwd_typed(const ScanProblem& p, const void* x, const float* la, const int32_t* cu, const float* h0,
                      const void* dh, const float* dhT, void* dx, float* dla, float* dh0, const float* seg,
                      cudaStream_t s) {
     const int64_t groups = (PACKED ? p.H : p.B * p.H) * cdiv(p.D, 32 * VEC);
-    if (groups * 4 >= 148) return bwd_launch<T, VEC, PACKED, PREACT, LEAK, 4>(p, x, la, cu, h0, dh, dhT, dx, dla, dh0, seg, s);
+    if (many_groups(groups)) return bwd_launch<T, VEC, PACKED, PREACT, LEAK, 4>(p, x, la, cu, h0, dh, dhT, dx, dla, dh0, seg, s);
     return bwd_launch<T, VEC, PACKED, PREACT, LEAK, 8>(p, x, la, cu, h0, dh, dhT, dx, dla, dh0, seg, s);
 }
 
