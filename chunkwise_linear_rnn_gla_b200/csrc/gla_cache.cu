@@ -496,7 +496,7 @@ __global__ void __launch_bounds__(kThreads, 4) k_cache_step(Pool c, const T* __r
 }
 
 // ---- step, streamed ---------------------------------------------------------------------------
-// For calls with heads enough to give every SM some, of shapes that bulk copies can move (stream_plan below). One
+// For calls with large heads for every SM, of shapes that bulk copies can move (stream_plan below). One
 // persistent block per SM takes its share of the heads; its warps have three parts, a head apart in time:
 //   3 producers  one thread of the first keeps a head's codes coming, one contiguous stretch fetched in chunks through a
 //                ring; the second's fetches its token, keys, log decays and scales ahead of them, the third's its values;
@@ -524,7 +524,6 @@ constexpr size_t kStreamSmem = 227 * 1024 - 8192;  // less the static part
 struct StreamPlan {
     int ring;         // chunks in flight
     int chunk_rows;   // state rows of a chunk
-    int lanes;        // lanes that share a group's row (16 codes each)
     int slices;       // rows read at a time
     int off_q, off_k, off_g, off_kw, off_gw, off_sc;   // what the window warps read
     int off_v, off_vw;                                 // what the readers read
@@ -802,7 +801,7 @@ __global__ void __launch_bounds__(kStreamThreads, 1)
                 const int n = last.n, half = t & 1;
                 const bool whole = last.grp < 0;
                 T* put = static_cast<T*>(c.v) + (last.sh * c.W + n) * V;
-                const int v0 = whole ? 0 : last.grp * kG, quads = (whole || v0 + kG > V ? V - v0 : kG) / 4;
+                const int v0 = whole ? 0 : last.grp * kG, quads = (whole ? V : kG) / 4;
                 const int rows = whole ? pl.slices : kReadWarps, ld = whole ? V : kG;
                 // four columns of two lanes, which take every other row of the sums and every other token
                 for (int i0 = 0; i0 < quads; i0 += kWinThreads / 2) {
@@ -931,8 +930,8 @@ __global__ void __launch_bounds__(kStreamThreads, 1)
         return;
     }
     // ---- readers
-    const int unit = tid / pl.lanes, ugrp = unit % NG, slice = unit / NG;
-    const int ucol = ugrp * kG + (tid % pl.lanes) * 16;
+    const int unit = tid / (kG / 16), ugrp = unit % NG, slice = unit / NG;  // eight lanes read a group's row
+    const int ucol = ugrp * kG + tid % (kG / 16) * 16;
     const bool reads = slice < pl.slices;
     Turn wt, rt;
     int lives = 0;
@@ -996,18 +995,7 @@ __global__ void __launch_bounds__(kStreamThreads, 1)
 #pragma unroll
                 for (int i = 0; i < kFoldRows; ++i) z[i] = cols.codes(codes + int64_t(r + i) * V);
                 const auto value = [&](int j, float2* t) {
-                    const T* vr = (j < n ? vw + j * V : vb) + cols.col[0];
-                    t[0] = t[1] = make_float2(0.f, 0.f);
-                    if (!cols.on[0]) return;
-                    if constexpr (sizeof(T) == 2) {
-                        const uint2 w = *reinterpret_cast<const uint2*>(vr);
-                        t[0] = __bfloat1622float2(*reinterpret_cast<const __nv_bfloat162*>(&w.x));
-                        t[1] = __bfloat1622float2(*reinterpret_cast<const __nv_bfloat162*>(&w.y));
-                    } else {
-                        const float4 w = *reinterpret_cast<const float4*>(vr);
-                        t[0] = make_float2(w.x, w.y);
-                        t[1] = make_float2(w.z, w.w);
-                    }
+                    ld4((j < n ? vw + j * V : vb) + cols.col[0], t);
                 };
                 form_rows<INT8, kFoldRows>(z, wq + K + r, dec + r, kt + r, K, used, value, y);
 #pragma unroll
@@ -1081,17 +1069,18 @@ gla_status step_typed(const CacheProblem& p, const void* q, const void* k, const
 }
 
 // Shared memory and tiling of the streamed step, or smem = 0 where it does not apply: bulk copies want every stretch (a
-// token's k, v and log a, a window, a row of scales) to be a multiple of 16 bytes, groups want whole rows of lanes, and a
-// window must fit beside a ring of at least three chunks. It starts later than k_cache_step (the rows' order, the first
-// copies: 6 us against 4 for one head), which therefore keeps the calls that leave SMs without a head.
+// token's k, v and log a, a window, a row of scales) to be a multiple of 16 bytes, the readers want whole groups, and a
+// window must fit beside a ring of at least three chunks. A head costs it about 4 us of phases besides its codes, and a
+// call 6 us before the first sums; k_cache_step starts a block for every group and pays those in parallel. So it takes
+// the calls with a head of at least 96 K entries for every SM: 1024 heads of 256 x 512 in 42 us against 73, 256 heads in
+// 18.6 against 20.6, 148 heads in 11.9 against 11.8, but 1024 heads of 128 x 256 in 33 against 27.
 StreamPlan stream_plan(const CacheProblem& p) {
     StreamPlan pl{};
     const int K = int(p.K), V = int(p.V), W = p.c.window, e = p.bf16 ? 2 : 4;
-    if (p.B * p.H < kSms || p.H * cdiv(p.V, kG) > (1 << 20)) return pl;
-    if (K % 8 != 0 || K > 4096 || !(V % kG == 0 ? V <= 2048 : V < kG && V % 16 == 0)) return pl;
-    const int NG = int(cdiv(V, kG));
-    pl.lanes = V < kG ? V / 16 : kG / 16;
-    pl.slices = kReadThreads / pl.lanes / NG;
+    if (p.B * p.H < kSms || p.K * p.V < 96 * 1024 || p.H * cdiv(p.V, kG) > (1 << 20)) return pl;
+    if (K % 8 != 0 || K > 4096 || V % kG != 0 || V > 2048) return pl;
+    const int NG = V / kG;
+    pl.slices = kReadThreads / (kG / 16) / NG;
     int at = 0;
     const auto take = [&](int bytes) {
         const int here = at;
