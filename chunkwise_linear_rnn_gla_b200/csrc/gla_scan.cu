@@ -179,7 +179,8 @@ gla_status fwd_launch(const ScanProblem& p, const void* x, const float* la, cons
     constexpr int threads = WARPS * 32, stages = WARPS * kFwdStage<T, VEC, kFwdRows>;
     const int64_t groups = (PACKED ? p.H : p.B * p.H) * cdiv(p.D, 32 * VEC);
     const auto kernel = k_scan_fwd<T, VEC, PACKED, PREACT, LEAK, WARPS, kFwdRows>;
-    static const ClusterFit fit = ask_fit(kernel, threads, smem_of<V>, stages);
+    static FitOnce once;
+    const ClusterFit fit = cluster_fit(once, kernel, threads, smem_of<V>, stages);
     const int cl = cluster_size(fit, groups, p.L, WARPS * kFwdRows);
     return launch_clusters("scan_fwd", kernel, fit, groups, cl, threads, smem_of<V>(cl, stages), s, p, cl,
                            static_cast<const T*>(x), la, cu, h0, static_cast<T*>(h), hT, seg, device_error_word());

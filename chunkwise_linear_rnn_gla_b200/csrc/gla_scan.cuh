@@ -8,11 +8,16 @@
 // then runs its steps from the state that enters it. All of this happens on one read of the inputs:
 //   warp     8 rows (steps) x 32 or 64 channels in registers, one or two channels a lane;
 //   block    4 or 8 warps, 32 or 64 rows: the warps' maps are joined in shared memory;
-//   cluster  up to 16 blocks, 512 or 1024 rows: every block puts its map into the shared memory of all the others
-//            (distributed shared memory), one cluster barrier a round, and each joins those in front of it.
+//   cluster  up to 16 blocks, 512 or 1024 rows: every block sends its map into the shared memory of all the others
+//            (asynchronous stores counted on their mbarriers), and each joins those in front of it.
 // A cluster walks the time axis in rounds and carries the state in registers, so a call needs no workspace,
-// no flags in memory and no second launch, and its result does not depend on timing. The kernels are bound by
-// memory: 8 (bf16) or 12 (fp32) bytes an element forward, 14 or 20 backward.
+// no flags in memory and no second launch, and its result does not depend on timing.
+//
+// Floor: 8 (bf16) or 12 (fp32) bytes an element forward, 14 or 20 backward, at the copy bandwidth. Measured (device time,
+// inputs larger than L2 in turn): forward 33.2 us at 8 sequences of 2048 steps, width 1024 (134 MB, 4.0 TB/s, floor
+// 20.5); forward and backward 101 us at 4 x 2048, width 2048, gate from its pre-activation (369 MB moved, floor 57).
+// What is left over the floor is issue slots (37 instructions an element forward, 70 backward, 60% of the slots taken)
+// and the chain of a round: gates, maps, the exchange, steps. Without its loads the forward still takes 32 us.
 //
 // A boundary between packed sequences is a step whose map forgets: (forget, a h0 + b). In the backward the same
 // steps stop the gradient, which walks the maps the other way: with y_t = a_t g_t, g_t = dh_t + y_{t+1}.
@@ -21,7 +26,9 @@
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
 
+#include <atomic>
 #include <cstdint>
+#include <mutex>
 #include <type_traits>
 
 #include "gla_common.cuh"
@@ -404,18 +411,31 @@ size_t smem_of(int cl, int stages_bytes) {
     return (cl > 1 ? size_t(2) * cl * 32 * sizeof(Map<V>) : 0) + size_t(2) * stages_bytes;
 }
 
-// How many clusters of each size the device holds at once, per kernel: a cluster sits inside one GPC, so large ones
-// leave some SMs empty. Asked once per kernel (the answer depends on nothing else).
+// What a launch with clusters of up to kMaxCluster blocks needs of the kernel, on the current device.
+template <typename K>
+bool allow_clusters(K kernel, size_t smem) {
+    return cudaFuncSetAttribute(kernel, cudaFuncAttributeNonPortableClusterSizeAllowed, 1) == cudaSuccess &&
+           cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, int(smem)) == cudaSuccess;
+}
+
+// How many clusters of each size the device holds at once, for one kernel: a cluster sits inside one GPC, so large ones
+// leave some SMs empty. Asked once (the answer depends on the kernel and the kind of GPU alone); an answer that could
+// not be had is asked for again.
 struct ClusterFit {
     int fit[kMaxCluster + 1] = {};
 };
-template <typename K>
-ClusterFit ask_fit(K kernel, int threads, size_t (*smem)(int, int), int stages_bytes) {
+struct FitOnce {
+    std::mutex mu;
+    std::atomic<bool> have{false};
     ClusterFit f;
-    if (cudaFuncSetAttribute(kernel, cudaFuncAttributeNonPortableClusterSizeAllowed, 1) != cudaSuccess ||
-        cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, int(smem(kMaxCluster, stages_bytes))) !=
-            cudaSuccess)
-        return f;
+};
+template <typename K>
+ClusterFit cluster_fit(FitOnce& once, K kernel, int threads, size_t (*smem)(int, int), int stages_bytes) {
+    if (once.have.load(std::memory_order_acquire)) return once.f;
+    std::lock_guard<std::mutex> lk(once.mu);
+    if (once.have.load(std::memory_order_relaxed)) return once.f;
+    ClusterFit f;
+    if (!allow_clusters(kernel, smem(kMaxCluster, stages_bytes))) return f;
     for (int cl = 1; cl <= kMaxCluster; ++cl) {
         cudaLaunchConfig_t cfg = {};
         cfg.gridDim = dim3(unsigned(cl));
@@ -429,6 +449,11 @@ ClusterFit ask_fit(K kernel, int threads, size_t (*smem)(int, int), int stages_b
         cfg.numAttrs = 1;
         int n = 0;
         if (cudaOccupancyMaxActiveClusters(&n, kernel, &cfg) == cudaSuccess) f.fit[cl] = n;
+        else (void)cudaGetLastError();  // a size that this device does not take is no error of the launch to come
+    }
+    if (f.fit[1] > 0) {
+        once.f = f;
+        once.have.store(true, std::memory_order_release);
     }
     return f;
 }
@@ -455,7 +480,7 @@ inline bool many_groups(int64_t groups) { return groups * 4 >= 148; }
 template <typename K, typename... Args>
 gla_status launch_clusters(const char* name, K kernel, const ClusterFit& f, int64_t groups, int cl, int threads, size_t smem,
                            cudaStream_t s, Args... args) {
-    if (f.fit[1] < 1) return GLA_ERR_CUDA;
+    if (f.fit[1] < 1 || !allow_clusters(kernel, smem)) return GLA_ERR_CUDA;
     if (groups * cl > (int64_t(1) << 31) - 1) return GLA_ERR_UNSUPPORTED;
     launch_begin(name, s);
     cudaLaunchConfig_t cfg = {};

@@ -166,7 +166,8 @@ gla_status bwd_launch(const ScanProblem& p, const void* x, const float* la, cons
     constexpr int threads = WARPS * 32, stages = WARPS * kBwdStage<T, VEC, kBwdRows>;
     const int64_t groups = (PACKED ? p.H : p.B * p.H) * cdiv(p.D, 32 * VEC);
     const auto kernel = k_scan_bwd<T, VEC, PACKED, PREACT, LEAK, WARPS>;
-    static const ClusterFit fit = ask_fit(kernel, threads, smem_of<V>, stages);
+    static FitOnce once;
+    const ClusterFit fit = cluster_fit(once, kernel, threads, smem_of<V>, stages);
     const int cl = cluster_size(fit, groups, p.L, WARPS * kBwdRows);
     return launch_clusters("scan_bwd", kernel, fit, groups, cl, threads, smem_of<V>(cl, stages), s, p, cl,
                            static_cast<const T*>(x), la, cu, h0, static_cast<const T*>(dh), dhT, static_cast<T*>(dx),

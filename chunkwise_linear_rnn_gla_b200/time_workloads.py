@@ -15,6 +15,10 @@ For the decode step (`inputs.DECODE`, and the same shape with B=256 whose 134 MB
 the median of 20 calls with L2 flushed before each, and a CUDA graph of 64 calls replayed 5 times
 with the state left in L2 between calls.
 
+For the elementwise recurrence ("scan": the widths of the 340M and 1.3B layers and the 16384-step sequence)
+and the recurrent-state cache ("cache": store, load and step of the decode batch and of the 1.3B layer's state
+size, beside gla_step's figures): the same way, L2 flushed before every call.
+
 One line per case on stdout. This is a measurement utility; the parity tests live in `tests/`.
 """
 import argparse
@@ -143,17 +147,76 @@ def time_decode(B, H, K, V, flush):
           % (B, H, K, V, us, state_bytes / us / 1e3), flush=True)
 
 
+def time_scan(flush):
+    from . import scan
+
+    for B, L, D in ((8, 2048, 1024), (4, 2048, 2048), (1, 16384, 1024)):
+        g = torch.Generator(device="cuda").manual_seed(0)
+        x, dh = (torch.randn(B, 1, L, D, generator=g, device="cuda").bfloat16() for _ in range(2))
+        la = torch.nn.functional.logsigmoid(torch.randn(B, 1, L, D, generator=g, device="cuda")) / 16
+        ws = scan.scan_workspace(x)
+
+        def fwd():
+            scan.scan_fwd(x, la, write="leak", workspace=ws)
+
+        def both():
+            fwd()
+            scan.scan_bwd(x, la, dh, write="leak", workspace=ws, ws_from_fwd=True)
+
+        for tag, fn, nbytes in (("fwd", fwd, 8), ("fwd+bwd", both, 22)):
+            for _ in range(3):
+                fn()
+            ms = _median_ms(fn, flush, 10)
+            print("scan B=%d L=%d D=%d %-8s %8.1f us  %8.2f Mtok/s  %6.0f GB/s moved"
+                  % (B, L, D, tag, ms * 1000, B * L / ms / 1e3, nbytes * B * L * D / ms / 1e6), flush=True)
+    for B, D in ((1, 1024), (256, 2048)):
+        x, la = torch.randn(B, 1, D, device="cuda").bfloat16(), -torch.rand(B, 1, D, device="cuda")
+        state, slots = torch.zeros(B, 1, D, device="cuda"), torch.arange(B, dtype=torch.int32, device="cuda")
+        h = torch.empty_like(x)
+        for _ in range(3):
+            scan.scan_step(x, la, state, slots, h=h)
+        ms = _median_ms(lambda: scan.scan_step(x, la, state, slots, h=h), flush, 20)
+        print("scan step B=%d D=%d %8.2f us" % (B, D, ms * 1000), flush=True)
+
+
+def time_cache(flush):
+    from . import cache
+
+    for B, H, K, V in ((DECODE["B"], DECODE["H"], DECODE["K"], DECODE["V"]), (256, 4, 256, 512)):
+        st = make_step_inputs(B, H, K, V, 1, DECODE["dtype"], seed=0)
+        tok = [st[n][0].cuda() for n in ("q", "k", "v", "log_a")]
+        S = torch.randn(B, H, K, V, device="cuda")
+        slots = torch.randperm(B, device="cuda").to(torch.int32)
+        for fmt in ("int8", "e4m3"):
+            c = cache.StateCache.empty(B, H, K, V, format=fmt)
+            W = c.window
+            fills = (("mid-window", torch.arange(B, device="cuda") % (W - 1)), ("1/%d fold" % W, torch.arange(B, device="cuda") % W),
+                     ("all fold", torch.full((B,), W - 1, device="cuda")))
+            cases = [("store", lambda: cache.cache_store(c, S, slots), 5 * S.numel()),
+                     ("load", lambda: cache.cache_load(c, slots, S=S), 5 * S.numel())]
+            for name, n in fills:
+                n = n.to(torch.int32)
+                cases.append(("step, " + name, lambda n=n: cache.cache_step(c, *tok, slots, n), S.numel()))
+            for name, fn, nbytes in cases:
+                for _ in range(3):
+                    fn()
+                ms = _median_ms(fn, flush, 10)
+                print("cache B=%-4d H=%d d_k=%d d_v=%d %s %-18s %8.2f us  %6.0f GB/s of state"
+                      % (B, H, K, V, fmt, name, ms * 1000, nbytes / ms / 1e6), flush=True)
+
+
 def main(argv=None):
     ap = argparse.ArgumentParser(description=__doc__.split("\n\n")[0])
-    ap.add_argument("--only", nargs="*", default=None, help="workload names (and/or 'decode') to time")
+    ap.add_argument("--only", nargs="*", default=None, help="workload names (and/or 'decode', 'scan', 'cache') to time")
     ap.add_argument("--list", action="store_true", help="list the workloads and exit")
     ap.add_argument("--reps", type=int, default=10, help="timed calls per case (gated slot attention)")
     args = ap.parse_args(argv)
-    names = [n for n, w in WORKLOADS.items() if w.dtype == "bf16"] + [GSA_WORKLOAD["name"], "decode"]
+    names = [n for n, w in WORKLOADS.items() if w.dtype == "bf16"] + [GSA_WORKLOAD["name"], "decode", "scan", "cache"]
+    notes = {"decode": "decode step, B=64 and B=256", "scan": "elementwise recurrence", "cache": "recurrent-state cache"}
     if args.list:
         for n in names:
             print(n, "-", WORKLOADS[n].note if n in WORKLOADS else
-                  GSA_WORKLOAD["note"] if n == GSA_WORKLOAD["name"] else "decode step, B=64 and B=256")
+                  GSA_WORKLOAD["note"] if n == GSA_WORKLOAD["name"] else notes[n])
         return 0
     if args.only:
         unknown = [n for n in args.only if n not in names]
@@ -170,6 +233,10 @@ def main(argv=None):
                 time_decode(B, DECODE["H"], DECODE["K"], DECODE["V"], flush)
         elif n == GSA_WORKLOAD["name"]:
             time_gsa(flush, max(1, args.reps))
+        elif n == "scan":
+            time_scan(flush)
+        elif n == "cache":
+            time_cache(flush)
         else:
             time_layer(WORKLOADS[n], flush)
     return 0
