@@ -426,6 +426,23 @@ def test_step_refuses_bad_rows(lib):
 
 
 @pytest.mark.gpu
+@pytest.mark.parametrize("B,H,K,V", [(5, 2, 32, 160), (40, 4, 256, 384)])
+def test_step_refuses_a_slot_that_a_refused_row_names(lib, B, H, K, V):
+    """Both forms of the step: a row whose length is bad is refused, and so is a later row with its slot."""
+    c, _, g = fill_pool(B, H, K, V, 4, "int8", torch.bfloat16)
+    before = c.codes.clone()
+    t = {n: x.cuda() for n, x in token(c, B, g).items()}
+    sl = list(range(B))
+    sl[3] = 1
+    ln = [0] * B
+    ln[1] = -1
+    o = gc.cache_step(c, t["q"], t["k"], t["v"], t["log_a"], *pool_case(c, sl, ln))
+    assert gla.gla_check_device_error() == _lib.GLA_ERR_INVALID_ARG
+    assert bool((o[[1, 3]] == 0).all()) and bool((o[[0, 2, 4]] != 0).any(-1).all())
+    assert torch.equal(c.codes, before)
+
+
+@pytest.mark.gpu
 def test_cache_on_another_stream_and_in_a_graph(lib):
     """A captured step reads lengths and slots from the device, so a replay advances with them."""
     mk = lambda: fill_pool(6, 2, 64, 128, 4, "int8", torch.bfloat16, seed=8)  # noqa: E731
