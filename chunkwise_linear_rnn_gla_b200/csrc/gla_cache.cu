@@ -637,7 +637,7 @@ __global__ void __launch_bounds__(kStreamThreads, 1)
                     const bool named = slot >= 0, good = slot < c.slots && len >= 0;
                     if (named && !good && blockIdx.x == 0) atomicOr(err, kErrBadRow);
                     const int n = named && good ? len % c.W : kDead;
-                    row_slot[b] = n == kDead ? -1 : slot;
+                    row_slot[b] = slot;  // a row that is refused names its slot all the same
                     row_n[b] = uint8_t(n);
                     fold[u] = n == c.W - 1;
                 } else row_slot[b] = -1;

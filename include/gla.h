@@ -318,6 +318,8 @@ gla_status gla_gsa_bwd(const gla_desc* d, int32_t slots, const void* q, const vo
  *     hT = h0 and dh0 = dhT. The values are not checked on the host; whatever
  *     they hold, no access leaves the tensors.
  *   h0, hT, dhT, dh0          [B, H, D] fp32 (nullable)
+ * Sizes: L <= 2^30, B <= 2^22, H <= 65535, D <= 2^20 and (sequences or, packed,
+ * heads) x D <= 2^30 (GLA_ERR_UNSUPPORTED beyond).
  * Sums and states are fp32; only h and dx are rounded to dtype. The result does
  * not depend on how the sequences are packed beyond the rounding of the joins.
  *
@@ -350,7 +352,7 @@ gla_status gla_scan_bwd(const gla_desc* d, int32_t write, const void* x, const f
  * (pool >= B). A negative slot marks a padding row: its h is 0 and no state is
  * touched. A slot >= pool, or one that an earlier row of the call names too, is
  * refused: that row is treated as padding and gla_check_device_error reports
- * GLA_ERR_INVALID_ARG. d->L is ignored. */
+ * GLA_ERR_INVALID_ARG. d->L is ignored; B <= 65535. */
 gla_status gla_scan_step(const gla_desc* d, int32_t write, const void* x, const float* log_a, const int32_t* slots,
                          int64_t pool, float* state, void* h, void* stream);
 
@@ -394,7 +396,8 @@ gla_status gla_scan_step(const gla_desc* d, int32_t write, const void* x, const 
  * gate_tau (gla_cache_step; all kinds, stored as per-channel log a) and flags
  * (GLA_FLAG_CHECKS); L is ignored, the other fields as for the scan. window is
  * 1 .. 64; GLA_ERR_UNSUPPORTED when a head's window does not fit on chip
- * (4 * window * (Dk + 128) + 16 Dk + 8192 bytes above 200 KB). */
+ * (4 * window * (Dk + 128) + 16 Dk + 8192 bytes above 200 KB), and beyond B = 2^22,
+ * H = 65535 or B H ceil(Dv / 128) ceil(Dk / 64) = 2^30. */
 typedef enum gla_cache_format {
     GLA_CACHE_INT8 = 0,
     GLA_CACHE_E4M3 = 1
