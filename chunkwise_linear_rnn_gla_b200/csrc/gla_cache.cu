@@ -421,7 +421,8 @@ __global__ void __launch_bounds__(kThreads, 4) k_cache_step(Pool c, const T* __r
     float* vs = kt + c.W * ld;         // [W][128]
     float* decay = vs + c.W * kG;      // [ld]
     float* wq = decay + ld;            // [ld] q e^G scale
-    float* p = wq + ld;                // [64] scores
+    float* sc = wq + ld;               // [ld] scale
+    float* p = sc + ld;                // [64] scores
     float* red = p + 64;               // [8][128]
     uint32_t x[PASS][kBatch];
     const auto fetch = [&](int r0) {
@@ -436,8 +437,11 @@ __global__ void __launch_bounds__(kThreads, 4) k_cache_step(Pool c, const T* __r
     fetch(0);
     window_keys<T, true>(c, sh, bh, n, 0, c.K, ld, k, ga, grp == 0, kt, decay);
     window_values<T, true, VEC>(c, sh, bh, n, grp, v, vs);
-    for (int r = tid; r < ld; r += kThreads)
-        wq[r] = r < c.K ? ldf(q + bh * c.K + r) * decay[r] * scale[int64_t(r) * c.NG] : 0.f;
+    for (int r = tid; r < ld; r += kThreads) {
+        const float f = r < c.K ? scale[int64_t(r) * c.NG] : 0.f;
+        sc[r] = f;
+        wq[r] = r < c.K ? ldf(q + bh * c.K + r) * decay[r] * f : 0.f;
+    }
     __syncthreads();
     for (int j = warp; j < used; j += kWarps) {
         float s = 0.f;
@@ -482,16 +486,12 @@ __global__ void __launch_bounds__(kThreads, 4) k_cache_step(Pool c, const T* __r
     // the window is full: round the state back
     for (int r = warp * kBatch; r < c.K; r += kWarps * kBatch) {
         uint32_t z[kBatch];
-        float sc[kBatch], y[kBatch][4];
+        float y[kBatch][4];
 #pragma unroll
-        for (int i = 0; i < kBatch; ++i) {
-            const int ri = r + i < c.K ? r + i : c.K - 1;
-            z[i] = cols.codes(codes + int64_t(ri) * c.V);
-            sc[i] = scale[int64_t(ri) * c.NG];
-        }
-        form_rows<INT8>(z, sc, decay + r, kt + r, ld, used, [&](int j, float2* t) { cols.pairs(vs + j * kG, t); }, y);
+        for (int i = 0; i < kBatch; ++i) z[i] = cols.codes(codes + int64_t(r + i < c.K ? r + i : c.K - 1) * c.V);
+        form_rows<INT8>(z, sc + r, decay + r, kt + r, ld, used, [&](int j, float2* t) { cols.pairs(vs + j * kG, t); }, y);
         put_rows<INT8>(cols, y, c.K - r < kBatch ? c.K - r : kBatch, c.codes + (sh * c.K + r) * c.V, c.V,
-                            scale + int64_t(r) * c.NG, c.NG);
+                       scale + int64_t(r) * c.NG, c.NG);
     }
 }
 
@@ -1023,7 +1023,7 @@ Pool pool_of(const CacheProblem& p) {
 
 size_t step_smem(const CacheProblem& p) {
     const size_t ld = size_t(round_up(int(p.K), kBatch));
-    return sizeof(float) * (size_t(p.c.window) * (ld + kG) + 2 * ld + 64 + kWarps * kG);
+    return sizeof(float) * (size_t(p.c.window) * (ld + kG) + 3 * ld + 64 + kWarps * kG);
 }
 size_t load_smem(const CacheProblem& p) {
     return sizeof(float) * (size_t(p.c.window) * (kLoadRows + kG) + 2 * kLoadRows);
