@@ -62,14 +62,18 @@ def _need(t, name, shape, dtype, dev):
         raise ValueError("%s must be contiguous" % name)
 
 
+_Tensor = torch.Tensor
+
+
 def _same(t, name, shape, dtype, dev):
     """_need with a quick way through for the usual case (shape: a tuple or torch.Size)."""
-    if not (isinstance(t, torch.Tensor) and t.shape == shape and t.dtype is dtype and t.device == dev
+    if not (t.__class__ is _Tensor and t.shape == shape and t.dtype is dtype and t.device == dev
             and t.is_contiguous()):
         _need(t, name, shape, dtype, dev)
 
 
-# the current stream's handle without a Stream object around it, where torch offers that
+# the current device, and the current stream's handle without a Stream object around it, where torch offers that
+_current_device = getattr(torch._C, "_cuda_getDevice", None) or torch.cuda.current_device
 _raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None) or (lambda i: torch.cuda.current_stream(i).cuda_stream)
 
 
@@ -78,7 +82,7 @@ def _enqueue(dev: torch.device, what: str, fn, *args):
     microseconds of device time, so the device is switched only where another one is current."""
     if dev.type != "cuda":
         raise ValueError("%s needs CUDA tensors, got %s" % (what, dev))
-    if dev.index == torch.cuda.current_device():
+    if dev.index == _current_device():
         st = fn(*args, _raw_stream(dev.index))
     else:
         with torch.cuda.device(dev):

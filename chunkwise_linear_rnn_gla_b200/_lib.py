@@ -147,6 +147,8 @@ def _declare(lib):
 def load(path: str = LIB_PATH):
     """Load libgla.so (raises if it has not been built)."""
     global _lib
+    if _lib is not None:
+        return _lib
     with _lock:
         if _lib is None:
             if not os.path.exists(path):

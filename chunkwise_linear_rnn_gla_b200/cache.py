@@ -135,7 +135,8 @@ def cache_load(cache, slots, lengths=None, S=None, *, checks=False):
     dev = cache.device
     if S is None:
         S = torch.empty(B, cache.H, cache.Dk, cache.Dv, dtype=torch.float32, device=dev)
-    _same(S, "S", (B, cache.H, cache.Dk, cache.Dv), torch.float32, dev)
+    else:
+        _same(S, "S", (B, cache.H, cache.Dk, cache.Dv), torch.float32, dev)
     desc = cache._desc(B, checks=checks)
     _enqueue(dev, "gla_cache_load", lib.gla_cache_load, desc, cache._ref, slots.data_ptr(),
              None if lengths is None else lengths.data_ptr(), S.data_ptr())
@@ -158,7 +159,8 @@ def cache_step(cache, q, k, v, log_a, slots, lengths, o=None, *, gate="channel",
     _same(log_a, "log_a", gate_shape(gate, B, H, None, Dk), torch.float32, dev)
     if o is None:
         o = torch.empty(B, H, Dv, dtype=dt, device=dev)
-    _same(o, "o", (B, H, Dv), dt, dev)
+    else:
+        _same(o, "o", (B, H, Dv), dt, dev)
     _enqueue(dev, "gla_cache_step", lib.gla_cache_step, desc, cache._ref, q.data_ptr(), k.data_ptr(), v.data_ptr(),
              log_a.data_ptr(), slots.data_ptr(), lengths.data_ptr(), o.data_ptr())
     _finish(dev, checks, "gla_cache_step")

@@ -112,10 +112,10 @@ def scan_fwd(x, log_a, h0=None, *, cu_seqlens=None, write="input", gate="channel
         _same(h0, "h0", (B, H, D), torch.float32, dev)
     desc = _desc(x, B, H, L, D, gate, tau, _flags(checks))
     h = _buffer(h, x, "h", cu_seqlens is not None)
-    if hT is None and want_hT:
-        hT = torch.empty(B, H, D, dtype=torch.float32, device=dev)
     if hT is not None:
         _same(hT, "hT", (B, H, D), torch.float32, dev)
+    elif want_hT:
+        hT = torch.empty(B, H, D, dtype=torch.float32, device=dev)
     ws, nbytes = None, 0
     if workspace is not None:
         ws, nbytes = _workspace(lib.gla_scan_workspace_size(desc, cu_seqlens is not None), dev, workspace)
@@ -147,10 +147,10 @@ def scan_bwd(x, log_a, dh, h0=None, dhT=None, *, cu_seqlens=None, write="input",
     dx = _buffer(out.get("dx"), x, "dx", packed)
     dla = _buffer(out.get("dlog_a"), log_a, "dlog_a", packed)
     dh0 = out.get("dh0")
-    if dh0 is None and want_dh0:
-        dh0 = torch.empty(B, H, D, dtype=torch.float32, device=dev)
     if dh0 is not None:
         _same(dh0, "dh0", (B, H, D), torch.float32, dev)
+    elif want_dh0:
+        dh0 = torch.empty(B, H, D, dtype=torch.float32, device=dev)
     ws, nbytes = _workspace(lib.gla_scan_workspace_size(desc, packed), dev, workspace)
     _enqueue(dev, "gla_scan_bwd", lib.gla_scan_bwd, desc, _write(write), x.data_ptr(), log_a.data_ptr(),
              _addr(cu_seqlens), _addr(h0), dh.data_ptr(), _addr(dhT), dx.data_ptr(), dla.data_ptr(), _addr(dh0),
@@ -167,10 +167,11 @@ def scan_step(x, log_a, state, slots=None, *, write="input", gate="channel", tau
     lib = load()
     if not isinstance(x, torch.Tensor) or x.dim() != 3:
         raise ValueError("x must be a [B, H, D] tensor")
-    dev = x.device
-    B, H, D = x.shape
-    _same(x, "x", x.shape, x.dtype, dev)
-    _same(log_a, "log_a", x.shape, torch.float32, dev)
+    if not x.is_contiguous():
+        raise ValueError("x must be contiguous")
+    dev, shape = x.device, x.shape
+    B, H, D = shape
+    _same(log_a, "log_a", shape, torch.float32, dev)
     if not isinstance(state, torch.Tensor) or state.dim() != 3:
         raise ValueError("state must be a [pool, H, D] tensor")
     _same(state, "state", (state.shape[0], H, D), torch.float32, dev)
@@ -180,7 +181,8 @@ def scan_step(x, log_a, state, slots=None, *, write="input", gate="channel", tau
         raise ValueError("state has %d entries for %d rows" % (state.shape[0], B))
     if h is None:
         h = torch.empty_like(x)
-    _same(h, "h", x.shape, x.dtype, dev)
+    else:
+        _same(h, "h", shape, x.dtype, dev)
     desc = _desc(x, B, H, 1, D, gate, tau, _flags(checks))
     _enqueue(dev, "gla_scan_step", lib.gla_scan_step, desc, _write(write), x.data_ptr(), log_a.data_ptr(),
              _addr(slots), state.shape[0], state.data_ptr(), h.data_ptr())
