@@ -14,7 +14,7 @@
 // no flags in memory and no second launch, and its result does not depend on timing.
 //
 // Floor: 8 (bf16) or 12 (fp32) bytes an element forward, 14 or 20 backward, at the copy bandwidth. Measured (device time,
-// inputs larger than L2 in turn): forward 33.2 us at 8 sequences of 2048 steps, width 1024 (134 MB, 4.0 TB/s, floor
+// inputs larger than L2 in turn): forward 33.4 us at 8 sequences of 2048 steps, width 1024 (134 MB, 4.0 TB/s, floor
 // 20.5); forward and backward 101 us at 4 x 2048, width 2048, gate from its pre-activation (369 MB moved, floor 57).
 // What is left over the floor is issue slots (37 instructions an element forward, 70 backward, 60% of the slots taken)
 // and the chain of a round: gates, maps, the exchange, steps. Without its loads the forward still takes 32 us.
