@@ -473,3 +473,11 @@ def test_scan_binding_refuses(lib):
                        torch.zeros(3, dtype=torch.int32))
     with pytest.raises(ValueError):
         scan.scan_fwd(x, z, write="add")
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("N", [255, 256, 257, 700])  # on both sides of a power of two, for the search of a row's sequence
+def test_scan_packed_many_sequences(lib, N):
+    g = torch.Generator().manual_seed(N)
+    cu = [2] + (2 + torch.randint(0, 4, (N,), generator=g).cumsum(0)).tolist()  # some empty, rows in front and behind
+    check(make(1, 1, cu[-1] + 5, 34, torch.float32, "channel", cu=cu, seed=N), cu, "leak", "channel")
