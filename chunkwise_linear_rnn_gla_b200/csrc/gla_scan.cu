@@ -170,28 +170,53 @@ __global__ void __launch_bounds__(kStepThreads) k_scan_step(ScanProblem p, const
     stf(h + b * n + c, y);
 }
 
-constexpr int kFwdRows = 8;
-
-template <typename T, int VEC, bool PACKED, bool PREACT, bool LEAK, int WARPS>
-gla_status fwd_launch(const ScanProblem& p, const void* x, const float* la, const int32_t* cu, const float* h0,
-                      void* h, float* hT, float* seg, cudaStream_t s) {
+// One form of the forward kernel and how a call would run on it.
+template <typename T, int VEC, bool PACKED, bool PREACT, bool LEAK, int WARPS, int ROWS>
+struct FwdForm {
     using V = typename VecOf<VEC>::type;
-    constexpr int threads = WARPS * 32, stages = WARPS * kFwdStage<T, VEC, kFwdRows>;
-    const int64_t groups = (PACKED ? p.H : p.B * p.H) * cdiv(p.D, 32 * VEC);
-    const auto kernel = k_scan_fwd<T, VEC, PACKED, PREACT, LEAK, WARPS, kFwdRows>;
-    static FitOnce once;
-    const ClusterFit fit = cluster_fit(once, kernel, threads, smem_of<V>, stages);
-    const int cl = cluster_size(fit, groups, p.L, WARPS * kFwdRows);
-    return launch_clusters("scan_fwd", kernel, fit, groups, cl, threads, smem_of<V>(cl, stages), s, p, cl,
-                           static_cast<const T*>(x), la, cu, h0, static_cast<T*>(h), hT, seg, device_error_word());
+    static constexpr int threads = WARPS * 32, stages = WARPS * kFwdStage<T, VEC, ROWS>;
+    ClusterFit fit;
+    int64_t groups;
+    ClusterPlan plan;
+    static auto kernel() { return k_scan_fwd<T, VEC, PACKED, PREACT, LEAK, WARPS, ROWS>; }
+    FwdForm(const ScanProblem& p, int64_t groups_) : groups(groups_) {
+        static FitOnce once;
+        fit = cluster_fit(once, kernel(), threads, smem_of<V>, stages);
+        plan = cluster_plan(fit, groups, p.L, WARPS * ROWS);
+    }
+    gla_status launch(const ScanProblem& p, const void* x, const float* la, const int32_t* cu, const float* h0, void* h,
+                      float* hT, float* seg, cudaStream_t s) const {
+        return launch_clusters("scan_fwd", kernel(), fit, groups, plan.size, threads, smem_of<V>(plan.size, stages), s, p,
+                               plan.size, static_cast<const T*>(x), la, cu, h0, static_cast<T*>(h), hT, seg,
+                               device_error_word());
+    }
+};
+
+// Rows a warp: 8, or 16 where they save rounds. A round of 16 takes 1.6 to 1.75 times as long as one of 8 (its exchange,
+// lookups and barriers are paid once), and its stages leave room for fewer blocks, which the plan's waves count. One
+// sequence of 16384 steps, width 64: 28.7 us against 35.6; 8000 steps, width 1001: 36.2 against 42.8; but 91 against 64 at
+// 16384 steps, width 1024, where half the clusters wait for a second wave, and 4.7 against 3.7 at 256 steps, width 64.
+// Two channels a lane in blocks of four warps fill an SM with 8 rows already (33 us against 40 at 8 sequences of 2048
+// steps, width 1024).
+template <typename T, int VEC, bool PACKED, bool PREACT, bool LEAK, int WARPS>
+gla_status fwd_rows(const ScanProblem& p, int64_t groups, const void* x, const float* la, const int32_t* cu,
+                    const float* h0, void* h, float* hT, float* seg, cudaStream_t s) {
+    const FwdForm<T, VEC, PACKED, PREACT, LEAK, WARPS, 8> few(p, groups);
+    if constexpr (VEC == 1 || WARPS == 8) {
+        if (few.plan.cost > 1) {
+            const FwdForm<T, VEC, PACKED, PREACT, LEAK, WARPS, 16> many(p, groups);
+            if (many.plan.cost * 7 <= few.plan.cost * 4) return many.launch(p, x, la, cu, h0, h, hT, seg, s);
+        }
+    }
+    return few.launch(p, x, la, cu, h0, h, hT, seg, s);
 }
 
 template <typename T, int VEC, bool PACKED, bool PREACT, bool LEAK>
 gla_status fwd_typed(const ScanProblem& p, const void* x, const float* la, const int32_t* cu, const float* h0,
                      void* h, float* hT, float* seg, cudaStream_t s) {
     const int64_t groups = (PACKED ? p.H : p.B * p.H) * cdiv(p.D, 32 * VEC);
-    if (many_groups(groups)) return fwd_launch<T, VEC, PACKED, PREACT, LEAK, 4>(p, x, la, cu, h0, h, hT, seg, s);
-    return fwd_launch<T, VEC, PACKED, PREACT, LEAK, 8>(p, x, la, cu, h0, h, hT, seg, s);
+    if (many_groups(groups)) return fwd_rows<T, VEC, PACKED, PREACT, LEAK, 4>(p, groups, x, la, cu, h0, h, hT, seg, s);
+    return fwd_rows<T, VEC, PACKED, PREACT, LEAK, 8>(p, groups, x, la, cu, h0, h, hT, seg, s);
 }
 
 template <typename T>

@@ -6,9 +6,9 @@
 // A step is the affine map s -> a s + b, and maps compose: (a2, b2) o (a1, b1) = (a1 a2, a2 b1 + b2). So a
 // sequence is cut into segments that are reduced to one map each, the maps are joined, and every segment
 // then runs its steps from the state that enters it. All of this happens on one read of the inputs:
-//   warp     8 rows (steps) x 32 or 64 channels in registers, one or two channels a lane;
-//   block    4 or 8 warps, 32 or 64 rows: the warps' maps are joined in shared memory;
-//   cluster  up to 16 blocks, 512 or 1024 rows: every block sends its map into the shared memory of all the others
+//   warp     8 or 16 rows (steps) x 32 or 64 channels in registers, one or two channels a lane;
+//   block    4 or 8 warps, 32 to 128 rows: the warps' maps are joined in shared memory;
+//   cluster  up to 16 blocks, 512 to 2048 rows: every block sends its map into the shared memory of all the others
 //            (asynchronous stores counted on their mbarriers), and each joins those in front of it.
 // A cluster walks the time axis in rounds and carries the state in registers, so a call needs no workspace,
 // no flags in memory and no second launch, and its result does not depend on timing.
@@ -459,22 +459,25 @@ ClusterFit cluster_fit(FitOnce& once, K kernel, int threads, size_t (*smem)(int,
 }
 
 // Blocks per cluster. A block's time goes by its rounds, and clusters that do not fit at once run in further waves:
-// the least waves x rounds, and of those the smallest cluster.
-int cluster_size(const ClusterFit& f, int64_t groups, int64_t L, int tile) {
+// the least waves x rounds (cost), and of those the smallest cluster.
+struct ClusterPlan {
+    int size;
+    int64_t cost;
+};
+ClusterPlan cluster_plan(const ClusterFit& f, int64_t groups, int64_t L, int tile) {
     const int64_t tiles = cdiv(L, tile);
-    int best = 1;
-    int64_t cost = INT64_MAX;
+    ClusterPlan best{1, INT64_MAX / 8};
     for (int cl = 1; cl <= kMaxCluster; ++cl) {
         if (f.fit[cl] < 1 || cl > tiles) continue;
         const int64_t c = cdiv(groups, int64_t(f.fit[cl])) * cdiv(tiles, int64_t(cl));
-        if (c < cost) cost = c, best = cl;
+        if (c < best.cost) best = ClusterPlan{cl, c};
     }
     return best;
 }
 
 // Blocks of four warps where there are channel tiles and sequences for a quarter of the SMs: more blocks that wait at
 // different times (forward 33.3 us against 35.6 at 8 sequences of 2048 steps, width 1024). Else of eight, whose rounds
-// cover twice the rows (29 us against 43 at one sequence of 16384 steps, width 64).
+// cover twice the rows (29 us against 43 at one sequence of 16384 steps, width 64, 8 rows a warp).
 inline bool many_groups(int64_t groups) { return groups * 4 >= 148; }
 
 template <typename K, typename... Args>

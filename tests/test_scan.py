@@ -481,3 +481,22 @@ def test_scan_packed_many_sequences(lib, N):
     g = torch.Generator().manual_seed(N)
     cu = [2] + (2 + torch.randint(0, 4, (N,), generator=g).cumsum(0)).tolist()  # some empty, rows in front and behind
     check(make(1, 1, cu[-1] + 5, 34, torch.float32, "channel", cu=cu, seed=N), cu, "leak", "channel")
+
+
+# several rounds with sixteen rows a warp: one and two channels a lane, blocks of four warps and of eight, a ragged end
+LONG = [(1, 1, 2077, 64), (1, 2, 4100, 33), (3, 7, 1100, 71), (1, 40, 1500, 37)]
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("dtype", [torch.float32, torch.bfloat16])
+@pytest.mark.parametrize("shape", LONG)
+def test_scan_long_dense(lib, shape, dtype):
+    check(make(*shape, dtype, "preact", seed=sum(shape)), None, "leak", "preact")
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("dtype", [torch.float32, torch.bfloat16])
+@pytest.mark.parametrize("H,D", [(1, 64), (2, 33), (40, 37)])
+def test_scan_long_packed(lib, H, D, dtype):
+    cu = [3, 15, 16, 16, 17, 31, 33, 900, 1057, 1057, 1999, 2060]
+    check(make(1, H, 2077, D, dtype, "channel", cu=cu, seed=H + D), cu, "input", "channel")
