@@ -1016,6 +1016,10 @@ __global__ void __launch_bounds__(kStreamThreads, 1)
     }
 }
 
+// The most shared memory that a block of the kernels without a ring takes: cache_supported admits the windows and widths
+// whose step (step_smem) stays below it, and a load takes at most 66,560 bytes (64 tokens).
+constexpr size_t kHeadSmem = 200 * 1024;
+
 Pool pool_of(const CacheProblem& p) {
     return Pool{static_cast<uint8_t*>(p.c.codes), p.c.scale, p.c.k, p.c.v, p.c.log_a, p.c.slots, p.c.window,
                 p.H, int(p.K), int(p.V), int(cdiv(p.V, kG))};
@@ -1029,10 +1033,13 @@ size_t load_smem(const CacheProblem& p) {
     return sizeof(float) * (size_t(p.c.window) * (kLoadRows + kG) + 2 * kLoadRows);
 }
 
+// The attribute belongs to the kernel, which other host threads may be about to launch with another window or width: so
+// every call above the default of 48 KB asks for `most`, the largest size that any call of the kernel may take, and none
+// lowers the limit under another's launch.
 template <typename K>
-bool allow_smem(K kernel, size_t bytes) {
-    return bytes <= 48 * 1024 ||
-           cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, int(bytes)) == cudaSuccess;
+bool allow_smem(K kernel, size_t bytes, size_t most) {
+    return bytes <= 48 * 1024 || (bytes <= most && cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                                                        int(most)) == cudaSuccess);
 }
 
 template <bool INT8, bool VEC>
@@ -1049,7 +1056,7 @@ gla_status load_typed(const CacheProblem& p, const int32_t* slots, const int32_t
     const Pool c = pool_of(p);
     const int parts = int(cdiv(p.K, kLoadRows));
     const size_t smem = load_smem(p);
-    if (!allow_smem(k_cache_load<T, INT8, VEC>, smem)) return GLA_ERR_CUDA;
+    if (!allow_smem(k_cache_load<T, INT8, VEC>, smem, kHeadSmem)) return GLA_ERR_CUDA;
     GLA_LAUNCH("cache_load", (k_cache_load<T, INT8, VEC>), unsigned(p.B * p.H * c.NG * parts), kThreads, smem, s, c,
                parts, slots, lengths, S, device_error_word());
     return GLA_OK;
@@ -1061,7 +1068,7 @@ gla_status step_typed(const CacheProblem& p, const void* q, const void* k, const
     const Pool c = pool_of(p);
     const GateArgs ga{la, p.gate, p.inv_tau, p.H};
     const size_t smem = step_smem(p);
-    if (!allow_smem(k_cache_step<T, INT8, VEC>, smem)) return GLA_ERR_CUDA;
+    if (!allow_smem(k_cache_step<T, INT8, VEC>, smem, kHeadSmem)) return GLA_ERR_CUDA;
     GLA_LAUNCH("cache_step", (k_cache_step<T, INT8, VEC>), unsigned(p.B * p.H * c.NG), kThreads, smem, s, c,
                static_cast<const T*>(q), static_cast<const T*>(k), static_cast<const T*>(v), ga, slots, lengths,
                static_cast<T*>(o), device_error_word());
@@ -1118,7 +1125,7 @@ gla_status stream_typed(const CacheProblem& p, const StreamPlan& pl, const void*
                         const float* la, const int32_t* slots, const int32_t* lengths, void* o, cudaStream_t s) {
     const Pool c = pool_of(p);
     const GateArgs ga{la, p.gate, p.inv_tau, p.H};
-    if (!allow_smem(k_cache_stream<T, INT8>, pl.smem)) return GLA_ERR_CUDA;
+    if (!allow_smem(k_cache_stream<T, INT8>, pl.smem, kStreamSmem)) return GLA_ERR_CUDA;
     const int64_t fit = (int64_t(1) << 24) / (p.H * c.NG), step = fit < kMaxRows ? fit : kMaxRows;  // rows a launch
     for (int64_t b0 = 0; b0 < p.B; b0 += step) {
         const int n = int(p.B - b0 < step ? p.B - b0 : step);
@@ -1140,7 +1147,7 @@ gla_status stream_typed(const CacheProblem& p, const StreamPlan& pl, const void*
 bool cache_supported(const CacheProblem& p) {
     if (p.B > (1 << 22) || p.H > 65535 || p.K > 65536 || p.V > 65536) return false;
     if (p.B * p.H * cdiv(p.V, kG) * cdiv(p.K, kWarps * kBatch) > (int64_t(1) << 30)) return false;
-    return 4 * size_t(p.c.window) * (p.K + kG) + 16 * p.K + 8192 <= 200 * 1024;
+    return 4 * size_t(p.c.window) * (p.K + kG) + 16 * p.K + 8192 <= kHeadSmem;
 }
 
 gla_status cache_store(const CacheProblem& p, const float* S, const int32_t* slots, cudaStream_t s) {

@@ -186,9 +186,8 @@ struct FwdForm {
     }
     gla_status launch(const ScanProblem& p, const void* x, const float* la, const int32_t* cu, const float* h0, void* h,
                       float* hT, float* seg, cudaStream_t s) const {
-        return launch_clusters("scan_fwd", kernel(), fit, groups, plan.size, threads, smem_of<V>(plan.size, stages), s, p,
-                               plan.size, static_cast<const T*>(x), la, cu, h0, static_cast<T*>(h), hT, seg,
-                               device_error_word());
+        return launch_clusters("scan_fwd", kernel(), fit, groups, plan.size, threads, smem_of<V>, stages, s, p, plan.size,
+                               static_cast<const T*>(x), la, cu, h0, static_cast<T*>(h), hT, seg, device_error_word());
     }
 };
 

@@ -411,7 +411,9 @@ size_t smem_of(int cl, int stages_bytes) {
     return (cl > 1 ? size_t(2) * cl * 32 * sizeof(Map<V>) : 0) + size_t(2) * stages_bytes;
 }
 
-// What a launch with clusters of up to kMaxCluster blocks needs of the kernel, on the current device.
+// What a launch with clusters of up to kMaxCluster blocks needs of the kernel, on the current device. The attributes
+// belong to the kernel, which other host threads may be about to launch, so `smem` is always what the largest cluster
+// takes: no call lowers the limit under another's launch. (How many blocks an SM holds follows the launch's own size.)
 template <typename K>
 bool allow_clusters(K kernel, size_t smem) {
     return cudaFuncSetAttribute(kernel, cudaFuncAttributeNonPortableClusterSizeAllowed, 1) == cudaSuccess &&
@@ -481,15 +483,15 @@ ClusterPlan cluster_plan(const ClusterFit& f, int64_t groups, int64_t L, int til
 inline bool many_groups(int64_t groups) { return groups * 4 >= 148; }
 
 template <typename K, typename... Args>
-gla_status launch_clusters(const char* name, K kernel, const ClusterFit& f, int64_t groups, int cl, int threads, size_t smem,
-                           cudaStream_t s, Args... args) {
-    if (f.fit[1] < 1 || !allow_clusters(kernel, smem)) return GLA_ERR_CUDA;
+gla_status launch_clusters(const char* name, K kernel, const ClusterFit& f, int64_t groups, int cl, int threads,
+                           size_t (*smem)(int, int), int stages_bytes, cudaStream_t s, Args... args) {
+    if (f.fit[1] < 1 || !allow_clusters(kernel, smem(kMaxCluster, stages_bytes))) return GLA_ERR_CUDA;
     if (groups * cl > (int64_t(1) << 31) - 1) return GLA_ERR_UNSUPPORTED;
     launch_begin(name, s);
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3(unsigned(groups * cl));
     cfg.blockDim = dim3(unsigned(threads));
-    cfg.dynamicSmemBytes = smem;
+    cfg.dynamicSmemBytes = smem(cl, stages_bytes);
     cfg.stream = s;
     cudaLaunchAttribute attr[1];
     attr[0].id = cudaLaunchAttributeClusterDimension;

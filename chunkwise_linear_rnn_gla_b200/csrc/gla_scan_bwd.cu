@@ -169,7 +169,7 @@ gla_status bwd_launch(const ScanProblem& p, const void* x, const float* la, cons
     static FitOnce once;
     const ClusterFit fit = cluster_fit(once, kernel, threads, smem_of<V>, stages);
     const int cl = cluster_plan(fit, groups, p.L, WARPS * kBwdRows).size;
-    return launch_clusters("scan_bwd", kernel, fit, groups, cl, threads, smem_of<V>(cl, stages), s, p, cl,
+    return launch_clusters("scan_bwd", kernel, fit, groups, cl, threads, smem_of<V>, stages, s, p, cl,
                            static_cast<const T*>(x), la, cu, h0, static_cast<const T*>(dh), dhT, static_cast<T*>(dx),
                            dla, dh0, seg, device_error_word());
 }
