@@ -318,6 +318,16 @@ bool scan_checks(const gla::ScanProblem& p) {
     return gla::checks_on(f);
 }
 
+// What checking mode looks at of a tensor with `per_row` elements a row: rows of packed sequences, rows with a slot.
+gla::CheckedRows packed_rows(const gla::ScanProblem& p, const int32_t* cu) {
+    if (!cu) return {};
+    return {gla::CheckedRows::kPacked, cu, p.D, p.L, p.B};
+}
+gla::CheckedRows slot_rows(const int32_t* slots, int64_t per_row, int64_t pool) {
+    if (!slots) return {};
+    return {gla::CheckedRows::kSlots, slots, per_row, 1, pool};
+}
+
 bool aligned4(const void* p) { return aligned(p, 4); }
 
 gla_status resolve_cache(const gla_desc* d, const gla_cache* c, gla::CacheProblem& p) {
@@ -779,15 +789,15 @@ gla_status gla_scan_fwd(const gla_desc* d, int32_t write, const void* x, const f
     }
     cudaStream_t s = static_cast<cudaStream_t>(stream);
     const bool chk = scan_checks(p);
-    const int64_t rows = (p.packed ? p.H : p.B * p.H) * p.L;
+    const int64_t n = (p.packed ? p.H : p.B * p.H) * p.L * p.D;
+    const gla::CheckedRows rows = packed_rows(p, cu_seqlens);
     if (chk) {
-        if (!p.preact && (st = gla::check_gates(log_a, rows * p.D, s)) != GLA_OK) return st;
+        if (!p.preact && (st = gla::check_gates(log_a, n, s, rows)) != GLA_OK) return st;
         if (workspace && (st = gla::guards_fill(a, s)) != GLA_OK) return st;
     }
     st = gla::scan_fwd(p, x, log_a, cu_seqlens, h0, h, hT, seg, s);
     if (st != GLA_OK || !chk) return st;
-    // a packed h has rows that belong to no sequence and hold whatever the caller left there
-    if (!p.packed) st = gla::check_finite(h, rows * p.D, p.bf16, s);
+    st = gla::check_finite(h, n, p.bf16, s, rows);
     if (st == GLA_OK) st = gla::check_finite(hT, p.B * p.H * p.D, false, s);
     if (st == GLA_OK && workspace) st = gla::guards_check(a, s);
     return st;
@@ -812,18 +822,17 @@ gla_status gla_scan_bwd(const gla_desc* d, int32_t write, const void* x, const f
     if ((st = check_ws(workspace, workspace_bytes, gla::scan_workspace(p, a))) != GLA_OK) return st;
     cudaStream_t s = static_cast<cudaStream_t>(stream);
     const bool chk = scan_checks(p);
-    const int64_t rows = (p.packed ? p.H : p.B * p.H) * p.L;
+    const int64_t n = (p.packed ? p.H : p.B * p.H) * p.L * p.D;
+    const gla::CheckedRows rows = packed_rows(p, cu_seqlens);
     if (chk) {
-        if (!p.preact && (st = gla::check_gates(log_a, rows * p.D, s)) != GLA_OK) return st;
+        if (!p.preact && (st = gla::check_gates(log_a, n, s, rows)) != GLA_OK) return st;
         if ((st = gla::guards_fill(a, s)) != GLA_OK) return st;
     }
     st = gla::scan_bwd(p, x, log_a, cu_seqlens, h0, dh, dhT, dx, dlog_a, dh0, static_cast<float*>(workspace),
                        (p.flags & GLA_FLAG_WS_FROM_FWD) != 0, s);
     if (st != GLA_OK || !chk) return st;
-    if (!p.packed) {
-        st = gla::check_finite(dx, rows * p.D, p.bf16, s);
-        if (st == GLA_OK) st = gla::check_finite(dlog_a, rows * p.D, false, s);
-    }
+    st = gla::check_finite(dx, n, p.bf16, s, rows);
+    if (st == GLA_OK) st = gla::check_finite(dlog_a, n, false, s, rows);
     if (st == GLA_OK) st = gla::check_finite(dh0, p.B * p.H * p.D, false, s);
     if (st == GLA_OK) st = gla::guards_check(a, s);
     return st;
@@ -844,7 +853,7 @@ gla_status gla_scan_step(const gla_desc* d, int32_t write, const void* x, const 
     cudaStream_t s = static_cast<cudaStream_t>(stream);
     const bool chk = scan_checks(p);
     const int64_t n = p.B * p.H * p.D;
-    if (chk && !p.preact && (st = gla::check_gates(log_a, n, s)) != GLA_OK) return st;
+    if (chk && !p.preact && (st = gla::check_gates(log_a, n, s, slot_rows(slots, p.H * p.D, pool))) != GLA_OK) return st;
     st = gla::scan_step(p, x, log_a, slots, pool, state, h, s);
     if (st != GLA_OK || !chk) return st;
     return gla::check_finite(h, n, p.bf16, s);
@@ -861,7 +870,9 @@ gla_status gla_cache_store(const gla_desc* d, const gla_cache* c, const float* S
     GLA_REQUIRE_PTR(S);
     if (!slots || !aligned4(slots)) return GLA_ERR_INVALID_ARG;
     cudaStream_t s = static_cast<cudaStream_t>(stream);
-    if (cache_checks(d) && (st = gla::check_finite(S, p.B * p.H * p.K * p.V, false, s)) != GLA_OK) return st;
+    if (cache_checks(d) && (st = gla::check_finite(S, p.B * p.H * p.K * p.V, false, s,
+                                                   slot_rows(slots, p.H * p.K * p.V, c->slots))) != GLA_OK)
+        return st;
     return gla::cache_store(p, S, slots, s);
 }
 
@@ -904,8 +915,10 @@ gla_status gla_cache_step(const gla_desc* d, const gla_cache* c, const void* q, 
     cudaStream_t s = static_cast<cudaStream_t>(stream);
     const bool chk = cache_checks(d);
     if (chk && d->gate != GLA_GATE_PREACT) {
-        const int64_t n = d->gate == GLA_GATE_HEAD ? p.H : p.B * p.H * (d->gate == GLA_GATE_SCALAR ? 1 : p.K);
-        if ((st = gla::check_gates(log_a, n, s)) != GLA_OK) return st;
+        const int64_t row = p.H * (d->gate == GLA_GATE_CHANNEL ? p.K : 1);  // one gate a head for all rows: GLA_GATE_HEAD
+        st = d->gate == GLA_GATE_HEAD ? gla::check_gates(log_a, row, s)
+                                      : gla::check_gates(log_a, p.B * row, s, slot_rows(slots, row, c->slots));
+        if (st != GLA_OK) return st;
     }
     st = gla::cache_step(p, q, k, v, log_a, slots, lengths, o, s);
     if (st != GLA_OK || !chk) return st;

@@ -33,10 +33,20 @@ unsigned blocks_for(int64_t n) {
 // positive value fail it, -inf is caught by the finiteness test.
 __device__ __forceinline__ bool gate_ok(float x) { return x <= 0.f && x > -INFINITY; }
 
-__global__ void __launch_bounds__(kThreads) k_check_gates(const float* __restrict__ la, int64_t n, int* err) {
+// Whether element i counts; asked only of those that fail.
+__device__ __forceinline__ bool counts(const CheckedRows& c, int64_t i) {
+    if (c.kind == CheckedRows::kAll) return true;
+    const int64_t r = i / c.per_row;
+    if (c.kind == CheckedRows::kSlots) return c.at[r] >= 0 && c.at[r] < c.n;
+    const int64_t t = r % c.rows;
+    return t >= c.at[0] && t < c.at[c.n];
+}
+
+__global__ void __launch_bounds__(kThreads) k_check_gates(const float* __restrict__ la, int64_t n, CheckedRows rows,
+                                                          int* err) {
     bool bad = false;
     for (int64_t i = int64_t(blockIdx.x) * blockDim.x + threadIdx.x; i < n; i += int64_t(gridDim.x) * blockDim.x)
-        bad |= !gate_ok(la[i]);
+        bad |= !gate_ok(la[i]) && counts(rows, i);
     if (__syncthreads_or(bad) && threadIdx.x == 0) atomicOr(err, kErrBadGate);
 }
 
@@ -48,10 +58,11 @@ template <>
 __device__ __forceinline__ float to_f<__nv_bfloat16>(__nv_bfloat16 x) { return __bfloat162float(x); }
 
 template <typename T>
-__global__ void __launch_bounds__(kThreads) k_check_finite(const T* __restrict__ p, int64_t n, int* err) {
+__global__ void __launch_bounds__(kThreads) k_check_finite(const T* __restrict__ p, int64_t n, CheckedRows rows,
+                                                           int* err) {
     bool bad = false;
     for (int64_t i = int64_t(blockIdx.x) * blockDim.x + threadIdx.x; i < n; i += int64_t(gridDim.x) * blockDim.x)
-        bad |= !isfinite(to_f(p[i]));
+        bad |= !isfinite(to_f(p[i])) && counts(rows, i);
     if (__syncthreads_or(bad) && threadIdx.x == 0) atomicOr(err, kErrNonFinite);
 }
 
@@ -94,20 +105,20 @@ Arena make_arena(const Problem& p, void* base, size_t cap) {
     return a;
 }
 
-gla_status check_gates(const float* log_a, int64_t n, cudaStream_t s) {
+gla_status check_gates(const float* log_a, int64_t n, cudaStream_t s, CheckedRows rows) {
     if (n <= 0) return GLA_OK;
-    GLA_LAUNCH("check_gates", k_check_gates, blocks_for(n), kThreads, 0, s, log_a, n, device_error_word());
+    GLA_LAUNCH("check_gates", k_check_gates, blocks_for(n), kThreads, 0, s, log_a, n, rows, device_error_word());
     return GLA_OK;
 }
 
-gla_status check_finite(const void* p, int64_t n, bool bf16, cudaStream_t s) {
+gla_status check_finite(const void* p, int64_t n, bool bf16, cudaStream_t s, CheckedRows rows) {
     if (!p || n <= 0) return GLA_OK;
     if (bf16)
         GLA_LAUNCH("check_finite", k_check_finite<__nv_bfloat16>, blocks_for(n), kThreads, 0, s,
-                   static_cast<const __nv_bfloat16*>(p), n, device_error_word());
+                   static_cast<const __nv_bfloat16*>(p), n, rows, device_error_word());
     else
         GLA_LAUNCH("check_finite", k_check_finite<float>, blocks_for(n), kThreads, 0, s, static_cast<const float*>(p),
-                   n, device_error_word());
+                   n, rows, device_error_word());
     return GLA_OK;
 }
 

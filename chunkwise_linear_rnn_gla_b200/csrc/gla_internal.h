@@ -73,8 +73,19 @@ enum : int { kErrBadGate = 2, kErrNonFinite = 4, kErrGuard = 8, kErrBadRow = 16 
 // Before a pass: every gate must be finite and <= 0 (kErrBadGate); the workspace
 // guards are filled. After it: every output element must be finite
 // (kErrNonFinite) and every guard intact (kErrGuard).
-gla_status check_gates(const float* log_a, int64_t n, cudaStream_t s);
-gla_status check_finite(const void* p, int64_t n, bool bf16, cudaStream_t s);
+// `rows` says which elements count: all of them, the rows of packed sequences that belong to one (cu[0] .. cu[n]-1 of
+// the `rows` rows of a head), or the rows of a call whose slot lies in a pool of n. What stands in the others is the
+// caller's business.
+struct CheckedRows {
+    enum Kind { kAll, kPacked, kSlots };
+    Kind kind = kAll;
+    const int32_t* at = nullptr;  // cu_seqlens or slots
+    int64_t per_row = 1;          // elements
+    int64_t rows = 1;
+    int64_t n = 0;
+};
+gla_status check_gates(const float* log_a, int64_t n, cudaStream_t s, CheckedRows rows = {});
+gla_status check_finite(const void* p, int64_t n, bool bf16, cudaStream_t s, CheckedRows rows = {});
 gla_status guards_fill(const Arena& a, cudaStream_t s);
 gla_status guards_check(const Arena& a, cudaStream_t s);
 bool checks_on(const Problem& p);

@@ -103,7 +103,8 @@ def scan_fwd(x, log_a, h0=None, *, cu_seqlens=None, write="input", gate="channel
              want_hT=True, workspace: Optional[torch.Tensor] = None, checks=False):
     """Forward. Returns (h, hT); hT is None when want_hT is False and no hT buffer is given. A `workspace`
     (scan_workspace) keeps what scan_bwd(ws_from_fwd=True) reuses. checks=True: the library's checking mode
-    (gate domain, finite outputs), synchronous, raises GlaError on a failure."""
+    (gate domain, finite outputs; of packed rows those that belong to a sequence), synchronous, raises GlaError on
+    a failure."""
     lib = load()
     B, H, L, D = _sizes(x, cu_seqlens)
     dev = x.device

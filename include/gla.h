@@ -322,6 +322,8 @@ gla_status gla_gsa_bwd(const gla_desc* d, int32_t slots, const void* q, const vo
  * heads) x D <= 2^30 (GLA_ERR_UNSUPPORTED beyond).
  * Sums and states are fp32; only h and dx are rounded to dtype. The result does
  * not depend on how the sequences are packed beyond the rounding of the joins.
+ * GLA_FLAG_CHECKS looks at the rows that belong to a sequence (a step's: that
+ * have a slot) alone, the gates before the call and the outputs after it.
  *
  * The backward returns the gradients of <dh, h> + <dhT, hT>:
  *     g_t = dh_t + a_{t+1} g_{t+1}  (+ dhT at the last step),   dx_t = w_t g_t,
@@ -394,7 +396,9 @@ gla_status gla_scan_step(const gla_desc* d, int32_t write, const void* x, const 
  *
  * Descriptor: B rows, H, Dk, Dv, dtype (q, k, v, o and the window), gate and
  * gate_tau (gla_cache_step; all kinds, stored as per-channel log a) and flags
- * (GLA_FLAG_CHECKS); L is ignored, the other fields as for the scan. window is
+ * (GLA_FLAG_CHECKS: for the rows with a slot, gates in their domain, finite o
+ * and S, the S that gla_cache_store is given included, though a state that is
+ * not finite can be held); L is ignored, the other fields as for the scan. window is
  * 1 .. 64; GLA_ERR_UNSUPPORTED when a head's window does not fit on chip
  * (4 * window * (Dk + 128) + 16 Dk + 8192 bytes above 200 KB), and beyond B = 2^22,
  * H = 65535 or B H ceil(Dv / 128) ceil(Dk / 64) = 2^30. */

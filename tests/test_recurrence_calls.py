@@ -95,3 +95,95 @@ def test_cache_from_two_threads(lib):
     both(lib, *calls)
     for o, o1, S, S1 in outs:
         assert torch.equal(o, o1) and torch.equal(S, S1)
+
+
+NAN = float("nan")
+
+
+def refused(call, *a, **kw):
+    with pytest.raises(gla.GlaError) as e:
+        call(*a, **kw)
+    assert e.value.status == _lib.GLA_ERR_INVALID_ARG and gla.gla_check_device_error() == _lib.GLA_OK
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("gate", ["channel", "preact"])
+@pytest.mark.parametrize("dtype", [torch.float32, torch.bfloat16])
+def test_checks_of_packed_rows(lib, gate, dtype):
+    """Rows outside every sequence may hold anything; the others are checked, their outputs too."""
+    cu, T, H, D = [3, 40, 40, 200], 333, 2, 70
+    t = ts.make(1, H, T, D, dtype, gate, cu=cu, seed=5)
+    d = {n: v.cuda() for n, v in t.items()}
+    for n in ("x", "z", "dh"):
+        d[n][:, :, :3], d[n][:, :, 200:] = NAN, NAN
+    o = dict(cu_seqlens=torch.tensor(cu, dtype=torch.int32, device="cuda"), write="leak", gate=gate,
+             tau=ts.TAU if gate == "preact" else 0.0)
+    full = lambda like: torch.full_like(like, NAN)  # noqa: E731
+    ws = scan.scan_workspace(d["x"], o["cu_seqlens"], checks=True)
+    h, hT = scan.scan_fwd(d["x"], d["z"], d["h0"], h=full(d["x"]), workspace=ws, checks=True, **o)
+    b = scan.scan_bwd(d["x"], d["z"], d["dh"], d["h0"], d["dhT"], out={"dx": full(h), "dlog_a": full(d["z"])}, workspace=ws,
+                      ws_from_fwd=True, checks=True, **o)
+    h1, hT1 = scan.scan_fwd(d["x"], d["z"], d["h0"], **o)
+    b1 = scan.scan_bwd(d["x"], d["z"], d["dh"], d["h0"], d["dhT"], **o)
+    for g, g1 in ((h, h1), (b["dx"], b1["dx"]), (b["dlog_a"], b1["dlog_a"])):
+        assert torch.equal(g[:, :, 3:200], g1[:, :, 3:200])
+        assert bool(g[:, :, :3].isnan().all()) and bool(g[:, :, 200:].isnan().all())
+    assert torch.equal(hT, hT1) and torch.equal(b["dh0"], b1["dh0"])
+    # the first and the last row that belong to a sequence, in each input
+    for n, row, bad in (("x", 3, NAN), ("x", 199, float("inf")), ("z", 199, 0.5), ("z", 3, NAN)):
+        if n == "z" and gate == "preact" and bad == 0.5:
+            continue  # every finite pre-activation is a gate
+        p = dict(d, **{n: d[n].clone()})
+        p[n][0, 1, row, 69] = bad
+        refused(scan.scan_fwd, p["x"], p["z"], p["h0"], checks=True, **o)
+    p = dict(d, dh=d["dh"].clone())
+    p["dh"][0, 0, 100, 0] = NAN
+    refused(scan.scan_bwd, p["x"], p["z"], p["dh"], p["h0"], p["dhT"], checks=True, **o)
+
+
+@pytest.mark.gpu
+def test_checks_of_padding_rows_in_a_scan_step(lib):
+    B, D = 5, 40
+    x, z = torch.randn(B, 1, D, device="cuda"), -torch.rand(B, 1, D, device="cuda")
+    slots = torch.tensor([4, -1, 0, -7, 2], dtype=torch.int32, device="cuda")
+    x[1], z[1], z[3] = NAN, NAN, 0.25
+    h = scan.scan_step(x, z, torch.zeros(6, 1, D, device="cuda"), slots, checks=True)
+    assert bool((h[[1, 3]] == 0).all()) and torch.equal(h[[0, 2, 4]], x[[0, 2, 4]])
+    refused(scan.scan_step, x, z, torch.zeros(6, 1, D, device="cuda"), checks=True)  # without slots every row counts
+    for b in (0, 4):
+        zb = z.clone()
+        zb[b, 0, D - 1] = 0.25
+        refused(scan.scan_step, x, zb, torch.zeros(6, 1, D, device="cuda"), slots, checks=True)
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("gate", ["channel", "scalar"])
+def test_checks_of_padding_rows_in_a_cached_step(lib, gate):
+    c, S, g = fill_pool(4, 2, 32, 64, 4, "int8", torch.float32)
+    t = {n: x.cuda() for n, x in token(c, 3, g, gate).items()}
+    slots, lengths = pool_case(c, [3, -2, 0], [0, 0, 2])
+    for x in t.values():
+        x[1] = NAN
+    gc.cache_step(c, t["q"], t["k"], t["v"], t["log_a"], slots, lengths, gate=gate, checks=True)
+    S = S.cuda()[:3].contiguous()
+    S[1] = NAN
+    gc.cache_store(c, S, slots, checks=True)
+    gc.cache_load(c, slots, lengths, checks=True)
+    S[2, 1, 31, 63] = NAN
+    refused(gc.cache_store, c, S, slots, checks=True)
+    t["log_a"][2, 1] = 0.25
+    refused(gc.cache_step, c, t["q"], t["k"], t["v"], t["log_a"], slots, lengths, gate=gate, checks=True)
+
+
+@pytest.mark.gpu
+def test_checks_still_report_refused_rows(lib):
+    """A slot outside the pool has no row to check, and is reported."""
+    x, z = torch.randn(2, 1, 40, device="cuda"), torch.full((2, 1, 40), NAN, device="cuda")
+    z[0] = -1
+    refused(scan.scan_step, x, z, torch.zeros(3, 1, 40, device="cuda"),
+            torch.tensor([0, 3], dtype=torch.int32, device="cuda"), checks=True)
+    # boundaries beyond the rows or out of order: nothing outside the tensors is read
+    x = torch.randn(1, 1, 300, 64, device="cuda")
+    for cu in ([-5, 100, 400], [250, 10, 20], [2**31 - 1, 5, -2**31]):
+        scan.scan_fwd(x, -x.abs(), cu_seqlens=torch.tensor(cu, dtype=torch.int32, device="cuda"), hT=None, want_hT=False,
+                      checks=True)
