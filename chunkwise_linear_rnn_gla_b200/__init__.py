@@ -366,6 +366,12 @@ def gla_selftest_wait_timeout(limit_cycles=0, stream=None) -> None:
     _check(load().gla_selftest_wait_timeout(int(limit_cycles), s), "gla_selftest_wait_timeout")
 
 
+def gla_selftest_wait_limit(limit_cycles=0) -> None:
+    """Limit in SM cycles of the waits inside the scan's kernels from now on (0: the built-in one; negative: run out
+    before they begin)."""
+    load().gla_selftest_wait_limit(int(limit_cycles))
+
+
 def gla_launch_count() -> int:
     return int(load().gla_launch_count())
 

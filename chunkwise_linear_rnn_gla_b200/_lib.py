@@ -35,6 +35,7 @@ EXPORTS = (
     "gla_check_device_error", "gla_status_string", "gla_abi_version", "gla_resolve", "gla_launch_count",
     "gla_launch_count_reset", "gla_profile_enable", "gla_profile_read", "gla_profile_reset", "gla_fwd_noalloc",
     "gla_selftest_wait_timeout", "gla_last_device_error", "gla_fwd_workspace_bytes", "gla_bwd_workspace_bytes",
+    "gla_selftest_wait_limit",
     "gla_segment_decay", "gla_state_combine", "gla_fwd_final_state", "gla_bwd_initial_grad",
     "gla_gsa_resolve", "gla_gsa_fwd_workspace_size", "gla_gsa_bwd_workspace_size", "gla_gsa_fwd", "gla_gsa_bwd",
     "gla_gsa_step",
@@ -91,6 +92,8 @@ def _declare(lib):
     lib.gla_bwd_workspace_bytes.restype = sz
     lib.gla_selftest_wait_timeout.argtypes = [ctypes.c_longlong, vp]
     lib.gla_selftest_wait_timeout.restype = ctypes.c_int
+    lib.gla_selftest_wait_limit.argtypes = [ctypes.c_longlong]
+    lib.gla_selftest_wait_limit.restype = None
     lib.gla_status_string.argtypes = [ctypes.c_int]
     lib.gla_status_string.restype = ctypes.c_char_p
     lib.gla_abi_version.restype = ctypes.c_int

@@ -98,6 +98,14 @@ gla_status launch_end(const char* name, cudaStream_t s) {
     return err == cudaSuccess ? GLA_OK : GLA_ERR_CUDA;
 }
 
+namespace {
+std::atomic<long long> g_wait_limit{0};
+}
+long long wait_limit() {
+    const long long l = g_wait_limit.load(std::memory_order_relaxed);
+    return l == 0 ? tc::kWaitLimit : l;
+}
+
 int* device_error_word() {
     void* p = nullptr;
     if (cudaGetSymbolAddress(&p, g_device_error) != cudaSuccess) return nullptr;
@@ -297,6 +305,7 @@ gla_status resolve_scan(const gla_desc* d, int32_t write, bool packed, bool one_
     p.preact = d->gate == GLA_GATE_PREACT;
     p.inv_tau = gp.inv_tau;
     p.flags = d->flags;
+    p.wait_limit = gla::wait_limit();
     // the grid's first axis counts (sequence or head, channel tile, segment); its second a step's rows
     const int64_t lead = packed ? p.H : p.B * p.H;
     if (lead > (int64_t(1) << 22) || p.B > (int64_t(1) << 22) || p.H > 65535 || p.L > (int64_t(1) << 30) ||
@@ -947,6 +956,8 @@ gla_status gla_selftest_wait_timeout(long long limit_cycles, void* stream) {
                limit_cycles > 0 ? limit_cycles : 2000000LL);
     return GLA_OK;
 }
+
+void gla_selftest_wait_limit(long long limit_cycles) { gla::g_wait_limit.store(limit_cycles, std::memory_order_relaxed); }
 
 gla_status gla_check_device_error(void* stream) {
     if (cudaStreamSynchronize(static_cast<cudaStream_t>(stream)) != cudaSuccess) return GLA_ERR_CUDA;

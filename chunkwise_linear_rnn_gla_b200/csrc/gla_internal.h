@@ -69,6 +69,10 @@ gla_status launch_end(const char* name, cudaStream_t s);
 int* device_error_word();
 enum : int { kErrBadGate = 2, kErrNonFinite = 4, kErrGuard = 8, kErrBadRow = 16 };
 
+// Cycles after which the bounded waits of the scan's kernels give up
+// (gla_selftest_wait_limit).
+long long wait_limit();
+
 // ---- checking build (gla_checks.cu) ------------------------------------------
 // Before a pass: every gate must be finite and <= 0 (kErrBadGate); the workspace
 // guards are filled. After it: every output element must be finite
@@ -174,6 +178,7 @@ struct ScanProblem {
     bool preact;    // log_a holds z
     float inv_tau;
     int flags;
+    long long wait_limit;  // of the kernels' bounded waits, in cycles
 };
 // Workspace: the fp32 state entering every segment of rows, [B*H or H][segments][D].
 size_t scan_workspace(const ScanProblem& p, Arena& a);

@@ -21,9 +21,9 @@ __global__ void __launch_bounds__(WARPS * 32, 16 / WARPS)
     const Place<T, VEC, WARPS, ROWS, STAGE> at(p, cl, dyn + (cl > 1 ? 2 * cl * 32 * sizeof(Map<V>) : 0));
     const int lane = at.lane, warp = at.warp, rank = at.rank;
     const int64_t lead = at.lead, c = at.c, cc = at.cc, head = PACKED ? lead : 0;
-    const bool mine = at.mine;
+    bool mine = at.mine;
     const int rounds = int(cdiv(p.L, int64_t(WARPS * ROWS) * cl));
-    Exchange<V> ex{reinterpret_cast<Map<V>*>(dyn), bar, &abort_flag, err, cl, rank, rounds};
+    Exchange<V> ex{reinterpret_cast<Map<V>*>(dyn), bar, &abort_flag, err, cl, rank, rounds, p.wait_limit};
     const RowOffsets<ROWS> whole(ROWS, p.D);
     const auto offsets = [&](int64_t t) { return p.L - t >= ROWS ? whole : RowOffsets<ROWS>(p.L - t, p.D); };
     Ahead<float, VEC, ROWS> ga;
@@ -77,6 +77,7 @@ __global__ void __launch_bounds__(WARPS * 32, 16 / WARPS)
         }
         if (PACKED && ri.start) own.a = vset<V>(kForget);
         agg[par][warp][lane] = own;
+        const bool sends = cl > 1 && warp == WARPS - 1 && !ex.gave_up();
         __syncthreads();
         Map<V> pre{vset<V>(1.f), vset<V>(0.f)};  // of the block's rows in front of this warp's
 #pragma unroll
@@ -88,8 +89,8 @@ __global__ void __launch_bounds__(WARPS * 32, 16 / WARPS)
         }
         V in = carry;  // state entering the block's rows
         if (cl > 1) {
-            if (warp == WARPS - 1) ex.put(r, Map<V>{join<PACKED>(own.a, pre.a), join<PACKED>(own.a, pre.u, own.u)});
-            const Map<V>* m = ex.get(r);
+            if (sends) ex.put(r, Map<V>{join<PACKED>(own.a, pre.a), join<PACKED>(own.a, pre.u, own.u)});
+            const Map<V>* m = ex.get(r, mine);
             for (int q = 0; q < cl; ++q) {
                 if (q == rank) in = carry;
                 carry = join<PACKED>(m[q * 32].a, carry, m[q * 32].u);

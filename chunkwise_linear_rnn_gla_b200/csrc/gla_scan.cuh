@@ -214,6 +214,10 @@ __device__ __forceinline__ void send(Map<V>* place, uint64_t* bar, uint32_t rank
 // cl maps on its own barrier, of which there are two for alternate rounds. A map of round i + 2 cannot overtake the
 // reading of round i's: its sender has waited for this block's map of round i + 1, which left after all of this
 // block's warps were done with round i.
+//
+// A block in which a wait ran out (abort) sends no more maps, so that the waits of the others run out too; a thread whose
+// wait ran out arms no barrier and writes no results from then on. Both keep to the block's barriers and the cluster's,
+// and the maps that are still on their way to the block land (with a limit) before it ends.
 template <typename V>
 struct Exchange {
     Map<V>* maps;   // [2][cl][32]
@@ -221,6 +225,8 @@ struct Exchange {
     int* abort;
     int* err;
     int cl, rank, rounds;
+    long long limit;  // of a wait, in cycles
+    __device__ __forceinline__ bool gave_up() const { return *static_cast<volatile int*>(abort) != 0; }
     __device__ __forceinline__ uint32_t bytes() const { return uint32_t(cl * 32 * sizeof(Map<V>)); }
     __device__ __forceinline__ void begin() {
         if (cl == 1) return;
@@ -236,16 +242,17 @@ struct Exchange {
     __device__ __forceinline__ void ready() const {
         if (cl > 1) cluster_wait();
     }
-    // one warp sends its block's map of round `it`
+    // one warp sends its block's map of round `it`, unless the block gave up before
     __device__ __forceinline__ void put(int it, Map<V> m) const {
         const int par = it & 1;
         for (int q = 0; q < cl; ++q) send(maps + (par * cl + rank) * 32 + (threadIdx.x & 31), bar + par, uint32_t(q), m);
     }
-    // every thread waits for the maps of round `it`
-    __device__ __forceinline__ const Map<V>* get(int it) const {
+    // every thread waits for the maps of round `it`; `ok` becomes false where the wait ran out
+    __device__ __forceinline__ const Map<V>* get(int it, bool& ok) const {
         const int par = it & 1;
-        (void)tc::mbar_wait(bar + par, uint32_t(it >> 1) & 1u, err, abort);
-        if (threadIdx.x == 0 && it + 2 < rounds) tc::mbar_arrive_expect_tx(bar + par, bytes());
+        const bool got = tc::mbar_wait(bar + par, uint32_t(it >> 1) & 1u, err, abort, limit);
+        ok = ok && got;
+        if (got && threadIdx.x == 0 && it + 2 < rounds) tc::mbar_arrive_expect_tx(bar + par, bytes());
         return maps + par * cl * 32 + (threadIdx.x & 31);
     }
     // no block leaves while another may still send to it
@@ -253,6 +260,9 @@ struct Exchange {
         if (cl > 1) {
             cluster_arrive();
             cluster_wait();
+            if (gave_up()) {  // of each barrier one phase is over and the other may not be
+                for (int i = 0; i < 4; ++i) tc::mbar_drain(bar + (i & 1), uint32_t(i >> 1), 1000000LL);
+            }
         }
     }
 };

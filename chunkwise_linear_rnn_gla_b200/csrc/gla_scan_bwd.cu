@@ -25,9 +25,9 @@ __global__ void __launch_bounds__(WARPS * 32, 16 / WARPS)
     const Place<T, VEC, WARPS, ROWS, STAGE> at(p, cl, dyn + (cl > 1 ? 2 * cl * 32 * sizeof(Map<V>) : 0));
     const int lane = at.lane, warp = at.warp, rank = at.rank;
     const int64_t lead = at.lead, c = at.c, cc = at.cc, head = PACKED ? lead : 0;
-    const bool mine = at.mine;
+    bool mine = at.mine;
     const int rounds = int(cdiv(p.L, int64_t(WARPS * ROWS) * cl));
-    Exchange<V> ex{reinterpret_cast<Map<V>*>(dyn), bar, &abort_flag, err, cl, rank, rounds};
+    Exchange<V> ex{reinterpret_cast<Map<V>*>(dyn), bar, &abort_flag, err, cl, rank, rounds, p.wait_limit};
     const RowOffsets<ROWS> whole(ROWS, p.D);
     const auto offsets = [&](int64_t t) { return p.L - t >= ROWS ? whole : RowOffsets<ROWS>(p.L - t, p.D); };
     Ahead<float, VEC, ROWS> ga;
@@ -97,6 +97,7 @@ __global__ void __launch_bounds__(WARPS * 32, 16 / WARPS)
         if (PACKED && ri.start) own.a = vset<V>(kForget);
         agg[par][warp][lane] = own;
         aggy[par][warp][lane] = Y;
+        const bool sends = cl > 1 && warp == 0 && !ex.gave_up();
         __syncthreads();
         Map<V> post{vset<V>(1.f), vset<V>(0.f)};  // the map (of y) of the block's rows behind this warp's
 #pragma unroll
@@ -115,8 +116,8 @@ __global__ void __launch_bounds__(WARPS * 32, 16 / WARPS)
         }
         V in = carry;
         if (cl > 1) {
-            if (warp == 0) ex.put(it, Map<V>{join<PACKED>(own.a, post.a), join<PACKED>(own.a, post.u, Y)});
-            const Map<V>* m = ex.get(it);
+            if (sends) ex.put(it, Map<V>{join<PACKED>(own.a, post.a), join<PACKED>(own.a, post.u, Y)});
+            const Map<V>* m = ex.get(it, mine);
             for (int q = cl - 1; q >= 0; --q) {
                 if (q == rank) in = carry;
                 carry = join<PACKED>(m[q * 32].a, carry, m[q * 32].u);

@@ -30,6 +30,7 @@ namespace tc {
 
 // Error codes written to the device error word by a wait that ran out.
 enum : int { kErrWaitTimeout = 1 };
+constexpr long long kWaitLimit = 2000000000LL;  // cycles after which a bounded wait gives up, about a second
 
 __device__ __forceinline__ uint32_t smem_u32(const void* p) {
     return static_cast<uint32_t>(__cvta_generic_to_shared(p));
@@ -84,14 +85,14 @@ __device__ __forceinline__ bool mbar_try_wait_sleep(uint64_t* bar, uint32_t pari
 // after ~`limit_cycles` SM cycles, records kErrWaitTimeout in *err (device
 // memory) and in *abort (shared memory), and returns false. A set *abort
 // makes every later wait return false at once so that all roles of the block
-// drain to the exit.
+// drain to the exit. A negative limit has run out before the wait begins.
 __device__ __forceinline__ bool mbar_wait(uint64_t* bar, uint32_t parity, int* err, volatile int* abort,
-                                          long long limit_cycles = 2000000000LL) {
-    if (mbar_try_wait(bar, parity)) return true;
+                                          long long limit_cycles = kWaitLimit) {
+    if (limit_cycles >= 0 && mbar_try_wait(bar, parity)) return true;
     const long long t0 = clock64();
     while (true) {
         if (*abort) return false;
-        if (mbar_try_wait_sleep(bar, parity, 20000u)) return true;
+        if (limit_cycles >= 0 && mbar_try_wait_sleep(bar, parity, 20000u)) return true;
         if (clock64() - t0 > limit_cycles) {
             if (err) atomicOr(err, kErrWaitTimeout);
             *abort = 1;
@@ -103,7 +104,7 @@ __device__ __forceinline__ bool mbar_wait(uint64_t* bar, uint32_t parity, int* e
 // The same wait for short ones on the critical path (a neighbour's message, the next chunk of a stream): it polls, since
 // a suspended thread is woken late.
 __device__ __forceinline__ bool mbar_wait_poll(uint64_t* bar, uint32_t parity, int* err, volatile int* abort,
-                                               long long limit_cycles = 2000000000LL) {
+                                               long long limit_cycles = kWaitLimit) {
     if (mbar_try_wait(bar, parity)) return true;
     const long long t0 = clock64();
     while (true) {
@@ -119,7 +120,7 @@ __device__ __forceinline__ bool mbar_wait_poll(uint64_t* bar, uint32_t parity, i
 
 // Bounded wait that ignores the abort flag: lets copies and MMAs that were
 // already issued land before a block that gave up exits.
-__device__ __forceinline__ void mbar_drain(uint64_t* bar, uint32_t parity, long long limit_cycles = 2000000000LL) {
+__device__ __forceinline__ void mbar_drain(uint64_t* bar, uint32_t parity, long long limit_cycles = kWaitLimit) {
     const long long t0 = clock64();
     while (!mbar_try_wait_sleep(bar, parity, 20000u))
         if (clock64() - t0 > limit_cycles) return;

@@ -187,3 +187,48 @@ def test_checks_still_report_refused_rows(lib):
     for cu in ([-5, 100, 400], [250, 10, 20], [2**31 - 1, 5, -2**31]):
         scan.scan_fwd(x, -x.abs(), cu_seqlens=torch.tensor(cu, dtype=torch.int32, device="cuda"), hT=None, want_hT=False,
                       checks=True)
+
+
+@pytest.fixture
+def no_patience(lib):
+    """Waits inside the kernels run out before they begin, until the fixture's function is called."""
+    gla.gla_selftest_wait_limit(-1)
+    yield lambda: gla.gla_selftest_wait_limit(0)
+    gla.gla_selftest_wait_limit(0)
+    gla.gla_check_device_error()
+
+
+def timed_out():
+    return gla.gla_check_device_error() == _lib.GLA_ERR_TIMEOUT and gla.gla_check_device_error() == _lib.GLA_OK
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("cu", [None, [0, 1500, 1507, 4100]])
+@pytest.mark.parametrize("dtype,D", [(torch.float32, 64), (torch.bfloat16, 33)])
+def test_scan_writes_nothing_after_a_wait_that_ran_out(lib, no_patience, dtype, D, cu):
+    """Several rounds of several blocks a sequence: the call ends, reports the timeout, leaves its outputs and the kept
+    states as they were, and the next call is right."""
+    t = ts.make(1, 2, 4100, D, dtype, "channel", cu=cu, seed=D)
+    d = {n: v.cuda() for n, v in t.items()}
+    c = None if cu is None else torch.tensor(cu, dtype=torch.int32, device="cuda")
+    seven = lambda like: torch.full_like(like, 7)  # noqa: E731
+    h, hT, ws = seven(d["x"]), seven(d["h0"]), scan.scan_workspace(d["x"], c).fill_(7)
+    scan.scan_fwd(d["x"], d["z"], d["h0"], cu_seqlens=c, h=h, hT=hT, workspace=ws)
+    assert timed_out()
+    for x in (h, hT, ws[:2 * -(-4100 // 32) * D * 4]):  # (a guard block may follow the states)
+        assert bool((x == 7).all())
+    out = {"dx": seven(d["x"]), "dlog_a": seven(d["z"]), "dh0": seven(hT)}
+    ws.zero_()
+    scan.scan_bwd(d["x"], d["z"], d["dh"], d["h0"], d["dhT"], cu_seqlens=c, workspace=ws, ws_from_fwd=True, out=out)
+    assert timed_out()
+    for x in out.values():
+        assert bool((x == 7).all())
+    no_patience()
+    ts.check(t, cu, "input", "channel")
+    assert gla.gla_check_device_error() == _lib.GLA_OK
+
+
+@pytest.mark.gpu
+def test_scan_of_one_block_waits_for_nobody(lib, no_patience):
+    ts.check(ts.make(2, 1, 30, 64, torch.float32, "channel"), None, "leak", "channel")
+    assert gla.gla_check_device_error() == _lib.GLA_OK
