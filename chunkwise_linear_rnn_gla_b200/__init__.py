@@ -367,8 +367,8 @@ def gla_selftest_wait_timeout(limit_cycles=0, stream=None) -> None:
 
 
 def gla_selftest_wait_limit(limit_cycles=0) -> None:
-    """Limit in SM cycles of the waits inside the scan's kernels from now on (0: the built-in one; negative: run out
-    before they begin)."""
+    """Limit in SM cycles of the waits inside the scan's and the state cache's kernels from now on (0: the built-in
+    one; negative: run out before they begin)."""
     load().gla_selftest_wait_limit(int(limit_cycles))
 
 

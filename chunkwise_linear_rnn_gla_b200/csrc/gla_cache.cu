@@ -510,6 +510,10 @@ __global__ void __launch_bounds__(kThreads, 4) k_cache_step(Pool c, const T* __r
 // so it is split into its groups of 128 columns, which share nothing but the window: each is an item of its own that
 // forms its columns of S_t, reads o from them and rounds them back. The blocks' shares are cut by cost, from the lengths
 // that every block reads.
+//
+// A warp whose wait ran out (abort) neither writes nor announces anything more, so that the waits that depend on it run out
+// too, and ends: readers and producers by themselves, window warps together, at their barrier. The producers let the
+// copies that they issued land before they end.
 constexpr int kReadWarps = 16, kWinWarps = 8;
 constexpr int kReadThreads = kReadWarps * 32, kWinThreads = kWinWarps * 32;
 constexpr int kStreamThreads = kReadThreads + kWinThreads + 96;
@@ -530,6 +534,7 @@ struct StreamPlan {
     int off_kt, off_dec, off_wq, off_p, win_bytes;     // what the window warps leave (two heads' worth)
     int off_red, off_ring, chunk_bytes;
     size_t smem;      // 0: not for this shape
+    long long wait_limit;
 };
 
 struct Item {
@@ -552,8 +557,9 @@ __device__ __forceinline__ bool warp_wait(uint64_t* bar, uint32_t parity, int* e
     return __all_sync(0xffffffffu, ok) != 0;
 }
 // for waits that are long by design: the warp leaves the issue slots to the others
-__device__ __forceinline__ bool warp_sleep(uint64_t* bar, uint32_t parity, int* err, int* abort) {
-    const bool ok = tc::mbar_wait(bar, parity, err, abort);
+__device__ __forceinline__ bool warp_sleep(uint64_t* bar, uint32_t parity, int* err, int* abort,
+                                           long long limit = tc::kWaitLimit) {
+    const bool ok = tc::mbar_wait(bar, parity, err, abort, limit);
     return __all_sync(0xffffffffu, ok) != 0;
 }
 __device__ __forceinline__ void warp_arrive(uint64_t* bar) {
@@ -676,15 +682,14 @@ __global__ void __launch_bounds__(kStreamThreads, 1)
     const Share share(folds, B, int(c.H), NG);
     const int items = share.count();
     const int chunks = (K + pl.chunk_rows - 1) / pl.chunk_rows;
-    // A wait that ran out leaves a thread's `ok` false: it then writes nothing, but keeps step with the block's barriers.
-    bool ok = true;
     if (warp >= kReadWarps + kWinWarps) {
         // ---- producers (all lanes look for rows that name a slot twice, lane 0 does the rest)
         const int part = warp - (kReadWarps + kWinWarps);  // 0: codes, 1: keys, 2: values
         Turn rt;
         int checked = -1;       // the row looked at last, and whether it stands
         bool stands = false;
-        int lives = 0;          // items so far that are not padding
+        bool ok = true;
+        int sent = 0;           // items whose copies this part has issued (keys: padding rows count too)
         int64_t nch = 0;        // chunks so far
         for (int it = 0; it < items && ok; ++it) {
             Item x;
@@ -738,6 +743,7 @@ __global__ void __launch_bounds__(kStreamThreads, 1)
                 if (lane == 0) {
                     if (it > 0) ok = tc::mbar_wait_poll(&a_empty, uint32_t(it - 1) & 1u, err, &abort_flag);
                     if (ok) {
+                        ++sent;
                         a_info = x;
                         if (!stands) tc::mbar_arrive(&a_full);
                         else {
@@ -755,24 +761,22 @@ __global__ void __launch_bounds__(kStreamThreads, 1)
                 }
             } else if (lane == 0 && stands) {
                 // the values' stage is free once the head before has been written out
-                if (lives > 0) ok = tc::mbar_wait(&b_empty, uint32_t(lives - 1) & 1u, err, &abort_flag);
+                if (sent > 0) ok = tc::mbar_wait(&b_empty, uint32_t(sent - 1) & 1u, err, &abort_flag);
                 if (ok) {
+                    ++sent;
                     tc::mbar_arrive_expect_tx(&b_full, (n + 1) * vb);
                     bulk_copy(dyn + pl.off_v, v + x.bh * V, vb, &b_full);
                     if (n > 0) bulk_copy(dyn + pl.off_vw, static_cast<T*>(c.v) + x.sh * c.W * V, n * vb, &b_full);
                 }
-                ++lives;
             }
             ok = __shfl_sync(0xffffffffu, int(ok), 0) != 0;
         }
-        if (!ok && lane == 0) {
-            // a wait ran out: let the copies that were issued land (each wait with its limit) before the block ends
-            constexpr long long limit = 100000000LL;
-            for (uint32_t par = 0; par < 2; ++par) {
-                for (int i = 0; i < pl.ring && part == 0; ++i) tc::mbar_drain(ring_full + i, par, limit);
-                if (part == 1) tc::mbar_drain(&a_full, par, limit);
-                if (part == 2) tc::mbar_drain(&b_full, par, limit);
-            }
+        // Warps that gave up do not wait for the copies that were issued: this part does, before the block can end.
+        if (lane == 0) {
+            for (int i = 0; i < pl.ring && part == 0; ++i)
+                if (nch > i) tc::mbar_drain(ring_full + i, uint32_t((nch - 1 - i) / pl.ring) & 1u);
+            if (part == 1 && sent > 0) tc::mbar_drain(&a_full, uint32_t(sent - 1) & 1u);
+            if (part == 2 && sent > 0) tc::mbar_drain(&b_full, uint32_t(sent - 1) & 1u);
         }
         return;
     }
@@ -791,13 +795,13 @@ __global__ void __launch_bounds__(kStreamThreads, 1)
         const int parts = K / 2 >= kWinThreads ? 1 : kWinThreads / (K / 2), part = parts == 1 ? 0 : t / (K / 2);
         Turn wt;
         Item last{0, 0, 0, -1, 0};
-        bool have = false;
+        bool ok = true;
         int lives = 0;
         // the head `last`: what the readers summed and, of an ordinary head, the window's part
         const auto finish = [&](const float* ps, int it) {
-            ok = ok && warp_sleep(&red_full, uint32_t(it) & 1u, err, &abort_flag);
+            ok = warp_sleep(&red_full, uint32_t(it) & 1u, err, &abort_flag);
             if (last.live) ok = ok && warp_sleep(&b_full, uint32_t(lives++) & 1u, err, &abort_flag);
-            if (have && ok) {
+            if (ok) {
                 const int n = last.n, half = t & 1;
                 const bool whole = last.grp < 0;
                 T* put = static_cast<T*>(c.v) + (last.sh * c.W + n) * V;
@@ -842,11 +846,11 @@ __global__ void __launch_bounds__(kStreamThreads, 1)
                     }
                 }
             }
-            warp_arrive(&red_empty);
-            if (last.live) warp_arrive(&b_empty);
+            if (ok) warp_arrive(&red_empty);
+            if (ok && last.live) warp_arrive(&b_empty);
         };
         for (int it = 0; it < items; ++it) {
-            ok = ok && warp_sleep(&a_full, uint32_t(it) & 1u, err, &abort_flag);
+            ok = ok && warp_sleep(&a_full, uint32_t(it) & 1u, err, &abort_flag, pl.wait_limit);
             if (it >= 2) ok = ok && warp_sleep(w_empty + wt.s, wt.par ^ 1u, err, &abort_flag);
             Item x{0, 0, 0, -1, 0};
             if (ok) x = a_info;
@@ -904,7 +908,7 @@ __global__ void __launch_bounds__(kStreamThreads, 1)
                     }
                 }
             }
-            tc::named_sync(2, kWinThreads);
+            if (!tc::named_all(2, kWinThreads, ok)) return;
             if (x.live && x.grp < 0) {
                 for (int j = w; j <= n; j += kWinWarps) {
                     float s = 0.f;
@@ -922,10 +926,9 @@ __global__ void __launch_bounds__(kStreamThreads, 1)
             warp_arrive(&a_empty);
             if (it > 0) finish(reinterpret_cast<const float*>(dyn + pl.off_p + (wt.s ^ 1) * pl.win_bytes), it - 1);
             last = x;
-            have = ok;
             wt.next(2);
         }
-        tc::named_sync(2, kWinThreads);
+        if (!tc::named_all(2, kWinThreads, ok)) return;
         if (items > 0) finish(reinterpret_cast<const float*>(dyn + pl.off_p + (wt.s ^ 1) * pl.win_bytes), items - 1);
         return;
     }
@@ -937,12 +940,11 @@ __global__ void __launch_bounds__(kStreamThreads, 1)
     int lives = 0;
     // the sums of the head before have been taken (waited for by padding rows too: no part gets two heads ahead)
     const auto last_written = [&](int it) {
-        if (it > 0) ok = ok && warp_wait(&red_empty, uint32_t(it - 1) & 1u, err, &abort_flag);
+        return it == 0 || warp_wait(&red_empty, uint32_t(it - 1) & 1u, err, &abort_flag);
     };
     for (int it = 0; it < items; ++it) {
-        ok = ok && warp_wait(w_full + wt.s, wt.par, err, &abort_flag);
-        Item x{0, 0, 0, -1, 0};
-        if (ok) x = w_info[wt.s];
+        if (!warp_wait(w_full + wt.s, wt.par, err, &abort_flag)) return;
+        const Item x = w_info[wt.s];
         const char* win = dyn + pl.off_kt + wt.s * pl.win_bytes;
         const float* kt = reinterpret_cast<const float*>(win);
         const float* dec = reinterpret_cast<const float*>(win + (pl.off_dec - pl.off_kt));
@@ -953,10 +955,10 @@ __global__ void __launch_bounds__(kStreamThreads, 1)
             for (int e = 0; e < 8; ++e) acc[e] = make_float2(0.f, 0.f);
             const float* w = wq + ugrp * K + slice;
             for (int ch = 0; ch < chunks; ++ch, w += pl.chunk_rows) {
-                ok = ok && warp_wait(ring_full + rt.s, rt.par, err, &abort_flag);
+                if (!warp_wait(ring_full + rt.s, rt.par, err, &abort_flag)) return;
                 const int rn = K - ch * pl.chunk_rows;  // rows from the chunk's first
                 const char* src = dyn + pl.off_ring + rt.s * pl.chunk_bytes + ucol;
-                if (reads && ok) {
+                if (reads) {
                     // rows behind the state's last one are read as the chunk's first with weight 0
                     uint4 z[kPasses];
                     float u[kPasses];
@@ -972,8 +974,8 @@ __global__ void __launch_bounds__(kStreamThreads, 1)
                 warp_arrive(ring_empty + rt.s);
                 rt.next(pl.ring);
             }
-            last_written(it);
-            if (reads && ok) {
+            if (!last_written(it)) return;
+            if (reads) {
                 // the e-th four columns of all lanes stand together: neighbouring lanes write neighbouring words
                 float* d = red + slice * V + ucol / 4;
 #pragma unroll
@@ -983,13 +985,13 @@ __global__ void __launch_bounds__(kStreamThreads, 1)
             }
         } else if (x.live) {
             // one group of a head whose window is full
-            ok = ok && warp_wait(&b_full, uint32_t(lives) & 1u, err, &abort_flag);
+            if (!warp_wait(&b_full, uint32_t(lives) & 1u, err, &abort_flag)) return;
             const int n = x.n, used = n + 1;
             uint8_t* codes = c.codes + x.sh * K * V;
             float* scale = c.scale + x.sh * K * NG + x.grp;
             const Cols<true> cols(x.grp, V);
             float acc[4] = {0.f, 0.f, 0.f, 0.f};
-            for (int r = warp * kFoldRows; r < K && ok; r += kReadWarps * kFoldRows) {
+            for (int r = warp * kFoldRows; r < K; r += kReadWarps * kFoldRows) {
                 uint32_t z[kFoldRows];
                 float y[kFoldRows][4];
 #pragma unroll
@@ -1006,9 +1008,9 @@ __global__ void __launch_bounds__(kStreamThreads, 1)
                 }
                 put_rows<INT8, kFoldRows>(cols, y, kFoldRows, codes + int64_t(r) * V, V, scale + int64_t(r) * NG, NG);
             }
-            last_written(it);
-            if (ok) *reinterpret_cast<float4*>(red + warp * kG + 4 * lane) = make_float4(acc[0], acc[1], acc[2], acc[3]);
-        } else last_written(it);
+            if (!last_written(it)) return;
+            *reinterpret_cast<float4*>(red + warp * kG + 4 * lane) = make_float4(acc[0], acc[1], acc[2], acc[3]);
+        } else if (!last_written(it)) return;
         lives += x.live;
         warp_arrive(&red_full);
         warp_arrive(w_empty + wt.s);
@@ -1117,6 +1119,7 @@ StreamPlan stream_plan(const CacheProblem& p) {
     if (ring < 3) return pl;
     pl.ring = int(ring < kMaxRing ? ring : kMaxRing);
     pl.smem = size_t(at) + size_t(pl.ring) * pl.chunk_bytes;
+    pl.wait_limit = wait_limit();
     return pl;
 }
 

@@ -69,7 +69,7 @@ gla_status launch_end(const char* name, cudaStream_t s);
 int* device_error_word();
 enum : int { kErrBadGate = 2, kErrNonFinite = 4, kErrGuard = 8, kErrBadRow = 16 };
 
-// Cycles after which the bounded waits of the scan's kernels give up
+// Cycles after which the bounded waits of the scan's and the cache's kernels give up
 // (gla_selftest_wait_limit).
 long long wait_limit();
 

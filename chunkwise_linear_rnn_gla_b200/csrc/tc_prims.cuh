@@ -131,6 +131,20 @@ __device__ __forceinline__ void named_sync(uint32_t id, uint32_t nthreads) {
     asm volatile("bar.sync %0, %1;" ::"r"(id), "r"(nthreads) : "memory");
 }
 
+// The same, and whether `ok` holds for all of them.
+__device__ __forceinline__ bool named_all(uint32_t id, uint32_t nthreads, bool ok) {
+    uint32_t all;
+    asm volatile(
+        "{\n\t.reg .pred p, q;\n\t"
+        "setp.ne.u32 p, %3, 0;\n\t"
+        "bar.red.and.pred q, %1, %2, p;\n\t"
+        "selp.u32 %0, 1, 0, q;\n\t}"
+        : "=r"(all)
+        : "r"(id), "r"(nthreads), "r"(uint32_t(ok))
+        : "memory");
+    return all != 0;
+}
+
 // nanoseconds of the global timer
 __device__ __forceinline__ uint64_t global_ns() {
     uint64_t t;

@@ -486,12 +486,12 @@ size_t gla_bwd_workspace_bytes(const gla_desc* d);
  * GLA_ERR_CUDA if the launch fails. */
 gla_status gla_selftest_wait_timeout(long long limit_cycles, void* stream);
 
-/* Self-test of the same path inside the scan's kernels: the limit in SM cycles
- * of their waits for one another's maps, for calls from now on (the whole
- * process; 0: the built-in one, about a second). A negative limit has run out
- * before a wait begins, so that a call with more than one block a sequence
- * writes nothing behind its first wait, ends as usual and is reported as
- * GLA_ERR_TIMEOUT. */
+/* Self-test of the same path inside the scan's and the state cache's kernels: the
+ * limit in SM cycles of the waits between their blocks or warps, for calls from
+ * now on (the whole process; 0: the built-in one, about a second). A negative
+ * limit has run out before a wait begins, so that a scan with more than one block
+ * a sequence, or a cached step of large heads, writes nothing behind its first
+ * wait, ends as usual and is reported as GLA_ERR_TIMEOUT. */
 void gla_selftest_wait_limit(long long limit_cycles);
 
 /* Static description of a status code (never NULL). */

@@ -8,7 +8,7 @@ import torch
 import chunkwise_linear_rnn_gla_b200 as gla
 from chunkwise_linear_rnn_gla_b200 import _lib, build as gbuild, cache as gc, scan
 from tests import test_scan as ts
-from tests.test_state_cache import fill_pool, pool_case, token
+from tests.test_state_cache import check_step, fill_pool, many_rows, pool_case, token
 
 
 @pytest.fixture(scope="module")
@@ -232,3 +232,23 @@ def test_scan_writes_nothing_after_a_wait_that_ran_out(lib, no_patience, dtype, 
 def test_scan_of_one_block_waits_for_nobody(lib, no_patience):
     ts.check(ts.make(2, 1, 30, 64, torch.float32, "channel"), None, "leak", "channel")
     assert gla.gla_check_device_error() == _lib.GLA_OK
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("folds", ["some", "all"])
+def test_cached_step_writes_nothing_after_a_wait_that_ran_out(lib, no_patience, folds):
+    """Large heads for every SM: the parts of a block wait for one another. The call ends, reports the timeout, leaves
+    its output and the pool as they were, and the next call is right."""
+    c, _, g = fill_pool(42, 4, 256, 512, 16, "int8", torch.bfloat16)
+    before = {n: getattr(c, n).clone() for n in ("codes", "scale", "k", "v", "log_a")}
+    sl, ln = many_rows(40, 42, 16, g, folds)
+    slots, lengths = pool_case(c, sl, ln)
+    t = {n: x.cuda() for n, x in token(c, 40, g).items()}
+    o = torch.full_like(t["v"], 7)
+    gc.cache_step(c, t["q"], t["k"], t["v"], t["log_a"], slots, lengths, o=o)
+    assert timed_out()
+    assert bool((o == 7).all())
+    for n, x in before.items():
+        assert torch.equal(getattr(c, n), x), n
+    no_patience()
+    check_step(c, sl, ln, "channel", g)
