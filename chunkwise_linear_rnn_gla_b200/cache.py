@@ -42,19 +42,30 @@ class StateCache:
         if not isinstance(k, torch.Tensor) or k.dim() != 4:
             raise ValueError("k must be a [slots, H, window, Dk] tensor")
         self.window = k.shape[2]
-        dev = codes.device
         _dt(k)
-        _need(codes, "codes", codes.shape, codes.dtype, dev)
-        _need(scale, "scale", (self.slots, self.H, self.Dk, -(-self.Dv // _lib.CACHE_GROUP)), torch.float32, dev)
-        _need(k, "k", (self.slots, self.H, self.window, self.Dk), k.dtype, dev)
-        _need(v, "v", (self.slots, self.H, self.window, self.Dv), k.dtype, dev)
-        _need(log_a, "log_a", k.shape, torch.float32, dev)
-        self._tensors = (codes, scale, k, v, log_a)  # fixed: the pool's addresses are handed to every call
-        self.format, self.dtype, self.device = _FORMATS[codes.dtype], k.dtype, dev
+        self._tensors = (codes, scale, k, v, log_a)
+        self._ptrs = tuple(t.data_ptr for t in self._tensors)
+        self.format, self.dtype, self.device = _FORMATS[codes.dtype], k.dtype, codes.device
         self._descs = {}
-        self._c = _lib.GlaCache(codes.data_ptr(), scale.data_ptr(), k.data_ptr(), v.data_ptr(), log_a.data_ptr(),
-                                self.slots, self.window, _lib.CACHE_FORMAT[self.format])
-        self._ref = ctypes.byref(self._c)
+        self._at = self._ref = None
+        self._pool()
+
+    def _pool(self):
+        """The pool as an argument of the library. Its tensors' storage may have been exchanged since the last call
+        (`t.data = ...`): the addresses are those of now, and new ones are looked over like the first."""
+        codes, scale, k, v, log_a = self._ptrs
+        at = (codes(), scale(), k(), v(), log_a())
+        if at != self._at:
+            codes, scale, k, v, log_a = self._tensors
+            P, H, K, V, W, dev = self.slots, self.H, self.Dk, self.Dv, self.window, self.device
+            _need(codes, "codes", (P, H, K, V), _CODES[self.format], dev)
+            _need(scale, "scale", (P, H, K, -(-V // _lib.CACHE_GROUP)), torch.float32, dev)
+            _need(k, "k", (P, H, W, K), self.dtype, dev)
+            _need(v, "v", (P, H, W, V), self.dtype, dev)
+            _need(log_a, "log_a", (P, H, W, K), torch.float32, dev)
+            self._ref = ctypes.byref(_lib.GlaCache(*at, P, W, _lib.CACHE_FORMAT[self.format]))
+            self._at = at
+        return self._ref
 
     @property
     def codes(self):
@@ -100,47 +111,50 @@ class StateCache:
 
 
 def _rows(cache, slots, lengths=None):
+    """(rows, the pool as an argument) of a call."""
     if not isinstance(cache, StateCache):
         raise TypeError("cache must be a StateCache")
     if not isinstance(slots, torch.Tensor) or slots.dim() != 1:
         raise ValueError("slots must be an int32 [B] tensor")
+    pool = cache._pool()
     _same(slots, "slots", slots.shape, torch.int32, cache.device)
     if lengths is not None:
         _same(lengths, "lengths", slots.shape, torch.int32, cache.device)
-    return slots.shape[0]
+    return slots.shape[0], pool
 
 
-def _finish(dev, checks, what):
-    if checks:
-        with torch.cuda.device(dev):
-            _finish_checks([], what)
+def _finish(dev, what):
+    with torch.cuda.device(dev):
+        _finish_checks([], what)
 
 
 def cache_store(cache, S, slots, *, checks=False):
     """Quantise the states S [B,H,Dk,Dv] (fp32) into their slots (int32 [B], device). Their lengths are 0 then."""
     lib = load()
-    B = _rows(cache, slots)
+    B, pool = _rows(cache, slots)
     dev = cache.device
     _same(S, "S", (B, cache.H, cache.Dk, cache.Dv), torch.float32, dev)
     desc = cache._desc(B, checks=checks)
-    _enqueue(dev, "gla_cache_store", lib.gla_cache_store, desc, cache._ref, S.data_ptr(), slots.data_ptr())
-    _finish(dev, checks, "gla_cache_store")
+    _enqueue(dev, "gla_cache_store", lib.gla_cache_store, desc, pool, S.data_ptr(), slots.data_ptr())
+    if checks:
+        _finish(dev, "gla_cache_store")
 
 
 def cache_load(cache, slots, lengths=None, S=None, *, checks=False):
     """The states of the slots, S [B,H,Dk,Dv] fp32, with the tokens in their windows applied (lengths None: as
     stored)."""
     lib = load()
-    B = _rows(cache, slots, lengths)
+    B, pool = _rows(cache, slots, lengths)
     dev = cache.device
     if S is None:
         S = torch.empty(B, cache.H, cache.Dk, cache.Dv, dtype=torch.float32, device=dev)
     else:
         _same(S, "S", (B, cache.H, cache.Dk, cache.Dv), torch.float32, dev)
     desc = cache._desc(B, checks=checks)
-    _enqueue(dev, "gla_cache_load", lib.gla_cache_load, desc, cache._ref, slots.data_ptr(),
+    _enqueue(dev, "gla_cache_load", lib.gla_cache_load, desc, pool, slots.data_ptr(),
              None if lengths is None else lengths.data_ptr(), S.data_ptr())
-    _finish(dev, checks, "gla_cache_load")
+    if checks:
+        _finish(dev, "gla_cache_load")
     return S
 
 
@@ -148,7 +162,7 @@ def cache_step(cache, q, k, v, log_a, slots, lengths, o=None, *, gate="channel",
     """One decode step through the cache: q, k [B,H,Dk], v [B,H,Dv] (the cache's dtype), log_a as for gla_step
     (fp32; every gate kind). Returns o [B,H,Dv]. The caller adds 1 to `lengths` afterwards."""
     lib = load()
-    B = _rows(cache, slots, lengths)
+    B, pool = _rows(cache, slots, lengths)
     if lengths is None:
         raise TypeError("cache_step needs lengths")
     dev, dt, H, Dk, Dv = cache.device, cache.dtype, cache.H, cache.Dk, cache.Dv
@@ -161,7 +175,8 @@ def cache_step(cache, q, k, v, log_a, slots, lengths, o=None, *, gate="channel",
         o = torch.empty(B, H, Dv, dtype=dt, device=dev)
     else:
         _same(o, "o", (B, H, Dv), dt, dev)
-    _enqueue(dev, "gla_cache_step", lib.gla_cache_step, desc, cache._ref, q.data_ptr(), k.data_ptr(), v.data_ptr(),
+    _enqueue(dev, "gla_cache_step", lib.gla_cache_step, desc, pool, q.data_ptr(), k.data_ptr(), v.data_ptr(),
              log_a.data_ptr(), slots.data_ptr(), lengths.data_ptr(), o.data_ptr())
-    _finish(dev, checks, "gla_cache_step")
+    if checks:
+        _finish(dev, "gla_cache_step")
     return o

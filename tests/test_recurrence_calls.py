@@ -252,3 +252,48 @@ def test_cached_step_writes_nothing_after_a_wait_that_ran_out(lib, no_patience, 
         assert torch.equal(getattr(c, n), x), n
     no_patience()
     check_step(c, sl, ln, "channel", g)
+
+
+def exchange(c, names=("codes", "scale", "k", "v", "log_a")):
+    """New storage with the same values behind a pool's tensors; returns the old storage, which stays alive."""
+    old = {}
+    for n in names:
+        t = getattr(c, n)
+        old[n] = t.detach()
+        t.data = t.clone()
+    return old
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("names", [("codes", "scale", "k", "v", "log_a"), ("scale",), ("v",)])
+def test_pool_with_exchanged_storage(lib, names):
+    """A pool is where its tensors are at the time of the call."""
+    c, _, g = fill_pool(4, 2, 32, 160, 4, "int8", torch.bfloat16)
+    ref, S, _ = fill_pool(4, 2, 32, 160, 4, "int8", torch.bfloat16)
+    t = {n: x.cuda() for n, x in token(c, 3, g).items()}
+    slots, lengths = pool_case(c, [3, 1, 0], [3, 0, 2])
+    S = S[:3].contiguous().cuda()
+    for call in (lambda p: gc.cache_step(p, t["q"], t["k"], t["v"], t["log_a"], slots, lengths),
+                 lambda p: gc.cache_load(p, slots, lengths), lambda p: gc.cache_store(p, S, slots)):
+        old = exchange(c, names)
+        before = {n: x.clone() for n, x in old.items()}
+        got, want = call(c), call(ref)
+        assert got is None or torch.equal(got, want)
+        for n, x in old.items():
+            assert torch.equal(x, before[n]), n
+        for n in ("codes", "scale", "k", "v", "log_a"):
+            assert torch.equal(getattr(c, n), getattr(ref, n)), n
+
+
+def test_pool_with_storage_that_does_not_fit(lib):
+    c = gc.StateCache.empty(4, 1, 8, 16, device="cpu")
+    s = torch.zeros(2, dtype=torch.int32)
+    for n, other in (("scale", torch.zeros(3, 1, 8, 1)), ("k", torch.zeros(4, 1, 16, 4, dtype=torch.bfloat16)),
+                     ("log_a", torch.zeros(4, 1, 16, 16)[..., ::2])):
+        t = getattr(c, n)
+        was, t.data = t.data, other
+        with pytest.raises(ValueError, match=n):
+            gc.cache_load(c, s, s)
+        t.data = was
+    with pytest.raises(ValueError, match="CUDA"):
+        gc.cache_load(c, s, s)
