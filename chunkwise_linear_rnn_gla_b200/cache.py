@@ -104,6 +104,8 @@ class StateCache:
         key = (B, gate, tau, checks)
         d = self._descs.get(key)
         if d is None:
+            if len(self._descs) >= 256:  # a server that has met many batch sizes starts afresh
+                self._descs.clear()
             d = self._descs[key] = ctypes.byref(make_desc(
                 B, self.H, 1, self.Dk, self.Dv, "bf16" if self.dtype == torch.bfloat16 else "f32",
                 flags=_lib.FLAG_CHECKS if checks else 0, gate=gate, tau=tau))

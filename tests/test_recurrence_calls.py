@@ -297,3 +297,13 @@ def test_pool_with_storage_that_does_not_fit(lib):
         t.data = was
     with pytest.raises(ValueError, match="CUDA"):
         gc.cache_load(c, s, s)
+
+
+def test_a_pool_keeps_a_limited_number_of_descriptors(lib):
+    """Continuous batching calls with every number of rows, and the options are the caller's floats."""
+    c = gc.StateCache.empty(4, 1, 8, 16, device="cpu")
+    for i in range(1000):
+        s = torch.zeros(i + 1, dtype=torch.int32)
+        with pytest.raises(ValueError, match="CUDA"):
+            gc.cache_load(c, s, s, S=torch.empty(i + 1, 1, 8, 16))
+    assert all(len(x) <= 256 for x in vars(c).values() if isinstance(x, (dict, list, tuple)))
