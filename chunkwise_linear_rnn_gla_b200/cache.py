@@ -19,7 +19,7 @@ import ctypes
 
 import torch
 
-from . import _dt, _enqueue, _finish_checks, _lib, _need, _same, gate_shape, make_desc
+from . import _dt, _enqueue, _finish_checks, _guarded, _lib, _need, _same, gate_shape, make_desc
 from ._lib import load
 
 __all__ = ["StateCache", "cache_store", "cache_load", "cache_step"]
@@ -125,9 +125,9 @@ def _rows(cache, slots, lengths=None):
     return slots.shape[0], pool
 
 
-def _finish(dev, what):
+def _finish(dev, guards, what):
     with torch.cuda.device(dev):
-        _finish_checks([], what)
+        _finish_checks(guards, what)
 
 
 def cache_store(cache, S, slots, *, checks=False):
@@ -139,7 +139,7 @@ def cache_store(cache, S, slots, *, checks=False):
     desc = cache._desc(B, checks=checks)
     _enqueue(dev, "gla_cache_store", lib.gla_cache_store, desc, pool, S.data_ptr(), slots.data_ptr())
     if checks:
-        _finish(dev, "gla_cache_store")
+        _finish(dev, [], "gla_cache_store")
 
 
 def cache_load(cache, slots, lengths=None, S=None, *, checks=False):
@@ -148,15 +148,17 @@ def cache_load(cache, slots, lengths=None, S=None, *, checks=False):
     lib = load()
     B, pool = _rows(cache, slots, lengths)
     dev = cache.device
+    guards = [] if checks else None
     if S is None:
-        S = torch.empty(B, cache.H, cache.Dk, cache.Dv, dtype=torch.float32, device=dev)
+        S = (torch.empty(B, cache.H, cache.Dk, cache.Dv, dtype=torch.float32, device=dev) if guards is None else
+             _guarded((B, cache.H, cache.Dk, cache.Dv), torch.float32, dev, guards))
     else:
         _same(S, "S", (B, cache.H, cache.Dk, cache.Dv), torch.float32, dev)
     desc = cache._desc(B, checks=checks)
     _enqueue(dev, "gla_cache_load", lib.gla_cache_load, desc, pool, slots.data_ptr(),
              None if lengths is None else lengths.data_ptr(), S.data_ptr())
     if checks:
-        _finish(dev, "gla_cache_load")
+        _finish(dev, guards, "gla_cache_load")
     return S
 
 
@@ -173,12 +175,13 @@ def cache_step(cache, q, k, v, log_a, slots, lengths, o=None, *, gate="channel",
     _same(v, "v", (B, H, Dv), dt, dev)
     desc = cache._desc(B, gate, tau, checks)
     _same(log_a, "log_a", gate_shape(gate, B, H, None, Dk), torch.float32, dev)
+    guards = [] if checks else None
     if o is None:
-        o = torch.empty(B, H, Dv, dtype=dt, device=dev)
+        o = torch.empty(B, H, Dv, dtype=dt, device=dev) if guards is None else _guarded((B, H, Dv), dt, dev, guards)
     else:
         _same(o, "o", (B, H, Dv), dt, dev)
     _enqueue(dev, "gla_cache_step", lib.gla_cache_step, desc, pool, q.data_ptr(), k.data_ptr(), v.data_ptr(),
              log_a.data_ptr(), slots.data_ptr(), lengths.data_ptr(), o.data_ptr())
     if checks:
-        _finish(dev, "gla_cache_step")
+        _finish(dev, guards, "gla_cache_step")
     return o

@@ -22,7 +22,7 @@ from typing import Optional
 
 import torch
 
-from . import _dt, _enqueue, _finish_checks, _lib, _same, _workspace, make_desc
+from . import _dt, _enqueue, _finish_checks, _guarded, _lib, _same, _workspace, make_desc
 from ._lib import load
 
 __all__ = ["scan_fwd", "scan_bwd", "scan_step", "scan_workspace_size", "scan_workspace"]
@@ -74,10 +74,9 @@ def _flags(checks, ws_from_fwd=False):
     return (_lib.FLAG_WS_FROM_FWD if ws_from_fwd else 0) | (_lib.FLAG_CHECKS if checks else 0)
 
 
-def _finish(dev, checks, what):
-    if checks:
-        with torch.cuda.device(dev):
-            _finish_checks([], what)
+def _finish(dev, guards, what):
+    with torch.cuda.device(dev):
+        _finish_checks(guards, what)
 
 
 def scan_workspace_size(desc, packed: bool = False) -> int:
@@ -92,9 +91,13 @@ def scan_workspace(x, cu_seqlens=None, checks=False) -> torch.Tensor:
     return torch.empty(n, dtype=torch.uint8, device=x.device)
 
 
-def _buffer(t, like, name, packed):
+def _buffer(t, like, name, packed, guards):
+    """An output: the caller's, or a new one, in checking mode (guards) between canaries."""
     if t is None:
-        return torch.zeros_like(like) if packed else torch.empty_like(like)
+        if guards is None:
+            return torch.zeros_like(like) if packed else torch.empty_like(like)
+        t = _guarded(like.shape, like.dtype, like.device, guards)
+        return t.zero_() if packed else t
     _same(t, name, like.shape, like.dtype, like.device)
     return t
 
@@ -103,8 +106,8 @@ def scan_fwd(x, log_a, h0=None, *, cu_seqlens=None, write="input", gate="channel
              want_hT=True, workspace: Optional[torch.Tensor] = None, checks=False):
     """Forward. Returns (h, hT); hT is None when want_hT is False and no hT buffer is given. A `workspace`
     (scan_workspace) keeps what scan_bwd(ws_from_fwd=True) reuses. checks=True: the library's checking mode
-    (gate domain, finite outputs; of packed rows those that belong to a sequence), synchronous, raises GlaError on
-    a failure."""
+    (gate domain, finite outputs; of packed rows those that belong to a sequence) with canaries around the outputs
+    allocated here, synchronous, raises GlaError on a failure."""
     lib = load()
     B, H, L, D = _sizes(x, cu_seqlens)
     dev = x.device
@@ -112,17 +115,20 @@ def scan_fwd(x, log_a, h0=None, *, cu_seqlens=None, write="input", gate="channel
     if h0 is not None:
         _same(h0, "h0", (B, H, D), torch.float32, dev)
     desc = _desc(x, B, H, L, D, gate, tau, _flags(checks))
-    h = _buffer(h, x, "h", cu_seqlens is not None)
+    guards = [] if checks else None
+    h = _buffer(h, x, "h", cu_seqlens is not None, guards)
     if hT is not None:
         _same(hT, "hT", (B, H, D), torch.float32, dev)
     elif want_hT:
-        hT = torch.empty(B, H, D, dtype=torch.float32, device=dev)
+        hT = (torch.empty(B, H, D, dtype=torch.float32, device=dev) if guards is None else
+              _guarded((B, H, D), torch.float32, dev, guards))
     ws, nbytes = None, 0
     if workspace is not None:
         ws, nbytes = _workspace(lib.gla_scan_workspace_size(desc, cu_seqlens is not None), dev, workspace)
     _enqueue(dev, "gla_scan_fwd", lib.gla_scan_fwd, desc, _write(write), x.data_ptr(), log_a.data_ptr(),
              _addr(cu_seqlens), _addr(h0), h.data_ptr(), _addr(hT), _addr(ws), nbytes)
-    _finish(dev, checks, "gla_scan_fwd")
+    if checks:
+        _finish(dev, guards, "gla_scan_fwd")
     return h, hT
 
 
@@ -144,19 +150,21 @@ def scan_bwd(x, log_a, dh, h0=None, dhT=None, *, cu_seqlens=None, write="input",
     if ws_from_fwd and workspace is None:
         raise ValueError("ws_from_fwd needs the forward's workspace")
     desc = _desc(x, B, H, L, D, gate, tau, _flags(checks, ws_from_fwd))
-    out = dict(out or {})
-    dx = _buffer(out.get("dx"), x, "dx", packed)
-    dla = _buffer(out.get("dlog_a"), log_a, "dlog_a", packed)
+    out, guards = dict(out or {}), [] if checks else None
+    dx = _buffer(out.get("dx"), x, "dx", packed, guards)
+    dla = _buffer(out.get("dlog_a"), log_a, "dlog_a", packed, guards)
     dh0 = out.get("dh0")
     if dh0 is not None:
         _same(dh0, "dh0", (B, H, D), torch.float32, dev)
     elif want_dh0:
-        dh0 = torch.empty(B, H, D, dtype=torch.float32, device=dev)
+        dh0 = (torch.empty(B, H, D, dtype=torch.float32, device=dev) if guards is None else
+               _guarded((B, H, D), torch.float32, dev, guards))
     ws, nbytes = _workspace(lib.gla_scan_workspace_size(desc, packed), dev, workspace)
     _enqueue(dev, "gla_scan_bwd", lib.gla_scan_bwd, desc, _write(write), x.data_ptr(), log_a.data_ptr(),
              _addr(cu_seqlens), _addr(h0), dh.data_ptr(), _addr(dhT), dx.data_ptr(), dla.data_ptr(), _addr(dh0),
              _addr(ws), nbytes)
-    _finish(dev, checks, "gla_scan_bwd")
+    if checks:
+        _finish(dev, guards, "gla_scan_bwd")
     return {"dx": dx, "dlog_a": dla, "dh0": dh0}
 
 
@@ -180,12 +188,14 @@ def scan_step(x, log_a, state, slots=None, *, write="input", gate="channel", tau
         _index(slots, "slots", B, dev)
     elif state.shape[0] < B:
         raise ValueError("state has %d entries for %d rows" % (state.shape[0], B))
+    guards = [] if checks else None
     if h is None:
-        h = torch.empty_like(x)
+        h = torch.empty_like(x) if guards is None else _guarded(shape, x.dtype, dev, guards)
     else:
         _same(h, "h", shape, x.dtype, dev)
     desc = _desc(x, B, H, 1, D, gate, tau, _flags(checks))
     _enqueue(dev, "gla_scan_step", lib.gla_scan_step, desc, _write(write), x.data_ptr(), log_a.data_ptr(),
              _addr(slots), state.shape[0], state.data_ptr(), h.data_ptr())
-    _finish(dev, checks, "gla_scan_step")
+    if checks:
+        _finish(dev, guards, "gla_scan_step")
     return h

@@ -1,5 +1,6 @@
 """Calls of the scan and of the state cache that their documentation allows: from two host threads at once, with a
 pool whose storage was exchanged, and in checking mode with rows that take no part."""
+import contextlib
 import threading
 
 import pytest
@@ -307,3 +308,43 @@ def test_a_pool_keeps_a_limited_number_of_descriptors(lib):
         with pytest.raises(ValueError, match="CUDA"):
             gc.cache_load(c, s, s, S=torch.empty(i + 1, 1, 8, 16))
     assert all(len(x) <= 256 for x in vars(c).values() if isinstance(x, (dict, list, tuple)))
+
+
+@pytest.mark.parametrize("wrong", [None, 0, 1, 2])
+def test_checks_look_at_the_margins_of_outputs(lib, monkeypatch, wrong):
+    """Every output that a binding allocates in checking mode lies between canaries (as gla_fwd's do). The library's call
+    is left out here; in its place the margin behind one of the outputs is overwritten."""
+    bufs = []
+
+    def fake(*a):
+        if wrong is not None:
+            bufs[min(wrong, len(bufs) - 1)][-1] = 0
+
+    for m in (scan, gc):
+        guarded = m._guarded
+
+        def record(shape, dtype, dev, guards, guarded=guarded):
+            t = guarded(shape, dtype, dev, guards)
+            bufs.append(guards[-1][0])
+            return t
+
+        monkeypatch.setattr(m, "_guarded", record)
+        monkeypatch.setattr(m, "_enqueue", fake)
+    monkeypatch.setattr(torch.cuda, "device", lambda dev: contextlib.nullcontext())
+    monkeypatch.setattr(gla, "gla_check_device_error", lambda: _lib.GLA_OK)
+    x, z, s = torch.zeros(1, 1, 8, 4), torch.zeros(1, 1, 8, 4), torch.zeros(1, dtype=torch.int32)
+    c = gc.StateCache.empty(4, 1, 8, 16, device="cpu", dtype=torch.float32)
+    q, v = torch.zeros(1, 1, 8), torch.zeros(1, 1, 16)
+    cu = torch.tensor([0, 8], dtype=torch.int32)
+    for outputs, call in ((2, lambda: scan.scan_fwd(x, z, checks=True)), (2, lambda: scan.scan_fwd(x, z, cu_seqlens=cu, checks=True)),
+                          (3, lambda: scan.scan_bwd(x, z, x, checks=True)),
+                          (1, lambda: scan.scan_step(x[:, :, 0].contiguous(), z[:, :, 0].contiguous(), torch.zeros(1, 1, 4), checks=True)),
+                          (1, lambda: gc.cache_load(c, s, s, checks=True)),
+                          (1, lambda: gc.cache_step(c, q, q, v, q, s, s, checks=True))):
+        bufs.clear()
+        if wrong is None:
+            call()
+        else:
+            with pytest.raises(gla.GlaError, match="canary"):
+                call()
+        assert len(bufs) == outputs
