@@ -60,12 +60,6 @@ __device__ __forceinline__ void decode4(uint32_t x, float2* y) {
         y[1] = __half22float2(__half2(__nv_cvt_fp8x2_to_halfraw2(__nv_fp8x2_storage_t(x >> 16), __NV_E4M3)));
     }
 }
-template <bool INT8>
-__device__ __forceinline__ void decode4(uint32_t x, float* y) {
-    float2 t[2];
-    decode4<INT8>(x, t);
-    y[0] = t[0].x, y[1] = t[0].y, y[2] = t[1].x, y[3] = t[1].y;
-}
 // scale of a group from the bits of its largest magnitude (NaN and inf order above every finite value)
 template <bool INT8>
 __device__ __forceinline__ float scale_of(uint32_t amax_bits) {
@@ -591,7 +585,10 @@ struct Turn {
 };
 
 // This block's items: of the folding groups (all of them first, then the other heads, in the order of `rows`) those
-// whose cost begins in the block's share. The host keeps the total below 2^27.
+// whose cost begins in the block's share. A launch has at most kMaxItems groups of heads, all of which may fold, and
+// the last share ends less than a unit per block behind the total.
+constexpr int kMaxItems = 1 << 24;
+static_assert(int64_t(kMaxItems) * kFoldCost + 2 * kSms < INT32_MAX, "Share counts in 32 bits");
 struct Share {
     int f0, f1, h0, h1;
     __device__ __forceinline__ Share(int folds, int B, int H, int NG) {
@@ -1129,7 +1126,7 @@ gla_status stream_typed(const CacheProblem& p, const StreamPlan& pl, const void*
     const Pool c = pool_of(p);
     const GateArgs ga{la, p.gate, p.inv_tau, p.H};
     if (!allow_smem(k_cache_stream<T, INT8>, pl.smem, kStreamSmem)) return GLA_ERR_CUDA;
-    const int64_t fit = (int64_t(1) << 24) / (p.H * c.NG), step = fit < kMaxRows ? fit : kMaxRows;  // rows a launch
+    const int64_t fit = kMaxItems / (p.H * c.NG), step = fit < kMaxRows ? fit : kMaxRows;  // rows a launch
     for (int64_t b0 = 0; b0 < p.B; b0 += step) {
         const int n = int(p.B - b0 < step ? p.B - b0 : step);
         GLA_LAUNCH("cache_step", (k_cache_stream<T, INT8>), unsigned(kSms), kStreamThreads, pl.smem, s, c, pl, n, b0,
