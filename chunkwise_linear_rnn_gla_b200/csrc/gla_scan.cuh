@@ -14,10 +14,11 @@
 // no flags in memory and no second launch, and its result does not depend on timing.
 //
 // Floor: 8 (bf16) or 12 (fp32) bytes an element forward, 14 or 20 backward, at the copy bandwidth. Measured (device time,
-// inputs larger than L2 in turn): forward 33.4 us at 8 sequences of 2048 steps, width 1024 (134 MB, 4.0 TB/s, floor
-// 20.5); forward and backward 101 us at 4 x 2048, width 2048, gate from its pre-activation (369 MB moved, floor 57).
-// What is left over the floor is issue slots (37 instructions an element forward, 70 backward, 60% of the slots taken)
-// and the chain of a round: gates, maps, the exchange, steps. Without its loads the forward still takes 32 us.
+// inputs larger than L2 in turn): forward 33.7 us at 8 sequences of 2048 steps, width 1024 (134 MB, 4.0 TB/s, floor
+// 20.5); forward and backward 101 us at 4 x 2048, width 2048, gate from its pre-activation (floor 41 if the inputs were
+// read once; 369 MB moved, 57 us, since the backward reads them again). What is left is the chain of a round: gates,
+// maps, the exchange, steps, each waiting for the one before. No resource is full: 43% of the issue slots are taken
+// forward and 51% backward, DRAM 37%. Without its loads the forward still takes 32 us.
 //
 // A boundary between packed sequences is a step whose map forgets: (forget, a h0 + b). In the backward the same
 // steps stop the gradient, which walks the maps the other way: with y_t = a_t g_t, g_t = dh_t + y_{t+1}.
@@ -52,8 +53,8 @@ __device__ __forceinline__ void cluster_arrive() { asm volatile("barrier.cluster
 __device__ __forceinline__ void cluster_wait() { asm volatile("barrier.cluster.wait.acquire;" ::: "memory"); }
 
 // ---- one or two adjacent channels -------------------------------------------------------
-// Two channels are one packed operand: the packed fp32 instructions do both for one issue slot, and issue slots are
-// what these kernels run out of first (a wide batch spends about as long issuing as it does on memory).
+// Two channels are one packed operand: the packed fp32 instructions do both for one issue slot, so a round's chain has
+// fewer of them (35 a channel and step forward, 69 backward).
 template <int VEC>
 struct VecOf {
     using type = float;

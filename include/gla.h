@@ -401,7 +401,9 @@ gla_status gla_scan_step(const gla_desc* d, int32_t write, const void* x, const 
  * not finite can be held); L is ignored, the other fields as for the scan. window is
  * 1 .. 64; GLA_ERR_UNSUPPORTED when a head's window does not fit on chip
  * (4 * window * (Dk + 128) + 16 Dk + 8192 bytes above 200 KB), and beyond B = 2^22,
- * H = 65535 or B H ceil(Dv / 128) ceil(Dk / 64) = 2^30. */
+ * H = 65535 or B H ceil(Dv / 128) ceil(Dk / 64) = 2^30. A row's slot is looked
+ * for among those of all rows in front of it, so the rows cost their square beside
+ * what their states cost (nothing to speak of at thousands of rows). */
 typedef enum gla_cache_format {
     GLA_CACHE_INT8 = 0,
     GLA_CACHE_E4M3 = 1
