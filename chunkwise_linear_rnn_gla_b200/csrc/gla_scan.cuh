@@ -248,12 +248,13 @@ struct Exchange {
         const int par = it & 1;
         for (int q = 0; q < cl; ++q) send(maps + (par * cl + rank) * 32 + (threadIdx.x & 31), bar + par, uint32_t(q), m);
     }
-    // every thread waits for the maps of round `it`; `ok` becomes false where the wait ran out
+    // Every thread waits for the maps of round `it`; `ok` becomes false where the wait ran out. (Thread 0 has a channel, so
+    // its `ok` is true until then. Afterwards a wait for the other parity may seem to succeed: it arms nothing more.)
     __device__ __forceinline__ const Map<V>* get(int it, bool& ok) const {
         const int par = it & 1;
         const bool got = tc::mbar_wait(bar + par, uint32_t(it >> 1) & 1u, err, abort, limit);
         ok = ok && got;
-        if (got && threadIdx.x == 0 && it + 2 < rounds) tc::mbar_arrive_expect_tx(bar + par, bytes());
+        if (ok && threadIdx.x == 0 && it + 2 < rounds) tc::mbar_arrive_expect_tx(bar + par, bytes());
         return maps + par * cl * 32 + (threadIdx.x & 31);
     }
     // no block leaves while another may still send to it
